@@ -168,7 +168,9 @@ def _quant(v):
     M, K = v.shape
     nb = _blocks(K)
     wide = torch.nn.functional.pad(v, (0, nb * BLOCK - K)).view(M, nb, BLOCK)
-    scale = wide.abs().amax(2).clamp(min=TINY) / E4M3_MAX
+    scale = wide.abs().amax(2).clamp(min=TINY)
+    # by a tensor: division by a plain number multiplies by its rounded reciprocal
+    scale = scale / torch.full_like(scale, E4M3_MAX)
     codes = (wide / scale[..., None]).view(M, nb * BLOCK)[:, :K].contiguous()
     return codes.to(torch.float8_e4m3fn), scale
 
