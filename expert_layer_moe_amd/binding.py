@@ -7,6 +7,7 @@ fallback: if the library is missing, loading raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -22,6 +23,8 @@ _STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED",
            -3: "MOE_ERR_WORKSPACE", -4: "MOE_ERR_HIP"}
 
 EXPORTS = ["moe_workspace_size", "moe_route", "moe_align", "moe_forward",
+           "moe_forward_few", "moe_few_workspace_size", "moe_gemm_fp8", "moe_quant_fp8",
+           "moe_silu_mul_quant_fp8",
            "moe_forward_noalloc", "moe_forward_signaled", "moe_block_signal_count", "moe_set_signal_wait_us", "moe_set_one_launch",
            "moe_pack_weights", "moe_set_path_thresholds", "moe_set_fp8_mfma", "moe_status_str", "moe_num_stages", "moe_stage_name",
            "moe_profile_enable", "moe_profile_read"]
@@ -39,6 +42,18 @@ class moe_desc(ctypes.Structure):
                 ("act_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
                 ("w13_scale", ctypes.c_void_p), ("w2_scale", ctypes.c_void_p),
                 ("block_m", ctypes.c_int32), ("w_layout", ctypes.c_int32)]
+
+
+class moe_gemm_desc(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("lda", ctypes.c_int64), ("ldb", ctypes.c_int64),
+                ("ld_as", ctypes.c_int64), ("ldo", ctypes.c_int64)]
+
+
+class moe_quant_desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("in_dtype", ctypes.c_int32), ("ld_in", ctypes.c_int64),
+                ("ld_codes", ctypes.c_int64), ("ld_scales", ctypes.c_int64)]
 
 
 _lib = None
@@ -73,6 +88,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_set_signal_wait_us.restype = ctypes.c_int
     lib.moe_set_one_launch.argtypes = [I32]
     lib.moe_set_one_launch.restype = ctypes.c_int
+    lib.moe_few_workspace_size.argtypes = [D, I32]
+    lib.moe_few_workspace_size.restype = SZ
+    lib.moe_forward_few.argtypes = [D, P, P, P, P, P, I32, P, P, SZ, P]
+    lib.moe_forward_few.restype = ctypes.c_int
+    lib.moe_gemm_fp8.argtypes = [ctypes.POINTER(moe_gemm_desc), P, P, P, P, P, P]
+    lib.moe_gemm_fp8.restype = ctypes.c_int
+    for name in ("moe_quant_fp8", "moe_silu_mul_quant_fp8"):
+        getattr(lib, name).argtypes = [ctypes.POINTER(moe_quant_desc), P, P, P, P]
+        getattr(lib, name).restype = ctypes.c_int
     lib.moe_pack_weights.argtypes = [D, P, P, P, P, P]
     lib.moe_pack_weights.restype = ctypes.c_int
     lib.moe_set_fp8_mfma.argtypes = [I32]
@@ -246,6 +270,141 @@ def moe_set_one_launch(enable: bool = False):
     """Calls where every segment streams: gate/up and down in one launch
     (True) or two (False, the default).  Process-wide."""
     _check(load_library().moe_set_one_launch(1 if enable else 0))
+
+
+# ---- few token rows, fp8 block-scale product, token quantisation -----------------
+FEW_MAX_ROWS = 16   # MOE_FEW_MAX_ROWS
+
+
+@contextlib.contextmanager
+def _on(stream, *tensors):
+    """Makes the tensors' GPU current for a call and yields the raw stream to
+    enqueue on: the given one, or that GPU's current stream.  All tensors (and
+    the stream) must be on one GPU."""
+    device = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors must be on the GPU")
+        if device is not None and t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}: one GPU expected")
+        device = t.device
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream on {stream.device}, tensors on {device}")
+    if device.index == torch.cuda.current_device():
+        yield _stream(stream)
+    else:
+        with torch.cuda.device(device):
+            yield _stream(stream)
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a result written on `stream` (its memory is reused in
+    that stream's order)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows(t: torch.Tensor, name: str, dtypes, cols=None, rows=None):
+    """A matrix whose rows are contiguous: (pointer, row stride)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols) or \
+            (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected "
+                         f"({'rows' if rows is None else rows}, {'cols' if cols is None else cols})")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    # the stride of a single row says nothing: dense
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else 0
+
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def moe_few_workspace_size(desc: moe_desc, topk: int) -> int:
+    return int(load_library().moe_few_workspace_size(ctypes.byref(desc), topk))
+
+
+def alloc_few_workspace(desc: moe_desc, topk: int, device="cuda") -> torch.Tensor:
+    n = moe_few_workspace_size(desc, topk)
+    if n == 0:
+        raise MoeError(-2, "not a layer of a few rows (bf16 activations, at most "
+                           f"{FEW_MAX_ROWS} rows)")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_forward_few(desc, x, valid_rows, router_w, w13, w2, topk, out, workspace,
+                    stream=None):
+    """moe_forward for at most FEW_MAX_ROWS token rows, in two launches."""
+    T, H, E, I, ns = desc.T, desc.H, desc.E, desc.I, desc.n_shared
+    with _on(stream, x, valid_rows, router_w, w13, w2, out, workspace) as s:
+        _check(load_library().moe_forward_few(
+            ctypes.byref(desc), _dev(x, "x", _act(desc), (T, H)),
+            _dev(valid_rows, "valid_rows", torch.uint8, (T,)),
+            _dev(router_w, "router_w", _act(desc), (E, H)),
+            _dev(w13, "w13", _w(desc), (E + ns, 2 * I, H)),
+            _dev(w2, "w2", _w(desc), (E + ns, H, I)), topk,
+            _dev(out, "out", _act(desc), (T, H)),
+            _dev(workspace, "workspace", torch.uint8), workspace.numel(), s))
+
+
+def moe_gemm_fp8(a, a_scale, b, b_scale, out=None, out_dtype=torch.bfloat16, stream=None):
+    """out [M, N] = (a * a_scale) (b * b_scale)^T of e4m3fn codes (uint8 or
+    float8_e4m3fn) a [M, K], b [N, K]; a_scale [M, ceil(K/128)], b_scale
+    [ceil(N/128), ceil(K/128)] fp32.  a, b, a_scale and out may have wider
+    rows (row strides); out is allocated here when not given."""
+    ap, lda = _rows(a, "a", _CODES)
+    M, K = a.shape
+    bp, ldb = _rows(b, "b", _CODES, cols=K)
+    N = b.shape[0]
+    nb = (K + 127) // 128
+    sp, ld_as = _rows(a_scale, "a_scale", (torch.float32,), cols=nb, rows=M)
+    if out is None:
+        out = _empty((M, N), out_dtype, a.device, stream)
+    op, ldo = _rows(out, "out", (torch.bfloat16, torch.float32), cols=N, rows=M)
+    with _on(stream, a, a_scale, b, b_scale, out) as s:
+        d = moe_gemm_desc(M, N, K, _DT[out.dtype], lda, ldb, ld_as, ldo)
+        _check(load_library().moe_gemm_fp8(
+            ctypes.byref(d), ap, sp, bp,
+            _dev(b_scale, "b_scale", torch.float32, ((N + 127) // 128, nb)), op, s))
+    return out
+
+
+def _quant(entry, x, cols, codes, scales, stream):
+    xp, ld_in = _rows(x, "x", (torch.float32, torch.bfloat16))
+    M = x.shape[0]
+    nb = (cols + 127) // 128
+    if codes is None:
+        codes = _empty((M, cols), torch.uint8, x.device, stream)
+    if scales is None:
+        scales = _empty((M, nb), torch.float32, x.device, stream)
+    cp, ld_codes = _rows(codes, "codes", _CODES, cols=cols, rows=M)
+    sp, ld_scales = _rows(scales, "scales", (torch.float32,), cols=nb, rows=M)
+    with _on(stream, x, codes, scales) as s:
+        d = moe_quant_desc(M, cols, _DT[x.dtype], ld_in, ld_codes, ld_scales)
+        _check(entry(ctypes.byref(d), xp, cp, sp, s))
+    return codes, scales
+
+
+def moe_quant_fp8(x, codes=None, scales=None, stream=None):
+    """Token rows x [M, K] (bf16 or fp32; rows may be strided) -> e4m3fn codes
+    [M, K] (uint8) and fp32 scales [M, ceil(K/128)], allocated here when not
+    given.  Returns (codes, scales)."""
+    return _quant(load_library().moe_quant_fp8, x, x.shape[-1], codes, scales, stream)
+
+
+def moe_silu_mul_quant_fp8(gu, codes=None, scales=None, stream=None):
+    """moe_quant_fp8 of SiLU(g) * u for gu [M, 2 I] (gate columns, then up)."""
+    if gu.shape[-1] % 2 != 0:
+        raise ValueError("gu holds gate and up columns: an even number")
+    return _quant(load_library().moe_silu_mul_quant_fp8, gu, gu.shape[-1] // 2, codes, scales,
+                  stream)
 
 
 SCRATCH_BYTES = 64 << 20   # MOE_SCRATCH_BYTES

@@ -224,6 +224,38 @@ int make_plan(const moe_desc* d, int32_t topk, Plan* p) {
   return MOE_OK;
 }
 
+// Workspace layout of one moe_forward_few call.
+struct FewPlan {
+  size_t off_part, off_hw, off_ticket, total;
+};
+
+static_assert(MOE_FEW_MAX_ROWS == moe::kFewRows, "row limit");
+
+int make_few_plan(const moe_desc* d, int32_t topk, FewPlan* p) {
+  const int st = check_desc(d, topk);
+  if (st != MOE_OK) return st;
+  if (d->T > MOE_FEW_MAX_ROWS || d->act_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { size_t r = o; o = round_up(o + bytes, kAlign); return r; };
+  p->off_part = take((size_t)moe::kFewLogitParts * d->T * d->E * 4);
+  p->off_hw = take((size_t)d->T * (topk + d->n_shared) * d->I * 4);
+  p->off_ticket = take(4);
+  p->total = o;
+  return MOE_OK;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// A row stride: 0 stands for the row length.  Below it: invalid; off its
+// multiple: not covered.
+int check_stride(int64_t ld, int64_t len, int multiple) {
+  if (ld != 0 && ld < len) return MOE_ERR_INVALID_ARG;
+  if ((ld != 0 ? ld : len) % multiple != 0) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int64_t or_dense(int64_t ld, int64_t len) { return ld != 0 ? ld : len; }
+
 template <typename T>
 T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
@@ -619,6 +651,87 @@ int moe_forward(const moe_desc* desc, const void* x, const uint8_t* valid_rows,
   if (workspace_bytes < p.total) return MOE_ERR_WORKSPACE;
   return forward_impl(p, desc, x, valid_rows, router_w, w13, w2, out, workspace,
                       static_cast<hipStream_t>(stream));
+}
+
+size_t moe_few_workspace_size(const moe_desc* desc, int32_t topk) {
+  FewPlan p;
+  if (make_few_plan(desc, topk, &p) != MOE_OK) return 0;
+  return p.total;
+}
+
+int moe_forward_few(const moe_desc* desc, const void* x, const uint8_t* valid_rows,
+                    const void* router_w, const void* w13, const void* w2, int32_t topk,
+                    void* out, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  FewPlan p;
+  const int st = make_few_plan(desc, topk, &p);
+  if (st != MOE_OK) return st;
+  if (!x || !router_w || !w13 || !w2 || !out || !workspace) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(router_w) || !aligned16(w13) || !aligned16(w2) ||
+      !aligned16(workspace))
+    return MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < p.total) return MOE_ERR_WORKSPACE;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (moe::launch_few(desc->w_dtype == MOE_BF16 ? moe::W_BF16 : moe::W_FP8,
+                      desc->w_layout == MOE_LAYOUT_FRAG16, x, valid_rows, router_w, w13, w2,
+                      desc->w13_scale, desc->w2_scale, at<float>(workspace, p.off_part),
+                      at<uint32_t>(workspace, p.off_hw), at<int32_t>(workspace, p.off_ticket), out,
+                      desc->T, desc->H, desc->I, desc->E, desc->n_shared, topk, s) != hipSuccess)
+    return MOE_ERR_HIP;
+  return MOE_OK;
+}
+
+int moe_gemm_fp8(const moe_gemm_desc* desc, const void* a, const float* a_scale, const void* b,
+                 const float* b_scale, void* out, moe_stream_t stream) {
+  if (desc == nullptr || desc->M < 1 || desc->N < 1 || desc->K < 1) return MOE_ERR_INVALID_ARG;
+  if (desc->out_dtype != MOE_F32 && desc->out_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (!a || !a_scale || !b || !b_scale || !out) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(b)) return MOE_ERR_INVALID_ARG;
+  const int64_t nb = ((int64_t)desc->K + 127) / 128;
+  int st;
+  if ((st = check_stride(desc->lda, desc->K, 16)) != MOE_OK ||
+      (st = check_stride(desc->ldb, desc->K, 16)) != MOE_OK ||
+      (st = check_stride(desc->ld_as, nb, 1)) != MOE_OK ||
+      (st = check_stride(desc->ldo, desc->N, 1)) != MOE_OK)
+    return st;
+  if (desc->K % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  const moe::Fp8Gemm p{static_cast<const uint8_t*>(a), a_scale, static_cast<const uint8_t*>(b),
+                       b_scale, out, desc->M, desc->N, desc->K, or_dense(desc->lda, desc->K),
+                       or_dense(desc->ld_as, nb), or_dense(desc->ldb, desc->K),
+                       or_dense(desc->ldo, desc->N), desc->out_dtype == MOE_F32};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return moe::launch_fp8_gemm(p, s) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+namespace {
+int quant_rows(const moe_quant_desc* d, const void* in, void* codes, float* scales, bool silu_mul,
+               moe_stream_t stream) {
+  if (d == nullptr || d->rows < 1 || d->cols < 1) return MOE_ERR_INVALID_ARG;
+  if (d->in_dtype != MOE_F32 && d->in_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (!in || !codes || !scales || !aligned16(in) || !aligned16(codes)) return MOE_ERR_INVALID_ARG;
+  if (d->cols % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  const bool bf16 = d->in_dtype == MOE_BF16;
+  const int64_t len = (silu_mul ? 2 : 1) * (int64_t)d->cols, nb = ((int64_t)d->cols + 127) / 128;
+  int st;
+  if ((st = check_stride(d->ld_in, len, bf16 ? 8 : 4)) != MOE_OK ||
+      (st = check_stride(d->ld_codes, d->cols, 16)) != MOE_OK ||
+      (st = check_stride(d->ld_scales, nb, 1)) != MOE_OK)
+    return st;
+  const moe::QuantRows p{in, static_cast<uint8_t*>(codes), scales, d->rows, d->cols,
+                         or_dense(d->ld_in, len), or_dense(d->ld_codes, d->cols),
+                         or_dense(d->ld_scales, nb), bf16};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return moe::launch_quant(p, silu_mul, s) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+}  // namespace
+
+int moe_quant_fp8(const moe_quant_desc* desc, const void* x, void* codes, float* scales,
+                  moe_stream_t stream) {
+  return quant_rows(desc, x, codes, scales, false, stream);
+}
+
+int moe_silu_mul_quant_fp8(const moe_quant_desc* desc, const void* gu, void* codes, float* scales,
+                           moe_stream_t stream) {
+  return quant_rows(desc, gu, codes, scales, true, stream);
 }
 
 size_t moe_block_signal_count(const moe_desc* desc) {

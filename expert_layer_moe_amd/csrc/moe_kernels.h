@@ -201,4 +201,45 @@ int combine_grid_y(int T, int H, int yfmt);
 // a[0 .. na) = 0 and b[0 .. nb) = 0 (a fill kernel: safe under graph capture)
 hipError_t launch_zero_i32(int32_t* a, size_t na, int32_t* b, size_t nb, hipStream_t s);
 
+
+// ---- few token rows ----------------------------------------------------------
+constexpr int kFewRows = 16;        // most rows of a call
+constexpr int kFewLogitParts = 4;   // K parts of the router logits
+// The whole layer for T <= kFewRows rows, bf16 activations, bf16 or fp8
+// weights, in two launches.  part: [kFewLogitParts][T][E] fp32; hw: [T (k +
+// n_shared)][I] words, 16-byte aligned; ticket: one int32.  None of them
+// needs to hold anything on entry.
+hipError_t launch_few(int wkind, bool packed, const void* x, const uint8_t* valid, const void* R,
+                      const void* w13, const void* w2, const float* s13, const float* s2,
+                      float* part, uint32_t* hw, int32_t* ticket, void* out, int T, int H, int I,
+                      int E, int n_shared, int k, hipStream_t s);
+
+// ---- fp8 block-scale product and token quantisation ----------------------------
+// out[M, N] = a[M, K] b[N, K]^T, e4m3 codes, scales sa [M][ceil(K / 128)],
+// sb [ceil(N / 128)][ceil(K / 128)]; strides in elements, K, lda and ldb
+// multiples of 16.
+struct Fp8Gemm {
+  const uint8_t* a;
+  const float* sa;
+  const uint8_t* b;
+  const float* sb;
+  void* out;
+  int M, N, K;
+  long long lda, ldsa, ldb, ldo;
+  bool out_f32;
+};
+hipError_t launch_fp8_gemm(const Fp8Gemm& p, hipStream_t s);
+// codes and scales of rows of cols values (of SiLU(gate) * up of rows of 2
+// cols values: gate, then up); strides in elements; cols and ld_codes
+// multiples of 16, rows of in 16-byte aligned.
+struct QuantRows {
+  const void* in;
+  uint8_t* codes;
+  float* scales;
+  int rows, cols;
+  long long ld_in, ld_codes, ld_scales;
+  bool bf16;
+};
+hipError_t launch_quant(const QuantRows& p, bool silu_mul, hipStream_t s);
+
 }  // namespace moe

@@ -7,8 +7,10 @@ from typing import Optional
 import torch
 
 from .binding import (MOE_BF16, MOE_F32, MOE_FP8_E4M3, MOE_LAYOUT_FRAG16,
-                      MOE_LAYOUT_ROW_MAJOR, alloc_workspace, make_desc, moe_forward,
-                      moe_forward_signaled, moe_pack_weights, moe_route)
+                      MOE_LAYOUT_ROW_MAJOR, _empty, alloc_few_workspace, alloc_workspace,
+                      make_desc, moe_forward, moe_forward_few, moe_forward_signaled,
+                      moe_gemm_fp8, moe_pack_weights, moe_quant_fp8, moe_route,
+                      moe_silu_mul_quant_fp8)
 
 _ACT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 _W = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.uint8: MOE_FP8_E4M3}
@@ -47,6 +49,7 @@ class DeviceLayer:
         self.device = device
         self.block_m = block_m
         self._ws = {}
+        self._few_ws = {}
         self.layout = MOE_LAYOUT_ROW_MAJOR
         if packed:
             self.w13, self.w2 = moe_pack_weights(self.desc(1), self.w13, self.w2)
@@ -68,6 +71,30 @@ class DeviceLayer:
         ws = workspace if workspace is not None else self.workspace(T)
         moe_forward(self.desc(T), x, valid, self.router, self.w13, self.w2, self.topk,
                     out, ws, stream)
+        return out
+
+    def few_workspace(self, T: int, stream=None) -> torch.Tensor:
+        """Workspace of forward_few, one per row count and stream (calls on one
+        stream follow each other); a new one while a graph is captured, so that
+        graphs do not share it with each other or with eager calls."""
+        if torch.cuda.is_current_stream_capturing():
+            with torch.cuda.stream(stream):
+                return alloc_few_workspace(self.desc(T), self.topk, self.router.device)
+        s = stream if stream is not None else torch.cuda.current_stream(self.router.device)
+        key = (T, s.cuda_stream)
+        if key not in self._few_ws:
+            self._few_ws[key] = alloc_few_workspace(self.desc(T), self.topk, self.router.device)
+        return self._few_ws[key]
+
+    def forward_few(self, x, valid=None, out=None, workspace=None, stream=None):
+        """forward for at most FEW_MAX_ROWS token rows (one or a few sequences
+        decoding), in two launches.  Returns out."""
+        T = x.shape[0]
+        if out is None:
+            out = _empty(x.shape, x.dtype, x.device, stream)
+        ws = workspace if workspace is not None else self.few_workspace(T, stream)
+        moe_forward_few(self.desc(T), x, valid, self.router, self.w13, self.w2, self.topk,
+                        out, ws, stream)
         return out
 
     def block_signals(self, T: int) -> torch.Tensor:
@@ -96,3 +123,34 @@ class DeviceLayer:
         moe_route(self.desc(T), x, valid, self.router, self.topk, ids, w, lg,
                   self.workspace(T), stream)
         return ids, w, lg
+
+
+class DenseFP8:
+    """The FFN of a dense block in the experts' fp8 format, tokens quantised
+    too: out = W2 (SiLU(W_gate x) * (W_up x)) in fp8 products with block scales.
+
+    w13 [2I, H] (gate rows, then up rows) and w2 [H, I]: uint8 e4m3fn codes,
+    with fp32 block scales s13 [ceil(2I/128), ceil(H/128)], s2 [ceil(H/128),
+    ceil(I/128)].  H and I multiples of 16.
+    """
+
+    def __init__(self, w13, w2, s13, s2, device="cuda"):
+        self.w13 = w13.to(device).contiguous()
+        self.w2 = w2.to(device).contiguous()
+        self.s13 = s13.to(device, torch.float32).contiguous()
+        self.s2 = s2.to(device, torch.float32).contiguous()
+        self.I, self.H = self.w13.shape[0] // 2, self.w13.shape[1]
+        blocks = lambda n: (n + 127) // 128  # noqa: E731
+        if tuple(self.w13.shape) != (2 * self.I, self.H) or tuple(self.w2.shape) != (self.H, self.I):
+            raise ValueError("dense weights are w13 [2I, H] and w2 [H, I]")
+        if tuple(self.s13.shape) != (blocks(2 * self.I), blocks(self.H)) or \
+                tuple(self.s2.shape) != (blocks(self.H), blocks(self.I)):
+            raise ValueError("s13 is [ceil(2I/128), ceil(H/128)], s2 [ceil(H/128), ceil(I/128)]")
+
+    def forward(self, x, out=None, stream=None):
+        """x [T, H] bf16 or fp32 -> out [T, H], bf16 unless `out` is fp32.  The
+        gate/up product stays in fp32 between the kernels."""
+        xq, xs = moe_quant_fp8(x, stream=stream)
+        gu = moe_gemm_fp8(xq, xs, self.w13, self.s13, out_dtype=torch.float32, stream=stream)
+        hq, hs = moe_silu_mul_quant_fp8(gu, stream=stream)
+        return moe_gemm_fp8(hq, hs, self.w2, self.s2, out=out, stream=stream)

@@ -254,6 +254,100 @@ int moe_forward_noalloc(const moe_desc* desc, const void* x, const uint8_t* vali
                         const void* router_w, const void* w13, const void* w2,
                         int32_t topk, void* out, moe_stream_t stream);
 
+/* Most token rows of a moe_forward_few call. */
+#define MOE_FEW_MAX_ROWS 16
+
+/* Bytes of workspace moe_forward_few needs (host, pure).  Returns 0 if the
+ * descriptor is invalid or not one moe_forward_few takes. */
+size_t moe_few_workspace_size(const moe_desc* desc, int32_t topk);
+
+/* moe_forward for a few token rows (T <= MOE_FEW_MAX_ROWS: one or a few
+ * sequences decoding) in two launches ("Step3 Inference Optimization on AMD
+ * Instinct MI308X", optimisation list: the MoE one-stage kernel).  Same
+ * arguments, layouts and routing rule as moe_forward; the workspace is
+ * moe_few_workspace_size's.  The arithmetic differs from moe_forward's in two
+ * roundings: the routing weight is applied to SiLU(g)*u, which is kept to 16
+ * mantissa bits instead of 8, and the expert sums meet in one fp32
+ * accumulator.  The order of the sums depends on the experts that the call's
+ * rows chose: a row's last bit may differ between batches; equal calls give
+ * equal bits.  A row whose router logits are NaN gets a NaN output row.
+ * desc->block_m is checked and not used.  Errors as moe_forward, plus
+ * MOE_ERR_UNSUPPORTED for T > MOE_FEW_MAX_ROWS or fp32 layers.  Calls must not
+ * share a workspace while either runs; its contents need not be kept or
+ * cleared between calls. */
+int moe_forward_few(const moe_desc* desc, const void* x, const uint8_t* valid_rows,
+                    const void* router_w, const void* w13, const void* w2,
+                    int32_t topk, void* out, void* workspace,
+                    size_t workspace_bytes, moe_stream_t stream);
+
+/* ---- fp8 block-scale product ------------------------------------------------
+ * For dense layers beside the expert layer (projections, the FFN of dense
+ * blocks), in the expert weights' format ("AMD Instinct MI355X: ATOM ...":
+ * block-scale GEMM).
+ *
+ * Descriptor of moe_gemm_fp8 (host struct).
+ *   M, N, K    >= 1; K a multiple of 16 (it may end inside a 128-wide block)
+ *   out_dtype  MOE_F32 or MOE_BF16
+ *   lda, ldb   row strides of a and b in elements (bytes): 0 = K, else at
+ *              least K and a multiple of 16
+ *   ld_as      row stride of a_scale in elements: 0 = ceil(K / 128), else at
+ *              least that
+ *   ldo        row stride of out in elements: 0 = N, else at least N */
+typedef struct moe_gemm_desc {
+  int32_t M, N, K;
+  int32_t out_dtype;
+  int64_t lda, ldb, ld_as, ldo;
+} moe_gemm_desc;
+
+/* out[m, n] = sum_b a_scale[m, b] b_scale[n / 128, b]
+ *             sum_{k in block b} a[m, k] b[n, k],   blocks of 128 along K.
+ *   a        [M, K] e4m3fn codes (token rows, moe_quant_fp8)
+ *   a_scale  [M, ceil(K / 128)] fp32
+ *   b        [N, K] e4m3fn codes (weights, K contiguous)
+ *   b_scale  [ceil(N / 128), ceil(K / 128)] fp32, dense
+ *   out      [M, N] out_dtype (must not alias an input)
+ * Block sums and their total are fp32 and rounded once to out_dtype; NaN
+ * codes give NaN in their row or column.  The bits of a row do not depend on
+ * the other rows' values.  Nothing of out outside its M x N values is
+ * written.  MOE_ERR_UNSUPPORTED: K or a stride not a multiple of 16;
+ * MOE_ERR_INVALID_ARG: null or (a, b) misaligned pointers, sizes below 1,
+ * strides below the row length, other out_dtype. */
+int moe_gemm_fp8(const moe_gemm_desc* desc, const void* a, const float* a_scale,
+                 const void* b, const float* b_scale, void* out, moe_stream_t stream);
+
+/* Descriptor of the token quantisations (host struct).
+ *   rows       >= 1
+ *   cols       values of an output row, >= 1, a multiple of 16
+ *   in_dtype   MOE_F32 or MOE_BF16
+ *   ld_in      row stride of the input in elements: 0 = dense, else at least
+ *              the row length; rows must stay 16-byte aligned (a multiple of
+ *              4 for fp32, of 8 for bf16)
+ *   ld_codes   row stride of codes: 0 = cols, else at least cols and a
+ *              multiple of 16
+ *   ld_scales  row stride of scales: 0 = ceil(cols / 128), else at least that */
+typedef struct moe_quant_desc {
+  int32_t rows, cols;
+  int32_t in_dtype;
+  int64_t ld_in, ld_codes, ld_scales;
+} moe_quant_desc;
+
+/* Token rows x [rows, cols] -> codes [rows, cols] (e4m3fn) and scales [rows,
+ * ceil(cols / 128)] (fp32), one scale per 128 values of a row (the last block
+ * may be shorter): scale = max(max |x|, 1e-12) / 448, code = e4m3(x / scale),
+ * both divisions correctly rounded in fp32, the code rounded to nearest even.
+ * A NaN value gives a NaN code and leaves the rest of its block as if it were
+ * 0; a block that holds an infinity gets an infinite scale, so that all of it
+ * stands for NaN.  Gaps between rows are not written.  Errors as moe_gemm_fp8
+ * (MOE_ERR_UNSUPPORTED for cols or strides off their multiples). */
+int moe_quant_fp8(const moe_quant_desc* desc, const void* x, void* codes, float* scales,
+                  moe_stream_t stream);
+
+/* The same of v = SiLU(g) * u for gu [rows, 2 cols]: g the first cols values
+ * of a row, u the last (the gate/up product of a dense FFN, rows of w13
+ * order), v kept in fp32. */
+int moe_silu_mul_quant_fp8(const moe_quant_desc* desc, const void* gu, void* codes,
+                           float* scales, moe_stream_t stream);
+
 /* One-time re-layout of the expert weights (at load time) into the order in
  * which the layer's MFMA kernels fetch them, so that each wave-wide weight
  * load is one contiguous 1 KB (bf16) / 512 B (fp8) block instead of 16 rows x
