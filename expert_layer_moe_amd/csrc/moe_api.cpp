@@ -1,6 +1,7 @@
 // C ABI of the MoE layer: validation, workspace layout, launch sequence.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <climits>
 #include <mutex>
@@ -253,6 +254,9 @@ int check_stride(int64_t ld, int64_t len, int multiple) {
   if ((ld != 0 ? ld : len) % multiple != 0) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
+
+constexpr int32_t kMaxGemmRows = 1 << 30;
+constexpr int64_t kMaxGemmStride = (int64_t)1 << 23;
 
 int64_t or_dense(int64_t ld, int64_t len) { return ld != 0 ? ld : len; }
 
@@ -694,6 +698,11 @@ int moe_gemm_fp8(const moe_gemm_desc* desc, const void* a, const float* a_scale,
       (st = check_stride(desc->ldo, desc->N, 1)) != MOE_OK)
     return st;
   if (desc->K % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  if (desc->M > kMaxGemmRows || desc->N > kMaxGemmRows) return MOE_ERR_UNSUPPORTED;
+  // the tile kernels' offsets from a tile's first row have 32 bits (256 rows)
+  if (std::max(or_dense(desc->lda, desc->K), or_dense(desc->ldb, desc->K)) > kMaxGemmStride ||
+      or_dense(desc->ld_as, nb) > kMaxGemmStride / 4)
+    return MOE_ERR_UNSUPPORTED;
   const moe::Fp8Gemm p{static_cast<const uint8_t*>(a), a_scale, static_cast<const uint8_t*>(b),
                        b_scale, out, desc->M, desc->N, desc->K, or_dense(desc->lda, desc->K),
                        or_dense(desc->ld_as, nb), or_dense(desc->ldb, desc->K),

@@ -286,12 +286,13 @@ int moe_forward_few(const moe_desc* desc, const void* x, const uint8_t* valid_ro
  * block-scale GEMM).
  *
  * Descriptor of moe_gemm_fp8 (host struct).
- *   M, N, K    >= 1; K a multiple of 16 (it may end inside a 128-wide block)
+ *   M, N, K    >= 1; M and N at most 2^30; K a multiple of 16 (it may end
+ *              inside a 128-wide block)
  *   out_dtype  MOE_F32 or MOE_BF16
  *   lda, ldb   row strides of a and b in elements (bytes): 0 = K, else at
- *              least K and a multiple of 16
+ *              least K, a multiple of 16, at most 2^23
  *   ld_as      row stride of a_scale in elements: 0 = ceil(K / 128), else at
- *              least that
+ *              least that, at most 2^21
  *   ldo        row stride of out in elements: 0 = N, else at least N */
 typedef struct moe_gemm_desc {
   int32_t M, N, K;
@@ -309,7 +310,8 @@ typedef struct moe_gemm_desc {
  * Block sums and their total are fp32 and rounded once to out_dtype; NaN
  * codes give NaN in their row or column.  The bits of a row do not depend on
  * the other rows' values.  Nothing of out outside its M x N values is
- * written.  MOE_ERR_UNSUPPORTED: K or a stride not a multiple of 16;
+ * written.  MOE_ERR_UNSUPPORTED: K or a stride not a multiple of 16, or a
+ * size or stride above its limit;
  * MOE_ERR_INVALID_ARG: null or (a, b) misaligned pointers, sizes below 1,
  * strides below the row length, other out_dtype. */
 int moe_gemm_fp8(const moe_gemm_desc* desc, const void* a, const float* a_scale,
