@@ -7,7 +7,6 @@ fallback: if the library is missing, loading raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -276,27 +275,36 @@ def moe_set_one_launch(enable: bool = False):
 FEW_MAX_ROWS = 16   # MOE_FEW_MAX_ROWS
 
 
-@contextlib.contextmanager
-def _on(stream, *tensors):
-    """Makes the tensors' GPU current for a call and yields the raw stream to
-    enqueue on: the given one, or that GPU's current stream.  All tensors (and
-    the stream) must be on one GPU."""
-    device = None
+def _device_of(*tensors) -> int:
+    """The GPU that all the tensors (None: absent) are on."""
+    device = -1
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("tensors must be on the GPU")
-        if device is not None and t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device}: one GPU expected")
-        device = t.device
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream on {stream.device}, tensors on {device}")
-    if device.index == torch.cuda.current_device():
-        yield _stream(stream)
+        if t is not None:
+            d = t.get_device()
+            if d < 0:
+                raise ValueError("tensors must be on the GPU")
+            if device >= 0 and d != device:
+                raise ValueError(f"tensors on cuda:{device} and cuda:{d}: one GPU expected")
+            device = d
+    return device
+
+
+def _enqueue(entry, device: int, stream, *args):
+    """Calls a library entry point with that GPU current, on the given stream
+    or its current one."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        if stream.device_index != device:
+            raise ValueError(f"stream on {stream.device}, tensors on cuda:{device}")
+        raw = stream.cuda_stream
+    if device == torch._C._cuda_getDevice():
+        status = entry(*args, raw)
     else:
         with torch.cuda.device(device):
-            yield _stream(stream)
+            status = entry(*args, raw)
+    if status:
+        _check(status)
 
 
 def _empty(shape, dtype, device, stream):
@@ -308,23 +316,20 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _rows(t: torch.Tensor, name: str, dtypes, cols=None, rows=None):
-    """A matrix whose rows are contiguous: (pointer, row stride)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if t.dim() != 2 or (cols is not None and t.shape[1] != cols) or \
-            (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected "
-                         f"({'rows' if rows is None else rows}, {'cols' if cols is None else cols})")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+def _row_stride(t: torch.Tensor, name: str, dtypes, rows: int, cols: int) -> int:
+    """Row stride of a rows x cols matrix with contiguous rows (0: one row,
+    whose stride says nothing)."""
+    if not (t.dtype in dtypes and t.dim() == 2 and t.size(0) == rows and t.size(1) == cols):
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected "
+                         f"{' or '.join(map(str, dtypes))} ({rows}, {cols})")
+    if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    # the stride of a single row says nothing: dense
-    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else 0
+    return t.stride(0) if rows > 1 else 0
 
 
 _CODES = (torch.uint8, torch.float8_e4m3fn)
+_F32 = (torch.float32,)
+_FLOATS = (torch.float32, torch.bfloat16)
 
 
 def moe_few_workspace_size(desc: moe_desc, topk: int) -> int:
@@ -334,7 +339,7 @@ def moe_few_workspace_size(desc: moe_desc, topk: int) -> int:
 def alloc_few_workspace(desc: moe_desc, topk: int, device="cuda") -> torch.Tensor:
     n = moe_few_workspace_size(desc, topk)
     if n == 0:
-        raise MoeError(-2, "not a layer of a few rows (bf16 activations, at most "
+        raise MoeError(-2, "not a layer of a few rows (bf16 activations, 1 to "
                            f"{FEW_MAX_ROWS} rows)")
     return torch.empty(n, dtype=torch.uint8, device=device)
 
@@ -343,15 +348,36 @@ def moe_forward_few(desc, x, valid_rows, router_w, w13, w2, topk, out, workspace
                     stream=None):
     """moe_forward for at most FEW_MAX_ROWS token rows, in two launches."""
     T, H, E, I, ns = desc.T, desc.H, desc.E, desc.I, desc.n_shared
-    with _on(stream, x, valid_rows, router_w, w13, w2, out, workspace) as s:
-        _check(load_library().moe_forward_few(
-            ctypes.byref(desc), _dev(x, "x", _act(desc), (T, H)),
-            _dev(valid_rows, "valid_rows", torch.uint8, (T,)),
-            _dev(router_w, "router_w", _act(desc), (E, H)),
-            _dev(w13, "w13", _w(desc), (E + ns, 2 * I, H)),
-            _dev(w2, "w2", _w(desc), (E + ns, H, I)), topk,
-            _dev(out, "out", _act(desc), (T, H)),
-            _dev(workspace, "workspace", torch.uint8), workspace.numel(), s))
+    _dev(router_w, "router_w", _act(desc), (E, H))
+    _dev(w13, "w13", _w(desc), (E + ns, 2 * I, H))
+    _dev(w2, "w2", _w(desc), (E + ns, H, I))
+    _forward_few(ctypes.byref(desc), T, H, _act(desc), _device_of(router_w, w13, w2), x,
+                 valid_rows, router_w.data_ptr(), w13.data_ptr(), w2.data_ptr(), topk, out,
+                 workspace, stream)
+
+
+def _forward_few(desc, T, H, act, device, x, valid_rows, router_w, w13, w2, topk, out,
+                 workspace, stream):
+    """moe_forward_few with the layer's own arrays checked before (a reference
+    to the descriptor, the GPU and the addresses of the weights)."""
+    for t, name in ((x, "x"), (out, "out")):
+        if t.dtype != act or t.dim() != 2 or t.size(0) != T or t.size(1) != H or \
+                not t.is_contiguous():
+            raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected contiguous {act} "
+                             f"({T}, {H})")
+    valid = None
+    if valid_rows is not None:
+        if valid_rows.dtype != torch.uint8 or valid_rows.dim() != 1 or \
+                valid_rows.size(0) != T or not valid_rows.is_contiguous():
+            raise ValueError(f"valid_rows: {valid_rows.dtype} {tuple(valid_rows.shape)}, "
+                             f"expected contiguous torch.uint8 ({T},)")
+        valid = valid_rows.data_ptr()
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace: contiguous torch.uint8 expected")
+    if _device_of(x, valid_rows, out, workspace) != device:
+        raise ValueError(f"tensors on {x.device}, the layer on cuda:{device}")
+    _enqueue(load_library().moe_forward_few, device, stream, desc, x.data_ptr(), valid, router_w,
+             w13, w2, topk, out.data_ptr(), workspace.data_ptr(), workspace.numel())
 
 
 def moe_gemm_fp8(a, a_scale, b, b_scale, out=None, out_dtype=torch.bfloat16, stream=None):
@@ -359,36 +385,41 @@ def moe_gemm_fp8(a, a_scale, b, b_scale, out=None, out_dtype=torch.bfloat16, str
     float8_e4m3fn) a [M, K], b [N, K]; a_scale [M, ceil(K/128)], b_scale
     [ceil(N/128), ceil(K/128)] fp32.  a, b, a_scale and out may have wider
     rows (row strides); out is allocated here when not given."""
-    ap, lda = _rows(a, "a", _CODES)
+    if a.dim() != 2 or b.dim() != 2:
+        raise ValueError("a and b are matrices")
     M, K = a.shape
-    bp, ldb = _rows(b, "b", _CODES, cols=K)
-    N = b.shape[0]
+    N = b.size(0)
     nb = (K + 127) // 128
-    sp, ld_as = _rows(a_scale, "a_scale", (torch.float32,), cols=nb, rows=M)
+    lda = _row_stride(a, "a", _CODES, M, K)
+    ldb = _row_stride(b, "b", _CODES, N, K)
+    ld_as = _row_stride(a_scale, "a_scale", _F32, M, nb)
+    _row_stride(b_scale, "b_scale", _F32, (N + 127) // 128, nb)
+    if not b_scale.is_contiguous():
+        raise ValueError("b_scale must be contiguous")
     if out is None:
         out = _empty((M, N), out_dtype, a.device, stream)
-    op, ldo = _rows(out, "out", (torch.bfloat16, torch.float32), cols=N, rows=M)
-    with _on(stream, a, a_scale, b, b_scale, out) as s:
-        d = moe_gemm_desc(M, N, K, _DT[out.dtype], lda, ldb, ld_as, ldo)
-        _check(load_library().moe_gemm_fp8(
-            ctypes.byref(d), ap, sp, bp,
-            _dev(b_scale, "b_scale", torch.float32, ((N + 127) // 128, nb)), op, s))
+    ldo = _row_stride(out, "out", _FLOATS, M, N)
+    _enqueue(load_library().moe_gemm_fp8, _device_of(a, a_scale, b, b_scale, out), stream,
+             moe_gemm_desc(M, N, K, _DT[out.dtype], lda, ldb, ld_as, ldo), a.data_ptr(),
+             a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), out.data_ptr())
     return out
 
 
-def _quant(entry, x, cols, codes, scales, stream):
-    xp, ld_in = _rows(x, "x", (torch.float32, torch.bfloat16))
-    M = x.shape[0]
+def _quant(entry, x, per_col, codes, scales, stream):
+    if x.dim() != 2 or x.size(1) % per_col != 0:
+        raise ValueError(f"a matrix of {per_col} n columns expected, not {tuple(x.shape)}")
+    M, cols = x.size(0), x.size(1) // per_col
     nb = (cols + 127) // 128
+    ld_in = _row_stride(x, "input", _FLOATS, M, cols * per_col)
     if codes is None:
         codes = _empty((M, cols), torch.uint8, x.device, stream)
     if scales is None:
         scales = _empty((M, nb), torch.float32, x.device, stream)
-    cp, ld_codes = _rows(codes, "codes", _CODES, cols=cols, rows=M)
-    sp, ld_scales = _rows(scales, "scales", (torch.float32,), cols=nb, rows=M)
-    with _on(stream, x, codes, scales) as s:
-        d = moe_quant_desc(M, cols, _DT[x.dtype], ld_in, ld_codes, ld_scales)
-        _check(entry(ctypes.byref(d), xp, cp, sp, s))
+    ld_codes = _row_stride(codes, "codes", _CODES, M, cols)
+    ld_scales = _row_stride(scales, "scales", _F32, M, nb)
+    _enqueue(entry, _device_of(x, codes, scales), stream,
+             moe_quant_desc(M, cols, _DT[x.dtype], ld_in, ld_codes, ld_scales), x.data_ptr(),
+             codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -396,15 +427,12 @@ def moe_quant_fp8(x, codes=None, scales=None, stream=None):
     """Token rows x [M, K] (bf16 or fp32; rows may be strided) -> e4m3fn codes
     [M, K] (uint8) and fp32 scales [M, ceil(K/128)], allocated here when not
     given.  Returns (codes, scales)."""
-    return _quant(load_library().moe_quant_fp8, x, x.shape[-1], codes, scales, stream)
+    return _quant(load_library().moe_quant_fp8, x, 1, codes, scales, stream)
 
 
 def moe_silu_mul_quant_fp8(gu, codes=None, scales=None, stream=None):
     """moe_quant_fp8 of SiLU(g) * u for gu [M, 2 I] (gate columns, then up)."""
-    if gu.shape[-1] % 2 != 0:
-        raise ValueError("gu holds gate and up columns: an even number")
-    return _quant(load_library().moe_silu_mul_quant_fp8, gu, gu.shape[-1] // 2, codes, scales,
-                  stream)
+    return _quant(load_library().moe_silu_mul_quant_fp8, gu, 2, codes, scales, stream)
 
 
 SCRATCH_BYTES = 64 << 20   # MOE_SCRATCH_BYTES

@@ -2,13 +2,14 @@
 moe_forward calls (memory management only; the math is in the kernels)."""
 from __future__ import annotations
 
+import ctypes
 from typing import Optional
 
 import torch
 
 from .binding import (MOE_BF16, MOE_F32, MOE_FP8_E4M3, MOE_LAYOUT_FRAG16,
-                      MOE_LAYOUT_ROW_MAJOR, _empty, alloc_few_workspace, alloc_workspace,
-                      make_desc, moe_forward, moe_forward_few, moe_forward_signaled,
+                      MOE_LAYOUT_ROW_MAJOR, _empty, _forward_few, alloc_few_workspace,
+                      alloc_workspace, make_desc, moe_forward, moe_forward_signaled,
                       moe_gemm_fp8, moe_pack_weights, moe_quant_fp8, moe_route,
                       moe_silu_mul_quant_fp8)
 
@@ -49,7 +50,7 @@ class DeviceLayer:
         self.device = device
         self.block_m = block_m
         self._ws = {}
-        self._few_ws = {}
+        self._few_ws, self._few = {}, {}
         self.layout = MOE_LAYOUT_ROW_MAJOR
         if packed:
             self.w13, self.w2 = moe_pack_weights(self.desc(1), self.w13, self.w2)
@@ -80,21 +81,28 @@ class DeviceLayer:
         if torch.cuda.is_current_stream_capturing():
             with torch.cuda.stream(stream):
                 return alloc_few_workspace(self.desc(T), self.topk, self.router.device)
-        s = stream if stream is not None else torch.cuda.current_stream(self.router.device)
-        key = (T, s.cuda_stream)
-        if key not in self._few_ws:
-            self._few_ws[key] = alloc_few_workspace(self.desc(T), self.topk, self.router.device)
-        return self._few_ws[key]
+        raw = torch._C._cuda_getCurrentRawStream(self.router.get_device()) if stream is None \
+            else stream.cuda_stream
+        ws = self._few_ws.get((T, raw))
+        if ws is None:
+            ws = alloc_few_workspace(self.desc(T), self.topk, self.router.device)
+            self._few_ws[T, raw] = ws
+        return ws
 
     def forward_few(self, x, valid=None, out=None, workspace=None, stream=None):
         """forward for at most FEW_MAX_ROWS token rows (one or a few sequences
         decoding), in two launches.  Returns out."""
-        T = x.shape[0]
+        T = x.size(0)
+        few = self._few.get(T)
+        if few is None:
+            d = self.desc(T)
+            few = self._few[T] = (d, ctypes.byref(d))
         if out is None:
-            out = _empty(x.shape, x.dtype, x.device, stream)
+            out = _empty((T, self.H), x.dtype, x.device, stream)
         ws = workspace if workspace is not None else self.few_workspace(T, stream)
-        moe_forward_few(self.desc(T), x, valid, self.router, self.w13, self.w2, self.topk,
-                        out, ws, stream)
+        _forward_few(few[1], T, self.H, self.router.dtype, self.router.get_device(), x, valid,
+                     self.router.data_ptr(), self.w13.data_ptr(), self.w2.data_ptr(), self.topk,
+                     out, ws, stream)
         return out
 
     def block_signals(self, T: int) -> torch.Tensor:
@@ -149,8 +157,9 @@ class DenseFP8:
 
     def forward(self, x, out=None, stream=None):
         """x [T, H] bf16 or fp32 -> out [T, H], bf16 unless `out` is fp32.  The
-        gate/up product stays in fp32 between the kernels."""
+        gate/up product is bf16 between the kernels: its rounding, 2^-9, is
+        nothing beside that of the codes made of it, 2^-4."""
         xq, xs = moe_quant_fp8(x, stream=stream)
-        gu = moe_gemm_fp8(xq, xs, self.w13, self.s13, out_dtype=torch.float32, stream=stream)
+        gu = moe_gemm_fp8(xq, xs, self.w13, self.s13, stream=stream)
         hq, hs = moe_silu_mul_quant_fp8(gu, stream=stream)
         return moe_gemm_fp8(hq, hs, self.w2, self.s2, out=out, stream=stream)
