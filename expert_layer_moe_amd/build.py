@@ -14,7 +14,7 @@ LIB = os.path.join(LIBDIR, "libmoe_amd.so")
 
 SOURCES = ["route.hip", "align.hip", "layout.hip", "experts.hip", "gemm.hip",
            "few.hip", "fp8_gemm.hip", "quant.hip", "moe_api.cpp"]
-HEADERS = ["moe_common.h", "moe_kernels.h", "topk.h"]
+HEADERS = ["moe_common.h", "moe_kernels.h"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",

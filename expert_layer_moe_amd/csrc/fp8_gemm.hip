@@ -458,7 +458,7 @@ void fp8_gemm_tile_kernel(Fp8Gemm p, int tiles_m, int tiles_n) {
   int cur = 0, next = S - 1;
   for (int kb = 0; kb < nb; kb += KB) {
     tl.step(lds + cur * T::kBytes, lds + next * T::kBytes, scales + (kb / SC & 1) * kScales,
-            scales + (kb / SC & 1 ^ 1) * kScales, kb, wave, lane, acc);
+            scales + ((kb / SC & 1) ^ 1) * kScales, kb, wave, lane, acc);
     cur = cur + 1 == S ? 0 : cur + 1;
     next = next + 1 == S ? 0 : next + 1;
     // the next stage has arrived (the S - 2 behind it may still be on their

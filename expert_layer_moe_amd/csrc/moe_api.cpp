@@ -235,7 +235,9 @@ static_assert(MOE_FEW_MAX_ROWS == moe::kFewRows, "row limit");
 int make_few_plan(const moe_desc* d, int32_t topk, FewPlan* p) {
   const int st = check_desc(d, topk);
   if (st != MOE_OK) return st;
-  if (d->T > MOE_FEW_MAX_ROWS || d->act_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (d->T > MOE_FEW_MAX_ROWS || d->act_dtype != MOE_BF16 ||
+      (long long)d->H * d->I >= moe::kMaxFewArea)
+    return MOE_ERR_UNSUPPORTED;
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t r = o; o = round_up(o + bytes, kAlign); return r; };
   p->off_part = take((size_t)moe::kFewLogitParts * d->T * d->E * 4);

@@ -205,6 +205,7 @@ hipError_t launch_zero_i32(int32_t* a, size_t na, int32_t* b, size_t nb, hipStre
 // ---- few token rows ----------------------------------------------------------
 constexpr int kFewRows = 16;        // most rows of a call
 constexpr int kFewLogitParts = 4;   // K parts of the router logits
+constexpr long long kMaxFewArea = 1LL << 30;   // H I below it: 32-bit offsets inside an expert
 // The whole layer for T <= kFewRows rows, bf16 activations, bf16 or fp8
 // weights, in two launches.  part: [kFewLogitParts][T][E] fp32; hw: [T (k +
 // n_shared)][I] words, 16-byte aligned; ticket: one int32.  None of them

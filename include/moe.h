@@ -272,7 +272,7 @@ size_t moe_few_workspace_size(const moe_desc* desc, int32_t topk);
  * rows chose: a row's last bit may differ between batches; equal calls give
  * equal bits.  A row whose router logits are NaN gets a NaN output row.
  * desc->block_m is checked and not used.  Errors as moe_forward, plus
- * MOE_ERR_UNSUPPORTED for T > MOE_FEW_MAX_ROWS or fp32 layers.  Calls must not
+ * MOE_ERR_UNSUPPORTED for T > MOE_FEW_MAX_ROWS, fp32 layers or H * I >= 2^30.  Calls must not
  * share a workspace while either runs; its contents need not be kept or
  * cleared between calls. */
 int moe_forward_few(const moe_desc* desc, const void* x, const uint8_t* valid_rows,
