@@ -28,34 +28,39 @@ constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * kWave;
 constexpr int kMaxTopk = 16;
 constexpr int kMaxSeg = 257;      // 256 routed experts + 1 shared
-constexpr int kDnCols = 32;       // output columns of a down unit
+// output columns of a down unit
+constexpr int few_down_cols(bool staged) { return staged ? 32 : 16; }
 
-// A word of h' that no gate/up unit has written yet: as a pair of bf16 it is
-// a NaN pattern that pack_h never makes.
+// h' is kept as two bf16, the value rounded and the rest rounded: 16 mantissa
+// bits, so that h' adds nothing visible to the rounding of the output, at two
+// MFMAs where the launch waits for HBM anyway.  In memory: the values [T (k +
+// n_shared) + 1][I], then the rests, the last row of both zero; a 32-bit word
+// holds two columns.  A word that no gate/up unit has written yet is kUnset, a
+// pair of NaN that split_h never makes.
 constexpr uint32_t kUnset = 0xffffffffu;
 
-// h' as two bf16, the value rounded (low half) and the rest rounded (high
-// half): 16 mantissa bits, so that h' adds nothing visible to the rounding of
-// the output, at two MFMAs where the launch waits for HBM anyway.
-__device__ __forceinline__ uint32_t pack_h(float v) {
-  const uint32_t hi = f32_to_bf16_bits(v);
-  if ((hi & 0x7f80u) == 0x7f80u) return (hi & 0x7fu) ? 0x7fc0u : hi;   // NaN, infinity
-  return hi | (uint32_t)f32_to_bf16_bits(v - bf16_bits_to_f32((uint16_t)hi)) << 16;
+__device__ __forceinline__ void split_h(float v, uint32_t& hi, uint32_t& lo) {
+  hi = f32_to_bf16_bits(v);
+  lo = 0;
+  if ((hi & 0x7f80u) != 0x7f80u) lo = f32_to_bf16_bits(v - bf16_bits_to_f32((uint16_t)hi));
+  else if (hi & 0x7fu) hi = 0x7fc0u;   // NaN
 }
 
-// part[z][t][e]: router logits over the z-th part of K (the 8 waves of a
+// part[z][t][e] (rows few_logit_stride(E) apart): router logits over the z-th part of K (the 8 waves of a
 // block split that part again and meet in LDS), 16 experts per block; the
 // second launch adds the parts up.  Rows with valid == 0 are not read.  Also
-// marks every word of h' unset and zeroes the ticket counter.
+// marks h' (rows of I) unset and zeroes the ticket counter.
 __global__ __launch_bounds__(kThreads) void few_logits_kernel(
     const uint16_t* __restrict__ x, const uint8_t* __restrict__ valid,
     const uint16_t* __restrict__ R, float* __restrict__ part, uint32_t* __restrict__ hw,
-    size_t n_hw, int32_t* __restrict__ ticket, int T, int H, int E) {
+    int rows, int I, int32_t* __restrict__ ticket, int T, int H, int E) {
   __shared__ floatx4 red[kWaves][kWave];
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
   const int m = lane % 16, g = lane / 16;
-  const size_t gid = ((size_t)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
-  for (size_t i = gid; i < n_hw; i += (size_t)gridDim.x * gridDim.y * kThreads) hw[i] = kUnset;
+  const uint32_t gid = (blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
+  const uint32_t plane = (uint32_t)(rows + 1) * (I / 2);
+  for (uint32_t i = gid; i < 2 * plane; i += gridDim.x * gridDim.y * kThreads)
+    hw[i] = i % plane < (uint32_t)rows * (I / 2) ? kUnset : 0u;
   if (gid == 0) *ticket = 0;
   const int e = blockIdx.x * 16 + m;
   const bool ev = e < E;
@@ -90,56 +95,9 @@ __global__ __launch_bounds__(kThreads) void few_logits_kernel(
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int t = 4 * g + i;
-    if (t < T) part[((size_t)blockIdx.y * T + t) * E + e] = acc[i];
+    if (t < T) part[((size_t)blockIdx.y * T + t) * few_logit_stride(E) + e] = acc[i];
   }
 }
-
-// The weights of one lane in a 128-wide K block of its row: four MFMA steps of
-// 8.  Row-major fp8 takes two steps with one load, 16 consecutive bytes, so
-// the steps' K order is that of k_of.
-template <bool FP8, bool PW>
-struct WBlock {
-  static constexpr bool kPair = FP8 && !PW;
-  static constexpr int kLoads = kPair ? 2 : 4;
-  typename std::conditional<FP8 && PW, u32x2, u32x4>::type v[kLoads];
-  // K of the lane's first weight of step u
-  static __device__ __forceinline__ int k_of(int u, int g) {
-    return kPair ? 64 * (u / 2) + 16 * g + 8 * (u & 1) : 32 * u + 8 * g;
-  }
-  // Offset (elements) of lane group g's weights of row r behind those of row 0
-  // of a 16-row tile, at K 0.
-  static __device__ __forceinline__ uint32_t lane_offset(int r, int K, int g) {
-    return PW ? (16 * g + r) * 8 : r * K + (kPair ? 16 : 8) * g;
-  }
-  // Loads one load's worth: `tile` points at a tile's first row, K 0; step i of
-  // K block `block`.  The uniform part of the address stays in scalar registers.
-  __device__ __forceinline__ void load1(const void* tile, uint32_t lane, int block, int i) {
-    const uint32_t at = (uint32_t)block * (PW ? 2048 : 128) + i * (PW ? 512 : kPair ? 64 : 32);
-    // packed: whole lines that no other block reads; row-major: a line's other
-    // half is asked for next
-    if constexpr (FP8) {
-      const uint8_t* p = static_cast<const uint8_t*>(tile) + at;
-      if constexpr (PW) v[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p + lane));
-      else v[i] = ld16(p + lane);
-    } else {
-      const uint8_t* p = static_cast<const uint8_t*>(tile) + 2 * (size_t)at;
-      if constexpr (PW) v[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + 2 * lane));
-      else v[i] = ld16(p + 2 * lane);
-    }
-  }
-  __device__ __forceinline__ void load(const void* tile, uint32_t lane, int block) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) load1(tile, lane, block, i);
-  }
-  static __device__ __forceinline__ const void* tile_at(const void* base, size_t row, int K) {
-    return static_cast<const uint8_t*>(base) + row * K * (FP8 ? 1 : 2);
-  }
-  __device__ __forceinline__ bf16x8 get(int u) const {
-    if constexpr (kPair) return fp8x8_to_bf16x8(v[u / 2][2 * (u & 1)], v[u / 2][2 * (u & 1) + 1]);
-    else if constexpr (FP8) return fp8x8_to_bf16x8(v[u][0], v[u][1]);
-    else return as_bf16x8(v[u]);
-  }
-};
 
 // Weights by way of LDS: chunks of 1 KB, 16 bytes a lane, that hold a 16-row
 // tile's next kSteps MFMA steps (bf16 one, fp8 two).
@@ -243,50 +201,51 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, kWave - 1);
 }
 
-// Row t's top-k by one wave (expert e in lane e % 64, register e / 64), into
-// the tables: k rounds of the largest logit left, the lowest expert among
-// equal ones, weights = softmax over the picks.  A loop that stays a loop: run
-// once per launch, unrolled rounds are fetched from memory instruction by
-// instruction (1 us each, against 0.2).
-__device__ __forceinline__ void few_topk(const float* __restrict__ part, int ks, int t, int T, int E,
-                                         int ns, int k, FewTables& tb) {
-  const int lane = threadIdx.x % kWave, kk = k + ns;
-  uint32_t v[4];
+// Row t's top-k by one wave, into the tables: lane l has experts 4 l .. + 3 and
+// keeps the best of them that is left; k rounds of the best of all, the lowest
+// expert among equal ones; weights = softmax over the picks.  A loop that
+// stays a loop: run once per launch, unrolled rounds would be fetched from
+// memory instruction by instruction (1 us each).
+__device__ __forceinline__ void few_topk(const float* __restrict__ part, int t, int T, int E, int ns,
+                                         int k, FewTables& tb) {
+  const int lane = threadIdx.x % kWave, kk = k + ns, e0 = 4 * lane;
+  floatx4 s = {0.f, 0.f, 0.f, 0.f};
+  if (e0 < E) {
+    floatx4 p[kFewLogitParts];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = lane + kWave * i;
-    v[i] = 0;
-    if (e < E) {
-      float p[kFewLogitParts];
+    for (int z = 0; z < kFewLogitParts; ++z)
+      p[z] = *reinterpret_cast<const floatx4*>(part + ((size_t)z * T + t) * few_logit_stride(E) + e0);
 #pragma unroll
-      for (int z = 0; z < kFewLogitParts; ++z) p[z] = part[((size_t)z * T + t) * E + e];
-      float s = 0.f;
+    for (int z = 0; z < kFewLogitParts; ++z)
 #pragma unroll
-      for (int z = 0; z < kFewLogitParts; ++z) s += p[z];
-      v[i] = logit_key(s);
-    }
+      for (int c = 0; c < 4; ++c) s[c] += p[z][c];
+  }
+  uint32_t v[4], mine = 0;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    v[c] = e0 + c < E ? logit_key(s[c]) : 0u;
+    mine = max(mine, v[c]);
   }
   uint32_t top = 0, my_v = 0;
   int my_e = -1;
 #pragma unroll 1
   for (int j = 0; j < k; ++j) {
-    const uint32_t best = wave_max(max(max(v[0], v[1]), max(v[2], v[3])));
-    unsigned long long at = __ballot(v[3] == best);
-    int e = 3 * kWave;
-#pragma unroll
-    for (int i = 2; i >= 0; --i) {
-      const unsigned long long b = __ballot(v[i] == best);
-      if (b) at = b, e = kWave * i;
-    }
-    e = best != 0 ? e + __builtin_ctzll(at) : -1;
+    const uint32_t best = wave_max(mine);
+    const int my_best = v[0] == best ? e0 : v[1] == best ? e0 + 1 : v[2] == best ? e0 + 2 : e0 + 3;
+    const int winner = __builtin_ctzll(__ballot(mine == best));
+    int e = __builtin_amdgcn_readlane(my_best, winner);
+    if (best == 0) e = -1;   // none left: the others are NaN
     if (j == 0) top = best;
     if (lane == j) {
       my_v = best;
       my_e = e;
     }
+    mine = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (e == lane + kWave * i) v[i] = 0;
+    for (int c = 0; c < 4; ++c) {
+      if (e == e0 + c) v[c] = 0;
+      mine = max(mine, v[c]);
+    }
   }
   // (equal infinities are an exact tie, not NaN)
   const float w = lane < k ? (my_v == top ? 1.f : expf(key_logit(my_v) - key_logit(top))) : 0.f;
@@ -315,10 +274,11 @@ struct FewArgs {
   const float* s13;
   const float* s2;
   const float* part;
-  uint32_t* hw;        // h' [T (k + ns)][I], words of pack_h
+  uint32_t* hw;        // h'
+  uint32_t plane;      // words from its values to their rests
   int32_t* ticket;
   uint16_t* out;
-  int T, H, I, E, ns, k, ks;
+  int T, H, I, E, ns, k;
 };
 
 __device__ __forceinline__ int take_ticket(int32_t* ticket) {
@@ -326,8 +286,8 @@ __device__ __forceinline__ int take_ticket(int32_t* ticket) {
 }
 
 // The tables the units work from and, STAGED, the token rows in LDS (a row of
-// 2 H bytes every 2 H + kPad, 16 zero bytes behind the last): rows' top-k by
-// the first waves, the copy by the others.  Called by every thread of the
+// 2 H bytes every 2 H + kPad, 16 zero bytes behind the last): a row's top-k by
+// a wave, the copy by the waves without one.  Called by every thread of the
 // block.
 template <bool STAGED>
 __device__ __forceinline__ void few_route(const FewArgs& a, FewTables& tb, uint8_t* xs, int& s_tk) {
@@ -338,9 +298,10 @@ __device__ __forceinline__ void few_route(const FewArgs& a, FewTables& tb, uint8
   if (threadIdx.x < kRows) tb.bad[threadIdx.x] = 0;
   if (threadIdx.x < (kMaxSeg + 31) / 32) tb.chosen[threadIdx.x] = 0;
   __syncthreads();
-  if (STAGED && wave >= a.T) {
-    const int pieces = a.H / 8, threads = kThreads - a.T * kWave;
-    for (int i = threadIdx.x - a.T * kWave; i < a.T * pieces; i += threads) {
+  const int copy = a.T < kWaves ? a.T : 0;   // the first wave that copies
+  if (STAGED && wave >= copy) {
+    const int pieces = a.H / 8, threads = kThreads - copy * kWave;
+    for (int i = threadIdx.x - copy * kWave; i < a.T * pieces; i += threads) {
       const int t = i / pieces, c = i - t * pieces;
       if (a.valid == nullptr || a.valid[t] != 0)
         *reinterpret_cast<u32x4*>(xs + t * (2 * a.H + kPad) + 16 * c) =
@@ -353,7 +314,7 @@ __device__ __forceinline__ void few_route(const FewArgs& a, FewTables& tb, uint8
   // ticket every 10 ns, so the last of 512 blocks waits 5 us)
   if (threadIdx.x == kThreads - 1) s_tk = take_ticket(a.ticket);
   for (int t = wave; t < a.T; t += kWaves)
-    if (a.valid == nullptr || a.valid[t] != 0) few_topk(a.part, a.ks, t, a.T, a.E, a.ns, a.k, tb);
+    if (a.valid == nullptr || a.valid[t] != 0) few_topk(a.part, t, a.T, a.E, a.ns, a.k, tb);
   __syncthreads();
   if (threadIdx.x < nseg) {
     const int e = threadIdx.x;
@@ -484,23 +445,32 @@ __device__ __forceinline__ void gate_up_unit(const FewArgs& a, const FewTables* 
 #pragma unroll
   for (int n = 0; n < NT; ++n) red[n * kWave + lane] = gu.acc[n];
   __syncthreads();
-  if (threadIdx.x < kCols * kRows) {
-    const int c = threadIdx.x % kCols, t = threadIdx.x / kCols;
+  // thread -> (columns c, c + 1, row t)
+  if (threadIdx.x < kCols / 2 * kRows) {
+    const int c = threadIdx.x % (kCols / 2) * 2, t = threadIdx.x / (kCols / 2);
     const int slot = tb->slot[e][t];
     if (slot >= 0) {
       const int up = FP8 ? c : 8 + c;
-      float gs = 0.f, us = 0.f;
+      float gs[2] = {0.f, 0.f}, us[2] = {0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
         const floatx4* r = reinterpret_cast<const floatx4*>(ring + w * kRing);
-        gs += r[c / 4 * 16 + t][c % 4];
-        us += r[(NT - 1) * kWave + up / 4 * 16 + t][up % 4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          gs[i] += r[c / 4 * 16 + t][c % 4 + i];
+          us[i] += r[(NT - 1) * kWave + up / 4 * 16 + t][up % 4 + i];
+        }
       }
       const float wt = tb->w[t][slot - t * (a.k + a.ns)];
-      // readers wait for the word itself to change, so nothing has to be
-      // ordered around the store
-      __hip_atomic_store(a.hw + (size_t)slot * I + c0 + c, pack_h(silu_mul(gs, us) * wt),
-                         __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      uint32_t hi[2], lo[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) split_h(silu_mul(gs[i], us[i]) * wt, hi[i], lo[i]);
+      // readers wait for the words themselves to change, so nothing has to be
+      // ordered around the stores
+      uint32_t* to = a.hw + ((size_t)slot * I + c0 + c) / 2;
+      __hip_atomic_store(to, hi[0] | hi[1] << 16, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __hip_atomic_store(to + a.plane, lo[0] | lo[1] << 16, __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_AGENT);
     }
   }
 }
@@ -509,68 +479,47 @@ __device__ __forceinline__ unsigned long long peek(const uint32_t* p) {
   return __hip_atomic_load(reinterpret_cast<const unsigned long long*>(p), __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ bool unset(unsigned long long v) {
-  return (uint32_t)v == kUnset || (uint32_t)(v >> 32) == kUnset;
+// The same by way of this XCD's caches: what it finds unset may be set by now.
+__device__ __forceinline__ unsigned long long peek_cached(const uint32_t* p) {
+  return __hip_atomic_load(reinterpret_cast<const unsigned long long*>(p), __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_WORKGROUP);
 }
-
-// Reads h' words (each lane N pairs from its p on, or none: zeros) until none
-// of them is unset.  The units that write them have smaller tickets, which
-// blocks take in order and only while they run, so each such unit has ended
-// or is running in a block that waits for nothing: the wait ends.
+// Whether a word of v is unset.
 template <int N>
-__device__ __forceinline__ void read_h(const uint32_t* const (&p)[N], unsigned long long (&v)[N]) {
-  for (;;) {
-    bool again = false;
+__device__ __forceinline__ bool unset(const unsigned long long (&v)[N]) {
+  uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = p[i] == nullptr ? 0ull : peek(p[i]);
-#pragma unroll
-    for (int i = 0; i < N; ++i) again |= unset(v[i]);
-    if (!__any(again)) return;
-    __builtin_amdgcn_s_sleep(1);
-  }
+  for (int i = 0; i < N; ++i) top = max(top, max((uint32_t)v[i], (uint32_t)(v[i] >> 32)));
+  return top == kUnset;
 }
 
-// All of h' to LDS, its two parts apart: row s (an assignment) of 2 I bytes of
-// high parts and 2 I of low parts every 4 I + kPad bytes, 16 zero bytes behind
-// the last row.  By every thread of the block, 16 bytes a turn.
+// All of h' to LDS: row s (an assignment) of 2 I bytes of values and 2 I of
+// rests every 4 I + kPad bytes, 16 zero bytes behind the last row.  By every
+// thread of the block, 16 bytes of both a turn.  Waits for the words that are
+// unset: the units that write them have smaller tickets, which blocks take in
+// order and only while they run, so each such unit has ended or is running in
+// a block that waits for nothing, and the wait ends.
 __device__ __forceinline__ void stage_h(const FewArgs& a, const FewTables* __restrict__ tb,
                                         uint8_t* __restrict__ hs) {
-  const int I = a.I, quads = I / 4, total = a.T * (a.k + a.ns) * quads, row_bytes = 4 * I + kPad;
+  const int I = a.I, pieces = I / 8, total = a.T * (a.k + a.ns) * pieces, row_bytes = 4 * I + kPad;
 #pragma unroll 1
-  for (int j0 = 0; j0 < total; j0 += 2 * kThreads) {
+  for (int j = threadIdx.x; j < total; j += kThreads) {
+    const int slot = j / pieces, t = slot / (a.k + a.ns);
+    if (tb->bad[t] || (a.valid != nullptr && a.valid[t] == 0)) continue;
+    const uint32_t* p = a.hw + 4 * (uint32_t)j;
     unsigned long long v[4];
-    int at[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int j = j0 + i * kThreads + (int)threadIdx.x;
-      const int slot = j / quads, t = min(slot / (a.k + a.ns), a.T - 1);
-      const bool in = j < total && !tb->bad[t] && (a.valid == nullptr || a.valid[t] != 0);
-      at[i] = in ? slot * row_bytes + 8 * (j - slot * quads) : -1;
-    }
     for (;;) {
-      bool again = false;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t* p = a.hw + 4 * (uint32_t)(j0 + i * kThreads + (int)threadIdx.x);
-        v[2 * i] = v[2 * i + 1] = 0;
-        if (at[i] >= 0) {
-          v[2 * i] = peek(p);
-          v[2 * i + 1] = peek(p + 2);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) again |= unset(v[i]);
-      if (!__any(again)) break;
+      v[0] = peek(p);
+      v[1] = peek(p + 2);
+      v[2] = peek(p + a.plane);
+      v[3] = peek(p + a.plane + 2);
+      if (!unset(v)) break;
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (at[i] < 0) continue;
-      const uint32_t w0 = (uint32_t)v[2 * i], w1 = (uint32_t)(v[2 * i] >> 32);
-      const uint32_t w2 = (uint32_t)v[2 * i + 1], w3 = (uint32_t)(v[2 * i + 1] >> 32);
-      *reinterpret_cast<u32x2*>(hs + at[i]) = u32x2{(w0 & 0xffffu) | w1 << 16, (w2 & 0xffffu) | w3 << 16};
-      *reinterpret_cast<u32x2*>(hs + at[i] + 2 * I) =
-          u32x2{w0 >> 16 | (w1 & 0xffff0000u), w2 >> 16 | (w3 & 0xffff0000u)};
-    }
+    uint8_t* to = hs + slot * row_bytes + 16 * (j - slot * pieces);
+    *reinterpret_cast<unsigned long long*>(to) = v[0];
+    *reinterpret_cast<unsigned long long*>(to + 8) = v[1];
+    *reinterpret_cast<unsigned long long*>(to + 2 * I) = v[2];
+    *reinterpret_cast<unsigned long long*>(to + 2 * I + 8) = v[3];
   }
   if (threadIdx.x == 0)
     *reinterpret_cast<u32x4*>(hs + a.T * (a.k + a.ns) * row_bytes) = u32x4{0u, 0u, 0u, 0u};
@@ -631,17 +580,17 @@ struct DownStaged {
 };
 
 // The sums of the waves (each at the start of its part of the ring) to
-// out[t][c0 .. c0 + 31].
-template <bool STAGED>
+// out[t][c0 .. c0 + 16 NT - 1].
+template <bool STAGED, int NT>
 __device__ __forceinline__ void store_out(const FewArgs& a, const FewTables* __restrict__ tb,
-                                          uint8_t* __restrict__ ring, int c0, const floatx4 (&acc)[2]) {
+                                          uint8_t* __restrict__ ring, int c0, const floatx4 (&acc)[NT]) {
   constexpr int kRing = FewShared<STAGED>::kRing;
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
   floatx4* red = reinterpret_cast<floatx4*>(ring + wave * kRing);
 #pragma unroll
-  for (int nt = 0; nt < 2; ++nt) red[nt * kWave + lane] = acc[nt];
+  for (int nt = 0; nt < NT; ++nt) red[nt * kWave + lane] = acc[nt];
   __syncthreads();
-  const int c = threadIdx.x % kDnCols, t = threadIdx.x / kDnCols;
+  const int c = threadIdx.x % (16 * NT), t = threadIdx.x / (16 * NT);
   if (t < a.T) {
     float s = 0.f;
 #pragma unroll
@@ -699,110 +648,153 @@ __device__ __forceinline__ void down_unit_staged(const FewArgs& a, const FewTabl
     if (++q == d.cpe) q = 0, ++ai;
     at = at + 1 == DS::kEntries ? 0 : at + 1;
   }
-  store_out<true>(a, tb, ring, c0, d.acc);
+  store_out<true, 2>(a, tb, ring, c0, d.acc);
 }
 
-// The same with W2 and h' straight to registers, for calls whose h' does not
-// fit in LDS.
+// The same for calls whose h' does not fit in LDS, one tile of 16 columns: the
+// wave's h' words go to registers, kAhead chunks ahead like the weights.
 template <bool FP8, bool PW>
-__device__ __forceinline__ void down_unit(const FewArgs& a, const FewTables* __restrict__ tbp,
-                                          uint8_t* __restrict__ ring, int c0, int& next) {
-  const FewTables& tb = *tbp;
-  using WB = WBlock<FP8, PW>;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
-  const int m = lane % 16, g = lane / 16;
-  const int H = a.H, I = a.I;
-  // a wave's work in groups of GS steps: fp8 a 128-wide block under one
-  // scale, bf16 single steps (72 of them for 9 experts of 256 columns: 9 a
-  // wave, where blocks of four would give three waves 12 and five 8)
-  constexpr int GS = FP8 ? 4 : 1, kBatch = 4 / GS;   // groups loaded at once
-  constexpr int kLoads = FP8 ? WB::kLoads : 1;
-  const int gpe = I / (32 * GS);   // groups of an expert
-  const int n = tb.n_act * gpe;
-  const int s0 = n * wave / kWaves, s1 = n * (wave + 1) / kWaves;
-  const uint32_t wl = WB::lane_offset(m, I, g);
-  floatx4 acc[2];
-  acc[0] = acc[1] = floatx4{0.f, 0.f, 0.f, 0.f};
-  bool take = true;
-  for (int s = s0; s < s1; s += kBatch) {
-    typename std::conditional<FP8 && PW, u32x2, u32x4>::type wv[kBatch][2][kLoads];
-    int ai = s / gpe, q = s - ai * gpe;
+struct DownDirect {
+  using WC = WChunk<FP8, PW>;
+  static constexpr int kAhead = FP8 ? 2 : 3, kSets = kAhead + 1;
+  static constexpr int kPairs = 4 * WC::kSteps, kLoads = 1 + kPairs;   // h' pairs, loads of a chunk
+  const uint8_t* w2;   // row c0 of expert 0
+  const uint32_t* hw;
+  uint32_t plane;
+  size_t expert;       // bytes of an expert
+  uint32_t wl;
+  int zero_row;
+  int I, cpe;          // chunks of an expert
+  int ai, q;           // the next chunk to load: chosen expert, chunk of it
+  floatx4 acc, part;
+  unsigned long long h[kSets][kPairs];
+  const uint32_t* hp[kSets];   // this lane's row of a chunk
+
+  // The weights first: once a chunk's h' has arrived, so have they.  (Lanes
+  // without a row have the zero row.)
+  template <int SET>
+  __device__ __forceinline__ void issue(uint8_t* __restrict__ to, const FewTables* __restrict__ tb,
+                                        int lane) {
+    const int e = __builtin_amdgcn_readfirstlane(tb->act[ai]);
+    to_lds16<PW>(buffer_at(w2 + e * expert), wl, q * WC::kBytes, to);
+    const int slot = tb->slot[e][lane % 16];
+    const uint32_t* p = hw + (uint32_t)(slot >= 0 ? slot : zero_row) * (I / 2) + q * 16 * WC::kSteps;
+    hp[SET] = p;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (s + i < s1) {
-        const int e = __builtin_amdgcn_readfirstlane(tb.act[ai]);
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const void* tile = WB::tile_at(a.w2, (size_t)e * H + c0 + 16 * nt, I);
-          WB w;
-          if constexpr (FP8) w.load(tile, wl, q);
-          else w.load1(static_cast<const uint16_t*>(tile) + (size_t)q * (PW ? 512 : 32), wl, 0, 0);
-#pragma unroll
-          for (int l = 0; l < kLoads; ++l) wv[i][nt][l] = w.v[l];
-        }
-        if (++q == gpe) q = 0, ++ai;
-      }
-    }
-    if (take && threadIdx.x == 0) next = take_ticket(a.ticket);
-    take = false;
-    ai = s / gpe, q = s - ai * gpe;
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (s + i >= s1) continue;
-      const int e = __builtin_amdgcn_readfirstlane(tb.act[ai]);
-      const int slot = tb.slot[e][m];
-      u32x4 hi[GS], lo[GS];
-      {
-        const uint32_t* p[4 * GS];
-        unsigned long long v[4 * GS];
-#pragma unroll
-        for (int u = 0; u < GS; ++u) {
-          const int k = GS == 4 ? 128 * q + WB::k_of(u, g) : 32 * q + 8 * g;
-#pragma unroll
-          for (int l = 0; l < 4; ++l)
-            p[4 * u + l] = slot >= 0 ? a.hw + (size_t)slot * I + k + 2 * l : nullptr;
-        }
-        read_h<4 * GS>(p, v);
-#pragma unroll
-        for (int u = 0; u < GS; ++u)
-#pragma unroll
-          for (int l = 0; l < 4; ++l) {
-            const uint32_t w0 = (uint32_t)v[4 * u + l], w1 = (uint32_t)(v[4 * u + l] >> 32);
-            hi[u][l] = (w0 & 0xffffu) | (w1 << 16);
-            lo[u][l] = (w0 >> 16) | (w1 & 0xffff0000u);
-          }
-      }
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        if constexpr (FP8) {
-          WB w;
-#pragma unroll
-          for (int l = 0; l < kLoads; ++l) w.v[l] = wv[i][nt][l];
-          floatx4 p = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int u = 0; u < GS; ++u) {
-            p = mfma16x16x32(w.get(u), as_bf16x8(hi[u]), p);
-            p = mfma16x16x32(w.get(u), as_bf16x8(lo[u]), p);
-          }
-          const float sc = a.s2[((size_t)e * (H / 128) + c0 / 128) * (I / 128) + q];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[nt][j] = fmaf(sc, p[j], acc[nt][j]);
-        } else {
-          acc[nt] = mfma16x16x32(as_bf16x8(wv[i][nt][0]), as_bf16x8(hi[0]), acc[nt]);
-          acc[nt] = mfma16x16x32(as_bf16x8(wv[i][nt][0]), as_bf16x8(lo[0]), acc[nt]);
-        }
-      }
-      if (++q == gpe) q = 0, ++ai;
-    }
+    for (int i = 0; i < kPairs; ++i) h[SET][i] = peek_cached(at(p, i, lane));
+    if (++q == cpe) q = 0, ++ai;
   }
-  if (take && threadIdx.x == 0) next = take_ticket(a.ticket);
-  store_out<false>(a, tbp, ring, c0, acc);
+  // Pair i of a chunk: step i / 4, values (0, 1) or rests (2, 3).
+  __device__ __forceinline__ const uint32_t* at(const uint32_t* p, int i, int lane) const {
+    return p + (i / 2 % 2 ? plane : 0) + WC::k_of(i / 4, lane / 16) / 2 + 2 * (i % 2);
+  }
+
+  template <int SET>
+  __device__ __forceinline__ void multiply(const uint8_t* __restrict__ cur, int lane, bool second,
+                                           float sc) {
+    // Words that the prefetch found unset: again, until they are there (see
+    // stage_h).  (The first look stays outside the loop: inside it would have
+    // to wait for the loads behind it too.)
+    if (__any(unset(h[SET]))) {
+      do {
+        __builtin_amdgcn_s_sleep(1);
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) h[SET][i] = peek(at(hp[SET], i, lane));
+      } while (__any(unset(h[SET])));
+    }
+#pragma unroll
+    for (int u = 0; u < WC::kSteps; ++u) {
+      const bf16x8 w = WC::get(cur, u, lane);
+      floatx4& d = FP8 ? part : acc;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const unsigned long long x = h[SET][4 * u + 2 * i], y = h[SET][4 * u + 2 * i + 1];
+        d = mfma16x16x32(w, as_bf16x8(u32x4{(uint32_t)x, (uint32_t)(x >> 32), (uint32_t)y,
+                                            (uint32_t)(y >> 32)}), d);
+      }
+    }
+    if (FP8 && second)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[i] = fmaf(sc, part[i], acc[i]);
+        part[i] = 0.f;
+      }
+  }
+};
+
+template <bool FP8, bool PW>
+__device__ __forceinline__ void down_unit(const FewArgs& a, const FewTables* __restrict__ tb,
+                                          uint8_t* __restrict__ ring, int c0, int& next) {
+  using DD = DownDirect<FP8, PW>;
+  using WC = typename DD::WC;
+  constexpr int kRing = FewShared<false>::kRing;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const int H = a.H, I = a.I;
+  constexpr int kSize = FP8 ? 1 : 2, GC = FP8 ? 2 : 1, S = DD::kSets;
+  static_assert(S * 1024 <= kRing, "a chunk of weights per set");
+  DD d;
+  d.w2 = static_cast<const uint8_t*>(a.w2) + (size_t)c0 * I * kSize;
+  d.hw = a.hw;
+  d.plane = a.plane;
+  d.zero_row = a.T * (a.k + a.ns);
+  d.expert = (size_t)H * I * kSize;
+  d.wl = PW ? 16 * lane : WC::lane_offset(lane % 16, I, lane / 16);
+  d.I = I;
+  d.cpe = I / (32 * WC::kSteps);
+  d.acc = d.part = floatx4{0.f, 0.f, 0.f, 0.f};
+  const int n = tb->n_act * (d.cpe / GC);
+  const int s0 = n * wave / kWaves * GC, s1 = n * (wave + 1) / kWaves * GC;
+  int ai = s0 / d.cpe, q = s0 - ai * d.cpe;
+  d.ai = ai;
+  d.q = q;
+  uint8_t* mine = ring + wave * kRing;
+  auto run = [&](auto set, auto tail, int s) {
+    constexpr int SET = decltype(set)::value, LAST = (SET + DD::kAhead) % S;
+    constexpr bool TAIL = decltype(tail)::value;
+    if (TAIL && s >= s1) return;
+    wait_loads<63>();   // the reads of the chunk that is loaded over
+    float sc = 0.f;
+    if constexpr (FP8) {
+      const int e = __builtin_amdgcn_readfirstlane(tb->act[ai]);
+      sc = a.s2[((size_t)e * (H / 128) + c0 / 128) * (I / 128) + q / 2];
+    }
+    if (!TAIL || s + DD::kAhead < s1) d.template issue<LAST>(mine + LAST * 1024, tb, lane);
+    if constexpr (TAIL) wait_loads<0>();
+    else wait_loads<DD::kAhead * DD::kLoads>();
+    d.template multiply<SET>(mine + SET * 1024, lane, q % 2 == 1, sc);
+    if (++q == d.cpe) q = 0, ++ai;
+  };
+  using F = std::false_type;
+  using Y = std::true_type;
+  if (s0 + 0 < s1) d.template issue<0>(mine, tb, lane);
+  if (s0 + 1 < s1) d.template issue<1>(mine + 1024, tb, lane);
+  if constexpr (DD::kAhead > 2)
+    if (s0 + 2 < s1) d.template issue<2>(mine + 2048, tb, lane);
+  if (threadIdx.x == 0) next = take_ticket(a.ticket);
+  int s = s0;
+#pragma unroll 1
+  for (; s + S + DD::kAhead <= s1; s += S) {
+    run(std::integral_constant<int, 0>(), F(), s);
+    run(std::integral_constant<int, 1>(), F(), s + 1);
+    run(std::integral_constant<int, 2>(), F(), s + 2);
+    if constexpr (S > 3) run(std::integral_constant<int, S - 1>(), F(), s + 3);
+  }
+#pragma unroll 1
+  for (; s < s1; s += S) {
+    run(std::integral_constant<int, 0>(), Y(), s);
+    run(std::integral_constant<int, 1>(), Y(), s + 1);
+    run(std::integral_constant<int, 2>(), Y(), s + 2);
+    if constexpr (S > 3) run(std::integral_constant<int, S - 1>(), Y(), s + 3);
+  }
+  const floatx4 acc[1] = {d.acc};
+  store_out<false, 1>(a, tb, ring, c0, acc);
 }
 
 template <bool FP8, bool PW, bool STAGED>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4)))
 void few_experts_kernel(FewArgs a) {
-  static_assert(kThreads == kRows * kDnCols, "one output per thread");
+  constexpr int kDnCols = few_down_cols(STAGED);
+  static_assert(kThreads >= kRows * kDnCols, "one output per thread");
   __shared__ FewShared<STAGED> sh;
   few_route<STAGED>(a, sh.tb, sh.stage, sh.tk);
   constexpr int kCols = few_cols(FP8);
@@ -839,22 +831,22 @@ hipError_t launch_few(int wkind, bool packed, const void* x, const uint8_t* vali
   if (wkind == W_F32 || T < 1 || T > kFewRows || E + n_shared > kMaxSeg || k > kMaxTopk ||
       H % 128 != 0 || I % 32 != 0 || (long long)H * I >= kMaxFewArea || (wkind == W_FP8 && I % 128 != 0))
     return hipErrorInvalidValue;
-  const size_t n_hw = (size_t)T * (k + n_shared) * I;
+  const int rows = T * (k + n_shared);
   hipLaunchKernelGGL(few_logits_kernel, dim3((E + 15) / 16, kFewLogitParts), dim3(kThreads), 0, s,
                      static_cast<const uint16_t*>(x), valid, static_cast<const uint16_t*>(R), part,
-                     hw, n_hw, ticket, T, H, E);
+                     hw, rows, I, ticket, T, H, E);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  const FewArgs a{static_cast<const uint16_t*>(x), valid, w13, w2, s13, s2, part, hw, ticket,
-                  static_cast<uint16_t*>(out), T, H, I, E, n_shared, k, kFewLogitParts};
+  const FewArgs a{static_cast<const uint16_t*>(x), valid, w13, w2, s13, s2, part, hw, (uint32_t)(rows + 1) * (I / 2), ticket,
+                  static_cast<uint16_t*>(out), T, H, I, E, n_shared, k};
+  // rows and h' in LDS where they fit
+  const bool staged = (long long)T * (2 * H + kPad) + 16 <= FewShared<true>::kStage &&
+                      (long long)T * (k + n_shared) * (4LL * I + kPad) + 16 <= FewShared<true>::kStage;
   // A block for every gate/up unit, so that they all run at once, from one to
   // two a CU; blocks loop over the tickets.
   const long long n_gu = (long long)(std::min(E, T * k) + n_shared) * (I / few_cols(wkind == W_FP8));
-  const long long units = n_gu + H / kDnCols;
+  const long long units = n_gu + H / few_down_cols(staged);
   const dim3 grid((unsigned)std::min(units, std::max(256LL, std::min(n_gu, 512LL))));
-  // rows and h' in LDS where they fit
-  const bool staged = T < kWaves && (long long)T * (2 * H + kPad) + 16 <= FewShared<true>::kStage &&
-                      (long long)T * (k + n_shared) * (4LL * I + kPad) + 16 <= FewShared<true>::kStage;
 #define MOE_FEW(F, P)                                                                         \
   if (staged)                                                                                 \
     hipLaunchKernelGGL((few_experts_kernel<F, P, true>), grid, dim3(kThreads), 0, s, a);      \
