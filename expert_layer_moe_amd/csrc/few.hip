@@ -28,8 +28,7 @@ constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * kWave;
 constexpr int kMaxTopk = 16;
 constexpr int kMaxSeg = 257;      // 256 routed experts + 1 shared
-// output columns of a down unit
-constexpr int few_down_cols(bool staged) { return staged ? 32 : 16; }
+constexpr int kDownCols = 32;      // output columns of a down unit
 
 // h' is kept as two bf16, the value rounded and the rest rounded: 16 mantissa
 // bits, so that h' adds nothing visible to the rounding of the output, at two
@@ -49,18 +48,20 @@ __device__ __forceinline__ void split_h(float v, uint32_t& hi, uint32_t& lo) {
 // part[z][t][e] (rows few_logit_stride(E) apart): router logits over the z-th part of K (the 8 waves of a
 // block split that part again and meet in LDS), 16 experts per block; the
 // second launch adds the parts up.  Rows with valid == 0 are not read.  Also
-// marks h' (rows of I) unset and zeroes the ticket counter.
+// zeroes the ticket counter, the zero rows of h' (rows of I) and, STAGED, marks
+// the other rows unset.
 __global__ __launch_bounds__(kThreads) void few_logits_kernel(
     const uint16_t* __restrict__ x, const uint8_t* __restrict__ valid,
     const uint16_t* __restrict__ R, float* __restrict__ part, uint32_t* __restrict__ hw,
-    int rows, int I, int32_t* __restrict__ ticket, int T, int H, int E) {
+    int rows, int I, bool staged, int32_t* __restrict__ ticket, int T, int H, int E) {
   __shared__ floatx4 red[kWaves][kWave];
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
   const int m = lane % 16, g = lane / 16;
   const uint32_t gid = (blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
-  const uint32_t plane = (uint32_t)(rows + 1) * (I / 2);
-  for (uint32_t i = gid; i < 2 * plane; i += gridDim.x * gridDim.y * kThreads)
-    hw[i] = i % plane < (uint32_t)rows * (I / 2) ? kUnset : 0u;
+  const uint32_t used = (uint32_t)rows * (I / 2), plane = used + I / 2, n = gridDim.x * gridDim.y * kThreads;
+  for (uint32_t i = gid; i < (uint32_t)I; i += n) hw[used + i % (I / 2) + (i < (uint32_t)I / 2 ? 0 : plane)] = 0u;
+  if (staged)
+    for (uint32_t i = gid; i < 2 * used; i += n) hw[i < used ? i : i + I / 2] = kUnset;
   if (gid == 0) *ticket = 0;
   const int e = blockIdx.x * 16 + m;
   const bool ev = e < E;
@@ -277,6 +278,7 @@ struct FewArgs {
   uint32_t* hw;        // h'
   uint32_t plane;      // words from its values to their rests
   int32_t* ticket;
+  FewTables* tables;   // not STAGED: block 0's, for the down launch
   uint16_t* out;
   int T, H, I, E, ns, k;
 };
@@ -479,11 +481,6 @@ __device__ __forceinline__ unsigned long long peek(const uint32_t* p) {
   return __hip_atomic_load(reinterpret_cast<const unsigned long long*>(p), __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_AGENT);
 }
-// The same by way of this XCD's caches: what it finds unset may be set by now.
-__device__ __forceinline__ unsigned long long peek_cached(const uint32_t* p) {
-  return __hip_atomic_load(reinterpret_cast<const unsigned long long*>(p), __ATOMIC_RELAXED,
-                           __HIP_MEMORY_SCOPE_WORKGROUP);
-}
 // Whether a word of v is unset.
 template <int N>
 __device__ __forceinline__ bool unset(const unsigned long long (&v)[N]) {
@@ -580,17 +577,16 @@ struct DownStaged {
 };
 
 // The sums of the waves (each at the start of its part of the ring) to
-// out[t][c0 .. c0 + 16 NT - 1].
-template <bool STAGED, int NT>
+// out[t][c0 .. c0 + 31].
 __device__ __forceinline__ void store_out(const FewArgs& a, const FewTables* __restrict__ tb,
-                                          uint8_t* __restrict__ ring, int c0, const floatx4 (&acc)[NT]) {
-  constexpr int kRing = FewShared<STAGED>::kRing;
+                                          uint8_t* __restrict__ ring, int c0, const floatx4 (&acc)[2]) {
+  constexpr int kRing = FewShared<true>::kRing;
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
   floatx4* red = reinterpret_cast<floatx4*>(ring + wave * kRing);
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) red[nt * kWave + lane] = acc[nt];
+  for (int nt = 0; nt < 2; ++nt) red[nt * kWave + lane] = acc[nt];
   __syncthreads();
-  const int c = threadIdx.x % (16 * NT), t = threadIdx.x / (16 * NT);
+  const int c = threadIdx.x % kDownCols, t = threadIdx.x / kDownCols;
   if (t < a.T) {
     float s = 0.f;
 #pragma unroll
@@ -624,7 +620,7 @@ __device__ __forceinline__ void down_unit_staged(const FewArgs& a, const FewTabl
   d.low = 2 * I;
 #pragma unroll
   for (int nt = 0; nt < 2; ++nt) d.acc[nt] = d.part[nt] = floatx4{0.f, 0.f, 0.f, 0.f};
-  const int n = tb->n_act * (d.cpe / GC);
+  const int n = __builtin_amdgcn_readfirstlane(tb->n_act) * (d.cpe / GC);
   const int s0 = n * wave / kWaves * GC, s1 = n * (wave + 1) / kWaves * GC;
   int ai = s0 / d.cpe, q = s0 - ai * d.cpe;
   d.ai = ai;
@@ -648,157 +644,181 @@ __device__ __forceinline__ void down_unit_staged(const FewArgs& a, const FewTabl
     if (++q == d.cpe) q = 0, ++ai;
     at = at + 1 == DS::kEntries ? 0 : at + 1;
   }
-  store_out<true, 2>(a, tb, ring, c0, d.acc);
+  store_out(a, tb, ring, c0, d.acc);
 }
 
-// The same for calls whose h' does not fit in LDS, one tile of 16 columns: the
-// wave's h' words go to registers, kAhead chunks ahead like the weights.
-template <bool FP8, bool PW>
-struct DownDirect {
+// Calls whose rows and h' do not fit in LDS have their down product in a
+// launch of its own, where h' is read like any other memory.
+//
+// A wave's loads and sums: NT tiles of 16 columns, W2 by way of LDS, h' in
+// registers, both kAhead chunks ahead.
+template <bool FP8, bool PW, int NT>
+struct Down {
   using WC = WChunk<FP8, PW>;
-  static constexpr int kAhead = FP8 ? 2 : 3, kSets = kAhead + 1;
-  static constexpr int kPairs = 4 * WC::kSteps, kLoads = 1 + kPairs;   // h' pairs, loads of a chunk
-  const uint8_t* w2;   // row c0 of expert 0
-  const uint32_t* hw;
-  uint32_t plane;
-  size_t expert;       // bytes of an expert
+  static constexpr int kEntry = 1024 * NT, kSets = FP8 || NT == 2 ? 4 : 8, kAhead = kSets - 1;
+  static constexpr int kLoads = NT + 2 * WC::kSteps;   // of a chunk
+  const uint8_t* w2;      // row c0 of expert 0
+  const float* s2;
+  const uint16_t* h;
+  size_t expert, plane;   // bytes of an expert, values of a plane of h'
+  uint32_t tile;          // bytes of 16 rows
   uint32_t wl;
-  int zero_row;
-  int I, cpe;          // chunks of an expert
-  int ai, q;           // the next chunk to load: chosen expert, chunk of it
-  floatx4 acc, part;
-  unsigned long long h[kSets][kPairs];
-  const uint32_t* hp[kSets];   // this lane's row of a chunk
+  int I, H, c0, zero_row, cpe;   // cpe: chunks of an expert
+  // the next chunk to load, and how many follow it
+  int ai, q, left;
+  int e;
+  const uint16_t* hrow;   // this lane's
+  floatx4 acc[NT], part[NT];
+  u32x4 hi[kSets][WC::kSteps], lo[kSets][WC::kSteps];
+  float sc[kSets];
 
-  // The weights first: once a chunk's h' has arrived, so have they.  (Lanes
-  // without a row have the zero row.)
-  template <int SET>
-  __device__ __forceinline__ void issue(uint8_t* __restrict__ to, const FewTables* __restrict__ tb,
-                                        int lane) {
-    const int e = __builtin_amdgcn_readfirstlane(tb->act[ai]);
-    to_lds16<PW>(buffer_at(w2 + e * expert), wl, q * WC::kBytes, to);
+  __device__ __forceinline__ void enter(const FewTables* __restrict__ tb, int lane) {
+    e = __builtin_amdgcn_readfirstlane(tb->act[ai]);
     const int slot = tb->slot[e][lane % 16];
-    const uint32_t* p = hw + (uint32_t)(slot >= 0 ? slot : zero_row) * (I / 2) + q * 16 * WC::kSteps;
-    hp[SET] = p;
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i) h[SET][i] = peek_cached(at(p, i, lane));
-    if (++q == cpe) q = 0, ++ai;
-  }
-  // Pair i of a chunk: step i / 4, values (0, 1) or rests (2, 3).
-  __device__ __forceinline__ const uint32_t* at(const uint32_t* p, int i, int lane) const {
-    return p + (i / 2 % 2 ? plane : 0) + WC::k_of(i / 4, lane / 16) / 2 + 2 * (i % 2);
+    hrow = h + (size_t)(slot >= 0 ? slot : zero_row) * I;
   }
 
-  template <int SET>
-  __device__ __forceinline__ void multiply(const uint8_t* __restrict__ cur, int lane, bool second,
-                                           float sc) {
-    // Words that the prefetch found unset: again, until they are there (see
-    // stage_h).  (The first look stays outside the loop: inside it would have
-    // to wait for the loads behind it too.)
-    if (__any(unset(h[SET]))) {
-      do {
-        __builtin_amdgcn_s_sleep(1);
+  // The weights first: once a chunk's h' has arrived, so have they.  (Behind
+  // the last chunk that one again, unused, so that as many loads are on the
+  // way at every step.)
+  __device__ __forceinline__ void issue(uint8_t* __restrict__ to, const FewTables* __restrict__ tb,
+                                        int lane, int set) {
+    const __amdgpu_buffer_rsrc_t buf = buffer_at(w2 + e * expert);
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) h[SET][i] = peek(at(hp[SET], i, lane));
-      } while (__any(unset(h[SET])));
-    }
+    for (int nt = 0; nt < NT; ++nt) to_lds16<PW>(buf, wl, nt * tile + q * WC::kBytes, to + 1024 * nt);
 #pragma unroll
     for (int u = 0; u < WC::kSteps; ++u) {
-      const bf16x8 w = WC::get(cur, u, lane);
-      floatx4& d = FP8 ? part : acc;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const unsigned long long x = h[SET][4 * u + 2 * i], y = h[SET][4 * u + 2 * i + 1];
-        d = mfma16x16x32(w, as_bf16x8(u32x4{(uint32_t)x, (uint32_t)(x >> 32), (uint32_t)y,
-                                            (uint32_t)(y >> 32)}), d);
+      const uint16_t* p = hrow + q * 32 * WC::kSteps + WC::k_of(u, lane / 16);
+      hi[set][u] = ld16(p);
+      lo[set][u] = ld16(p + plane);
+    }
+    if constexpr (FP8) sc[set] = s2[((size_t)e * (H / 128) + c0 / 128) * (I / 128) + q / 2];
+    if (left > 0) {
+      --left;
+      if (++q == cpe) {
+        q = 0;
+        ++ai;
+        enter(tb, lane);
       }
     }
+  }
+
+  // The chunk in `cur`; LOAD: the next one to load goes to `to`.
+  template <bool LOAD>
+  __device__ __forceinline__ void step(const uint8_t* __restrict__ cur, uint8_t* __restrict__ to,
+                                       const FewTables* __restrict__ tb, int lane, int set, bool second) {
+    if constexpr (LOAD) {
+      wait_loads<63>();   // the reads of the chunk that is loaded over
+      issue(to, tb, lane, (set + kAhead) % kSets);
+      wait_loads<kAhead * kLoads>();
+    }
+#pragma unroll
+    for (int u = 0; u < WC::kSteps; ++u)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const bf16x8 w = WC::get(cur + 1024 * nt, u, lane);
+        floatx4& d = FP8 ? part[nt] : acc[nt];
+        d = mfma16x16x32(w, as_bf16x8(hi[set][u]), d);
+        d = mfma16x16x32(w, as_bf16x8(lo[set][u]), d);
+      }
     if (FP8 && second)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[i] = fmaf(sc, part[i], acc[i]);
-        part[i] = 0.f;
-      }
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[nt][i] = fmaf(sc[set], part[nt][i], acc[nt][i]);
+          part[nt][i] = 0.f;
+        }
+  }
+  // Set i's chunk, in its place in the wave's part of the ring.  (A wave's
+  // chunks are whole pairs under a scale.)
+  template <bool LOAD>
+  __device__ __forceinline__ void run(uint8_t* ring, const FewTables* tb, int lane, int i) {
+    step<LOAD>(ring + i * kEntry, ring + (i + kAhead) % kSets * kEntry, tb, lane, i, i % 2 == 1);
   }
 };
 
-template <bool FP8, bool PW>
-__device__ __forceinline__ void down_unit(const FewArgs& a, const FewTables* __restrict__ tb,
-                                          uint8_t* __restrict__ ring, int c0, int& next) {
-  using DD = DownDirect<FP8, PW>;
-  using WC = typename DD::WC;
-  constexpr int kRing = FewShared<false>::kRing;
+constexpr int kDownWaves = 16;
+struct DownShared {
+  FewTables tb;
+  __attribute__((aligned(16))) uint8_t ring[kDownWaves][8 * 1024];
+};
+static_assert(sizeof(FewTables) % 4 == 0 && sizeof(FewTables) <= kFewTableBytes, "copied by words");
+
+// out[t][c0 .. c0 + 16 NT - 1] for every row: as down_unit_staged, by 16 waves.
+template <bool FP8, bool PW, int NT>
+__global__ __launch_bounds__(kDownWaves * kWave) void few_down_kernel(FewArgs a) {
+  using DN = Down<FP8, PW, NT>;
+  using WC = typename DN::WC;
+  __shared__ DownShared sh;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
-  const int H = a.H, I = a.I;
-  constexpr int kSize = FP8 ? 1 : 2, GC = FP8 ? 2 : 1, S = DD::kSets;
-  static_assert(S * 1024 <= kRing, "a chunk of weights per set");
-  DD d;
+  const int H = a.H, I = a.I, c0 = blockIdx.x * 16 * NT;
+  constexpr int kSize = FP8 ? 1 : 2, GC = FP8 ? 2 : 1;   // GC: chunks under one scale
+  for (int i = threadIdx.x; i < (int)(sizeof(FewTables) / 4); i += kDownWaves * kWave)
+    reinterpret_cast<uint32_t*>(&sh.tb)[i] = reinterpret_cast<const uint32_t*>(a.tables)[i];
+  __syncthreads();
+  DN d;
   d.w2 = static_cast<const uint8_t*>(a.w2) + (size_t)c0 * I * kSize;
-  d.hw = a.hw;
-  d.plane = a.plane;
-  d.zero_row = a.T * (a.k + a.ns);
+  d.s2 = a.s2;
+  d.h = reinterpret_cast<const uint16_t*>(a.hw);
   d.expert = (size_t)H * I * kSize;
+  d.plane = 2 * (size_t)a.plane;
+  d.tile = 16 * I * kSize;
   d.wl = PW ? 16 * lane : WC::lane_offset(lane % 16, I, lane / 16);
   d.I = I;
+  d.H = H;
+  d.c0 = c0;
+  d.zero_row = a.T * (a.k + a.ns);
   d.cpe = I / (32 * WC::kSteps);
-  d.acc = d.part = floatx4{0.f, 0.f, 0.f, 0.f};
-  const int n = tb->n_act * (d.cpe / GC);
-  const int s0 = n * wave / kWaves * GC, s1 = n * (wave + 1) / kWaves * GC;
-  int ai = s0 / d.cpe, q = s0 - ai * d.cpe;
-  d.ai = ai;
-  d.q = q;
-  uint8_t* mine = ring + wave * kRing;
-  auto run = [&](auto set, auto tail, int s) {
-    constexpr int SET = decltype(set)::value, LAST = (SET + DD::kAhead) % S;
-    constexpr bool TAIL = decltype(tail)::value;
-    if (TAIL && s >= s1) return;
-    wait_loads<63>();   // the reads of the chunk that is loaded over
-    float sc = 0.f;
-    if constexpr (FP8) {
-      const int e = __builtin_amdgcn_readfirstlane(tb->act[ai]);
-      sc = a.s2[((size_t)e * (H / 128) + c0 / 128) * (I / 128) + q / 2];
-    }
-    if (!TAIL || s + DD::kAhead < s1) d.template issue<LAST>(mine + LAST * 1024, tb, lane);
-    if constexpr (TAIL) wait_loads<0>();
-    else wait_loads<DD::kAhead * DD::kLoads>();
-    d.template multiply<SET>(mine + SET * 1024, lane, q % 2 == 1, sc);
-    if (++q == d.cpe) q = 0, ++ai;
-  };
-  using F = std::false_type;
-  using Y = std::true_type;
-  if (s0 + 0 < s1) d.template issue<0>(mine, tb, lane);
-  if (s0 + 1 < s1) d.template issue<1>(mine + 1024, tb, lane);
-  if constexpr (DD::kAhead > 2)
-    if (s0 + 2 < s1) d.template issue<2>(mine + 2048, tb, lane);
-  if (threadIdx.x == 0) next = take_ticket(a.ticket);
-  int s = s0;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) d.acc[nt] = d.part[nt] = floatx4{0.f, 0.f, 0.f, 0.f};
+  const int n = __builtin_amdgcn_readfirstlane(sh.tb.n_act) * (d.cpe / GC);
+  const int s0 = n * wave / kDownWaves * GC, s1 = n * (wave + 1) / kDownWaves * GC;
+  uint8_t* mine = sh.ring[wave];
+  if (s0 < s1) {
+    d.ai = s0 / d.cpe;
+    d.q = s0 - d.ai * d.cpe;
+    d.left = s1 - s0 - 1;
+    d.enter(&sh.tb, lane);
+#pragma unroll
+    for (int i = 0; i < DN::kAhead; ++i) d.issue(mine + i * DN::kEntry, &sh.tb, lane, i);
+    // whole rounds of the sets, then the rest, which is all loaded
+    int s = s0;
 #pragma unroll 1
-  for (; s + S + DD::kAhead <= s1; s += S) {
-    run(std::integral_constant<int, 0>(), F(), s);
-    run(std::integral_constant<int, 1>(), F(), s + 1);
-    run(std::integral_constant<int, 2>(), F(), s + 2);
-    if constexpr (S > 3) run(std::integral_constant<int, S - 1>(), F(), s + 3);
+    for (; s + DN::kSets <= s1; s += DN::kSets)
+#pragma unroll
+      for (int i = 0; i < DN::kSets; ++i) d.template run<true>(mine, &sh.tb, lane, i);
+    wait_loads<0>();
+#pragma unroll
+    for (int i = 0; i < DN::kAhead; ++i)
+      if (s + i < s1) d.template run<false>(mine, &sh.tb, lane, i);
   }
-#pragma unroll 1
-  for (; s < s1; s += S) {
-    run(std::integral_constant<int, 0>(), Y(), s);
-    run(std::integral_constant<int, 1>(), Y(), s + 1);
-    run(std::integral_constant<int, 2>(), Y(), s + 2);
-    if constexpr (S > 3) run(std::integral_constant<int, S - 1>(), Y(), s + 3);
+  floatx4* red = reinterpret_cast<floatx4*>(mine);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) red[nt * kWave + lane] = d.acc[nt];
+  __syncthreads();
+  const int c = threadIdx.x % (16 * NT), t = threadIdx.x / (16 * NT);
+  if (t < a.T) {
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kDownWaves; ++w)
+      sum += reinterpret_cast<const floatx4*>(sh.ring[w])[c / 16 * kWave + (c % 16) / 4 * 16 + t][c % 4];
+    a.out[(size_t)t * H + c0 + c] = sh.tb.bad[t] ? 0x7fc0u : f32_to_bf16_bits(sum);
   }
-  const floatx4 acc[1] = {d.acc};
-  store_out<false, 1>(a, tb, ring, c0, acc);
 }
 
 template <bool FP8, bool PW, bool STAGED>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4)))
 void few_experts_kernel(FewArgs a) {
-  constexpr int kDnCols = few_down_cols(STAGED);
-  static_assert(kThreads >= kRows * kDnCols, "one output per thread");
+  static_assert(kThreads >= kRows * kDownCols, "one output per thread");
   __shared__ FewShared<STAGED> sh;
   few_route<STAGED>(a, sh.tb, sh.stage, sh.tk);
+  if (!STAGED && blockIdx.x == 0)
+    for (int i = threadIdx.x; i < (int)(sizeof(FewTables) / 4); i += kThreads)
+      reinterpret_cast<uint32_t*>(a.tables)[i] = reinterpret_cast<const uint32_t*>(&sh.tb)[i];
   constexpr int kCols = few_cols(FP8);
-  const int n_cg = a.I / kCols, n_gu = sh.tb.n_act * n_cg, n_all = n_gu + a.H / kDnCols;
+  const int n_cg = a.I / kCols, n_gu = __builtin_amdgcn_readfirstlane(sh.tb.n_act) * n_cg;
+  const int n_all = n_gu + (STAGED ? a.H / kDownCols : 0);
   int tk = __builtin_amdgcn_readfirstlane(sh.tk);
   bool h_staged = false;   // the stage holds h' in place of the token rows (tickets grow)
   while (tk < n_all) {
@@ -809,11 +829,9 @@ void few_experts_kernel(FewArgs a) {
       gate_up_unit<FP8, PW, STAGED>(a, &sh.tb, sh.stage, &sh.ring[0][0],
                                     __builtin_amdgcn_readfirstlane(sh.tb.act[ai]),
                                     (tk - ai * n_cg) * kCols, next);
-    } else {
-      const int c0 = (tk - n_gu) * kDnCols;
-      if constexpr (STAGED)
-        down_unit_staged<FP8, PW>(a, &sh.tb, sh.stage, &sh.ring[0][0], h_staged, c0, next);
-      else down_unit<FP8, PW>(a, &sh.tb, &sh.ring[0][0], c0, next);
+    } else if constexpr (STAGED) {
+      down_unit_staged<FP8, PW>(a, &sh.tb, sh.stage, &sh.ring[0][0], h_staged, (tk - n_gu) * kDownCols,
+                                next);
       h_staged = true;
     }
     if (threadIdx.x == 0) sh.tk = next;
@@ -826,37 +844,48 @@ void few_experts_kernel(FewArgs a) {
 
 hipError_t launch_few(int wkind, bool packed, const void* x, const uint8_t* valid, const void* R,
                       const void* w13, const void* w2, const float* s13, const float* s2,
-                      float* part, uint32_t* hw, int32_t* ticket, void* out, int T, int H, int I,
-                      int E, int n_shared, int k, hipStream_t s) {
+                      float* part, uint32_t* hw, int32_t* ticket, void* tables, void* out, int T,
+                      int H, int I, int E, int n_shared, int k, hipStream_t s) {
   if (wkind == W_F32 || T < 1 || T > kFewRows || E + n_shared > kMaxSeg || k > kMaxTopk ||
       H % 128 != 0 || I % 32 != 0 || (long long)H * I >= kMaxFewArea || (wkind == W_FP8 && I % 128 != 0))
     return hipErrorInvalidValue;
   const int rows = T * (k + n_shared);
-  hipLaunchKernelGGL(few_logits_kernel, dim3((E + 15) / 16, kFewLogitParts), dim3(kThreads), 0, s,
-                     static_cast<const uint16_t*>(x), valid, static_cast<const uint16_t*>(R), part,
-                     hw, rows, I, ticket, T, H, E);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
-  const FewArgs a{static_cast<const uint16_t*>(x), valid, w13, w2, s13, s2, part, hw, (uint32_t)(rows + 1) * (I / 2), ticket,
-                  static_cast<uint16_t*>(out), T, H, I, E, n_shared, k};
   // rows and h' in LDS where they fit
   const bool staged = (long long)T * (2 * H + kPad) + 16 <= FewShared<true>::kStage &&
-                      (long long)T * (k + n_shared) * (4LL * I + kPad) + 16 <= FewShared<true>::kStage;
+                      rows * (4LL * I + kPad) + 16 <= FewShared<true>::kStage;
+  hipLaunchKernelGGL(few_logits_kernel, dim3((E + 15) / 16, kFewLogitParts), dim3(kThreads), 0, s,
+                     static_cast<const uint16_t*>(x), valid, static_cast<const uint16_t*>(R), part,
+                     hw, rows, I, staged, ticket, T, H, E);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  const FewArgs a{static_cast<const uint16_t*>(x), valid, w13, w2, s13, s2, part, hw,
+                  (uint32_t)(rows + 1) * (I / 2), ticket, static_cast<FewTables*>(tables),
+                  static_cast<uint16_t*>(out), T, H, I, E, n_shared, k};
   // A block for every gate/up unit, so that they all run at once, from one to
   // two a CU; blocks loop over the tickets.
   const long long n_gu = (long long)(std::min(E, T * k) + n_shared) * (I / few_cols(wkind == W_FP8));
-  const long long units = n_gu + H / few_down_cols(staged);
+  const long long units = n_gu + (staged ? H / kDownCols : 0);
   const dim3 grid((unsigned)std::min(units, std::max(256LL, std::min(n_gu, 512LL))));
+  // The down launch: 32 columns a block, or 16 if that gives fewer rounds of
+  // 256 blocks (one a CU) for its columns.
+  const bool narrow = (H / 16 + 255) / 256 < (H / 32 + 255) / 256 * 2;
+#define MOE_DOWN(F, P, N)                                                                     \
+  hipLaunchKernelGGL((few_down_kernel<F, P, N>), dim3(H / (16 * N)), dim3(kDownWaves * kWave), 0, s, a)
 #define MOE_FEW(F, P)                                                                         \
-  if (staged)                                                                                 \
+  if (staged) {                                                                               \
     hipLaunchKernelGGL((few_experts_kernel<F, P, true>), grid, dim3(kThreads), 0, s, a);      \
-  else                                                                                        \
-    hipLaunchKernelGGL((few_experts_kernel<F, P, false>), grid, dim3(kThreads), 0, s, a)
+  } else {                                                                                    \
+    hipLaunchKernelGGL((few_experts_kernel<F, P, false>), grid, dim3(kThreads), 0, s, a);     \
+    if ((err = hipGetLastError()) != hipSuccess) return err;                                  \
+    if (narrow) MOE_DOWN(F, P, 1);                                                            \
+    else MOE_DOWN(F, P, 2);                                                                   \
+  }
   if (wkind == W_FP8) {
     if (packed) { MOE_FEW(true, true); } else { MOE_FEW(true, false); }
   } else {
     if (packed) { MOE_FEW(false, true); } else { MOE_FEW(false, false); }
   }
+#undef MOE_DOWN
 #undef MOE_FEW
   return hipGetLastError();
 }

@@ -227,7 +227,7 @@ int make_plan(const moe_desc* d, int32_t topk, Plan* p) {
 
 // Workspace layout of one moe_forward_few call.
 struct FewPlan {
-  size_t off_part, off_hw, off_ticket, total;
+  size_t off_part, off_hw, off_ticket, off_tables, total;
 };
 
 static_assert(MOE_FEW_MAX_ROWS == moe::kFewRows, "row limit");
@@ -243,6 +243,7 @@ int make_few_plan(const moe_desc* d, int32_t topk, FewPlan* p) {
   p->off_part = take((size_t)moe::kFewLogitParts * d->T * moe::few_logit_stride(d->E) * 4);
   p->off_hw = take(((size_t)d->T * (topk + d->n_shared) + 1) * d->I * 4);
   p->off_ticket = take(4);
+  p->off_tables = take(moe::kFewTableBytes);
   p->total = o;
   return MOE_OK;
 }
@@ -680,8 +681,8 @@ int moe_forward_few(const moe_desc* desc, const void* x, const uint8_t* valid_ro
   if (moe::launch_few(desc->w_dtype == MOE_BF16 ? moe::W_BF16 : moe::W_FP8,
                       desc->w_layout == MOE_LAYOUT_FRAG16, x, valid_rows, router_w, w13, w2,
                       desc->w13_scale, desc->w2_scale, at<float>(workspace, p.off_part),
-                      at<uint32_t>(workspace, p.off_hw), at<int32_t>(workspace, p.off_ticket), out,
-                      desc->T, desc->H, desc->I, desc->E, desc->n_shared, topk, s) != hipSuccess)
+                      at<uint32_t>(workspace, p.off_hw), at<int32_t>(workspace, p.off_ticket),
+                      at<void>(workspace, p.off_tables), out, desc->T, desc->H, desc->I, desc->E, desc->n_shared, topk, s) != hipSuccess)
     return MOE_ERR_HIP;
   return MOE_OK;
 }

@@ -204,17 +204,19 @@ hipError_t launch_zero_i32(int32_t* a, size_t na, int32_t* b, size_t nb, hipStre
 
 // ---- few token rows ----------------------------------------------------------
 constexpr int kFewRows = 16;        // most rows of a call
+constexpr size_t kFewTableBytes = 16 * 1024;   // of the tables a launch leaves to the next
 constexpr int kFewLogitParts = 4;   // K parts of the router logits
 inline constexpr int few_logit_stride(int E) { return (E + 63) / 64 * 64; }
 constexpr long long kMaxFewArea = 1LL << 30;   // H I below it: 32-bit offsets inside an expert
 // The whole layer for T <= kFewRows rows, bf16 activations, bf16 or fp8
-// weights, in two launches.  part: [kFewLogitParts][T][few_logit_stride(E)] fp32, 16-byte aligned; hw: (T (k +
-// n_shared) + 1) I words, 16-byte aligned; ticket: one int32.  None of them
-// needs to hold anything on entry.
+// weights, in two or three launches.  part: [kFewLogitParts][T]
+// [few_logit_stride(E)] fp32; hw: (T (k + n_shared) + 1) I words; tables:
+// kFewTableBytes; ticket: one int32; all 16-byte aligned.  None of them needs
+// to hold anything on entry.
 hipError_t launch_few(int wkind, bool packed, const void* x, const uint8_t* valid, const void* R,
                       const void* w13, const void* w2, const float* s13, const float* s2,
-                      float* part, uint32_t* hw, int32_t* ticket, void* out, int T, int H, int I,
-                      int E, int n_shared, int k, hipStream_t s);
+                      float* part, uint32_t* hw, int32_t* ticket, void* tables, void* out, int T,
+                      int H, int I, int E, int n_shared, int k, hipStream_t s);
 
 // ---- fp8 block-scale product and token quantisation ----------------------------
 // out[M, N] = a[M, K] b[N, K]^T, e4m3 codes, scales sa [M][ceil(K / 128)],
