@@ -100,33 +100,45 @@ __global__ __launch_bounds__(kThreads) void few_logits_kernel(
   }
 }
 
-// Weights by way of LDS: chunks of 1 KB, 16 bytes a lane, that hold a 16-row
-// tile's next kSteps MFMA steps (bf16 one, fp8 two).
-template <bool FP8, bool PW>
+// Weights by way of LDS, 16 bytes a lane at a time: chunks of kParts KB that
+// hold a 16-row tile's next kSteps MFMA steps (packed and fp8 rows 1 KB, bf16
+// one step, fp8 two).  WIDE, for bf16 rows: 2 KB, 128 bytes = a whole line of
+// every row, the two halves of a line would be asked for twice (16 rows' gate/up
+// launch YY us in place of ZZ).
+template <bool FP8, bool PW, bool WIDE = false>
 struct WChunk {
-  static constexpr int kSteps = FP8 ? 2 : 1;
-  static constexpr int kBytes = PW ? 1024 : 64;   // from one chunk of a tile to the next
+  static_assert(!WIDE || !(FP8 || PW), "for bf16 rows");
+  static constexpr int kSteps = FP8 || WIDE ? 2 : 1, kParts = WIDE ? 2 : 1;
+  static constexpr int kBytes = PW ? 1024 : 64 * kParts;   // from one chunk of a tile to the next
   // K of the lane's first value of step u
   static __device__ __forceinline__ int k_of(int u, int g) {
     return FP8 && !PW ? 16 * g + 8 * u : 32 * u + 8 * g;
   }
-  // byte offset of lane (g, r)'s share behind the tile
-  static __device__ __forceinline__ uint32_t lane_offset(int r, int K, int g) {
-    return PW ? (FP8 ? 256 * g + 16 * r : (16 * g + r) * 16) : r * (K * (FP8 ? 1 : 2)) + 16 * g;
+  // The row whose share the lane loads (WIDE: of 8 rows), and the byte offset
+  // of that share behind the row (packed: behind the tile).  WIDE: piece p of
+  // row r takes the place of piece p ^ r % 8, so that the lanes of a step read
+  // all banks.
+  static __device__ __forceinline__ int load_row(int lane) { return WIDE ? lane / 8 : lane % 16; }
+  static __device__ __forceinline__ uint32_t load_offset(int lane) {
+    return WIDE ? 16 * (lane % 8 ^ lane / 8) : PW ? 16 * lane : 16 * (lane / 16);
   }
   static __device__ __forceinline__ bf16x8 get(const uint8_t* chunk, int u, int lane) {
     if constexpr (FP8) {
       const u32x2 v = ld8(chunk + (PW ? 512 * u + 8 * lane : 16 * lane + 8 * u));
       return fp8x8_to_bf16x8(v[0], v[1]);
+    } else if constexpr (WIDE) {
+      return as_bf16x8(ld16(chunk + 128 * (lane % 16) + 16 * ((4 * u + lane / 16) ^ lane % 8)));
     } else {
       return as_bf16x8(ld16(chunk + 16 * lane));
     }
   }
 };
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, -1, 0x00020000);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p, int bytes = -1) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);
 }
+// An offset behind the end of every buffer of less than 2 GB: loads give 0.
+constexpr uint32_t kNowhere = 0x80000000u;
 
 // 16 bytes a lane from buffer + lane_offset + offset straight to dst + 16 lane;
 // NT: data that no other block reads.
@@ -334,59 +346,82 @@ __device__ __forceinline__ void few_route(const FewArgs& a, FewTables& tb, uint8
 // h columns of a gate/up unit.
 constexpr int few_cols(bool fp8) { return fp8 ? 16 : 8; }
 
-// A gate/up unit's loads and sums of one wave.
+// A gate/up unit's loads and sums of one wave: weights by way of LDS, token
+// rows in LDS (STAGED) or registers, kAhead chunks ahead.
 template <bool FP8, bool PW, bool STAGED>
 struct GateUp {
-  using WC = WChunk<FP8, PW>;
-  static constexpr int NT = FP8 ? 2 : 1, XN = STAGED ? 0 : WC::kSteps;
-  static constexpr int kLoads = NT + XN, kEntry = 1024 * kLoads;
-  static constexpr int kEntries = FewShared<STAGED>::kRing / kEntry, kAhead = kEntries - 1;
+  using WC = WChunk<FP8, PW, !FP8 && !PW>;
+  static constexpr int NT = FP8 ? 2 : 1;
+  static constexpr int kLoads = NT * WC::kParts, kEntry = 1024 * kLoads;   // of a chunk's weights
+  static constexpr int kSets = FewShared<STAGED>::kRing / kEntry, kAhead = kSets - 1;
+  static constexpr int kXSets = STAGED ? 1 : kSets;
   __amdgpu_buffer_rsrc_t wbuf[NT], xbuf;
-  uint32_t wl, xl[2];
+  uint32_t wl[WC::kParts], xl[WC::kSteps];
+  const float* sp[NT];
   floatx4 acc[NT], part[NT];
+  u32x4 x[kXSets][WC::kSteps];
+  float sc[kXSets][NT];
 
-  __device__ __forceinline__ void issue(uint8_t* __restrict__ to, int c) const {
+  // Chunk c's weights to `to` and, not STAGED, the rest to set `set`.
+  __device__ __forceinline__ void issue(uint8_t* __restrict__ to, int c, int set) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) to_lds16<PW>(wbuf[n], wl, c * WC::kBytes, to + 1024 * n);
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int u = 0; u < XN; ++u)
-      to_lds16<false>(xbuf, xl[u], c * (64 * WC::kSteps), to + 1024 * (NT + u));
+      for (int p = 0; p < WC::kParts; ++p)
+        to_lds16<PW>(wbuf[n], wl[p], c * WC::kBytes, to + 1024 * (n * WC::kParts + p));
+    if constexpr (!STAGED) {
+#pragma unroll
+      for (int u = 0; u < WC::kSteps; ++u)
+        x[set][u] = __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(xbuf, xl[u], c * (64 * WC::kSteps), 0));
+      if constexpr (FP8)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) sc[set][n] = sp[n][c / 2];
+    }
   }
-
-  // Chunk c out of `cur`, chunk c + kAhead (if there is one) into `next`.
-  __device__ __forceinline__ void step(const uint8_t* __restrict__ cur, uint8_t* __restrict__ next,
-                                       const uint8_t* __restrict__ xs, int c, int c1, bool xv, int lane,
-                                       const float* __restrict__ const (&sp)[NT]) {
-    if (c + kAhead < c1) issue(next, c + kAhead);
-    const int g = lane / 16;
-    float sc[NT];
-    if constexpr (FP8)
+  // The sums of the chunk in `cur`, x and scales in set `set`; `second`: the
+  // second half of a 128-wide block.
+  __device__ __forceinline__ void multiply(const uint8_t* __restrict__ cur, int lane, int set, bool second) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) sc[n] = sp[n][c / 2];
-#pragma unroll
-    for (int u = 0; u < WC::kSteps; ++u) {
-      u32x4 x;
-      if constexpr (STAGED) x = ld16(xs + (xv ? 2 * (c * 32 * WC::kSteps + WC::k_of(u, g)) : 0));
-      else {
-        x = ld16(cur + 1024 * (NT + u) + 16 * lane);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = xv ? x[i] : 0u;
-      }
+    for (int u = 0; u < WC::kSteps; ++u)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         floatx4& d = FP8 ? part[n] : acc[n];
-        d = mfma16x16x32(WC::get(cur + 1024 * n, u, lane), as_bf16x8(x), d);
+        d = mfma16x16x32(WC::get(cur + 1024 * n, u, lane), as_bf16x8(x[set][u]), d);
       }
-    }
-    // fp8: the second half of a 128-wide block
-    if (FP8 && c % 2 == 1)
+    if (FP8 && second)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          acc[n][i] = fmaf(sc[n], part[n][i], acc[n][i]);
+          acc[n][i] = fmaf(sc[set][n], part[n][i], acc[n][i]);
           part[n][i] = 0.f;
         }
+  }
+  // STAGED: chunk c out of `cur`, chunk c + kAhead (if there is one) into `next`.
+  __device__ __forceinline__ void step_staged(const uint8_t* __restrict__ cur, uint8_t* __restrict__ next,
+                                              const uint8_t* __restrict__ xs, int c, int c1, bool xv,
+                                              int lane) {
+    if (c + kAhead < c1) issue(next, c + kAhead, 0);
+    if constexpr (FP8)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) sc[0][n] = sp[n][c / 2];
+#pragma unroll
+    for (int u = 0; u < WC::kSteps; ++u)
+      x[0][u] = ld16(xs + (xv ? 2 * (c * 32 * WC::kSteps + WC::k_of(u, lane / 16)) : 0));
+    multiply(cur, lane, 0, c % 2 == 1);
+  }
+  // Not STAGED: set i's chunk in its place in the wave's ring; LOAD: chunk c
+  // takes the place of the one before it.
+  template <bool LOAD>
+  __device__ __forceinline__ void step(const uint8_t* __restrict__ cur, uint8_t* __restrict__ to, int i,
+                                       int c, int lane) {
+    if constexpr (LOAD) {
+      wait_loads<63>();   // the reads of the chunk that is loaded over
+      issue(to, c, (i + kAhead) % kSets);
+      wait_loads<kAhead * (kLoads + WC::kSteps)>();
+    }
+    multiply(cur, lane, i, i % 2 == 1);
   }
 };
 
@@ -408,40 +443,66 @@ __device__ __forceinline__ void gate_up_unit(const FewArgs& a, const FewTables* 
   const int H = a.H, I = a.I;
   constexpr int kSize = FP8 ? 1 : 2;
   GU gu;
-  const float* sp[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     gu.wbuf[n] = buffer_at(static_cast<const uint8_t*>(a.w13) +
                            ((size_t)e * 2 * I + n * I + c0 / 16 * 16) * H * kSize);
-    sp[n] = FP8 ? a.s13 + ((size_t)e * (2 * I / 128) + (n * I + c0) / 128) * (H / 128) : nullptr;
+    gu.sp[n] = FP8 ? a.s13 + ((size_t)e * (2 * I / 128) + (n * I + c0) / 128) * (H / 128) : nullptr;
     gu.acc[n] = gu.part[n] = floatx4{0.f, 0.f, 0.f, 0.f};
   }
-  // bf16: lanes 8 .. 15 of a group have the up rows, I rows on
-  if constexpr (FP8) gu.wl = PW ? 16 * lane : WC::lane_offset(m, H, g);
-  else gu.wl = WC::lane_offset(c0 % 16 + m % 8, H, g) + (m >= 8 ? (uint32_t)I * H * kSize : 0u);
-  const bool xv = tb->slot[e][m] >= 0;
-  // (rows past T: row 0 again, not used)
-  gu.xbuf = buffer_at(a.x);
+  // bf16: the tile's rows 8 .. 15 are the up rows, I rows on
+  const uint32_t up_rows = (uint32_t)I * H * kSize;
+  const int lr = WC::load_row(lane);
 #pragma unroll
-  for (int u = 0; u < 2; ++u) gu.xl[u] = 2 * ((xv ? m : 0) * H + WC::k_of(u, g));
+  for (int p = 0; p < WC::kParts; ++p) {
+    if constexpr (FP8) gu.wl[p] = WC::load_offset(lane) + (PW ? 0 : lr * H * kSize);
+    else if constexpr (PW)   // lane (g, r)'s share lies at 256 g + 16 r
+      gu.wl[p] = 256 * g + 16 * (c0 % 16 + m % 8) + (m >= 8 ? up_rows : 0u);
+    else gu.wl[p] = WC::load_offset(lane) + (c0 % 16 + lr) * H * kSize + p * up_rows;
+  }
+  const bool xv = tb->slot[e][m] >= 0;
+  // rows that did not choose e: zeros
+  gu.xbuf = buffer_at(a.x, 2 * a.T * H);
+#pragma unroll
+  for (int u = 0; u < WC::kSteps; ++u) gu.xl[u] = xv ? 2 * (m * H + WC::k_of(u, g)) : kNowhere;
   // staged rows: a lane without one reads the 16 zero bytes behind them
   const uint8_t* xl = xs + (xv ? m * (2 * H + kPad) : a.T * (2 * H + kPad));
   // (rounded so that wave 0, which takes the tickets, has a block)
   const int nb = H / 128, cpb = 4 / WC::kSteps;
   const int s0 = (nb * wave + kWaves - 1) / kWaves * cpb, s1 = (nb * (wave + 1) + kWaves - 1) / kWaves * cpb;
   uint8_t* mine = ring + wave * kRing;
+  if constexpr (STAGED) {
 #pragma unroll
-  for (int i = 0; i < GU::kAhead; ++i)
-    if (s0 + i < s1) gu.issue(mine + i * GU::kEntry, s0 + i);
-  if (threadIdx.x == 0) next = take_ticket(a.ticket);
-  int at = 0;
+    for (int i = 0; i < GU::kAhead; ++i)
+      if (s0 + i < s1) gu.issue(mine + i * GU::kEntry, s0 + i, 0);
+    if (threadIdx.x == 0) next = take_ticket(a.ticket);
+    int at = 0;
 #pragma unroll 1
-  for (int c = s0; c < s1; ++c) {
-    if (c + GU::kAhead <= s1) wait_loads<(GU::kAhead - 1) * GU::kLoads>();
-    else wait_loads<0>();
-    const int to = at == 0 ? GU::kEntries - 1 : at - 1;
-    gu.step(mine + at * GU::kEntry, mine + to * GU::kEntry, xl, c, s1, xv, lane, sp);
-    at = at + 1 == GU::kEntries ? 0 : at + 1;
+    for (int c = s0; c < s1; ++c) {
+      if (c + GU::kAhead <= s1) wait_loads<(GU::kAhead - 1) * GU::kLoads>();
+      else wait_loads<0>();
+      const int to = at == 0 ? GU::kSets - 1 : at - 1;
+      gu.step_staged(mine + at * GU::kEntry, mine + to * GU::kEntry, xl, c, s1, xv, lane);
+      at = at + 1 == GU::kSets ? 0 : at + 1;
+    }
+  } else if (s0 < s1) {
+    // (behind the last chunk that one again, unused, so that as many loads are
+    // on the way at every step)
+#pragma unroll
+    for (int i = 0; i < GU::kAhead; ++i) gu.issue(mine + i * GU::kEntry, min(s0 + i, s1 - 1), i);
+    if (threadIdx.x == 0) next = take_ticket(a.ticket);
+    int c = s0;
+#pragma unroll 1
+    for (; c + GU::kSets <= s1; c += GU::kSets)
+#pragma unroll
+      for (int i = 0; i < GU::kSets; ++i)
+        gu.template step<true>(mine + i * GU::kEntry,
+                               mine + (i + GU::kAhead) % GU::kSets * GU::kEntry, i,
+                               min(c + i + GU::kAhead, s1 - 1), lane);
+    wait_loads<0>();
+#pragma unroll
+    for (int i = 0; i < GU::kAhead; ++i)
+      if (c + i < s1) gu.template step<false>(mine + i * GU::kEntry, nullptr, i, 0, lane);
   }
   floatx4* red = reinterpret_cast<floatx4*>(mine);
 #pragma unroll
@@ -613,7 +674,7 @@ __device__ __forceinline__ void down_unit_staged(const FewArgs& a, const FewTabl
   d.w2 = static_cast<const uint8_t*>(a.w2) + (size_t)c0 * I * kSize;
   d.expert = (size_t)H * I * kSize;
   d.tile = 16 * I * kSize;
-  d.wl = PW ? 16 * lane : WC::lane_offset(lane % 16, I, lane / 16);
+  d.wl = WC::load_offset(lane) + (PW ? 0 : WC::load_row(lane) * I * kSize);
   d.cpe = I / (32 * WC::kSteps);
   d.row_bytes = 4 * I + kPad;
   d.zeros = a.T * (a.k + a.ns) * d.row_bytes;
@@ -764,7 +825,7 @@ __global__ __launch_bounds__(kDownWaves * kWave) void few_down_kernel(FewArgs a)
   d.expert = (size_t)H * I * kSize;
   d.plane = 2 * (size_t)a.plane;
   d.tile = 16 * I * kSize;
-  d.wl = PW ? 16 * lane : WC::lane_offset(lane % 16, I, lane / 16);
+  d.wl = WC::load_offset(lane) + (PW ? 0 : WC::load_row(lane) * I * kSize);
   d.I = I;
   d.H = H;
   d.c0 = c0;
