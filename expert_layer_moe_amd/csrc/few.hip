@@ -104,7 +104,7 @@ __global__ __launch_bounds__(kThreads) void few_logits_kernel(
 // hold a 16-row tile's next kSteps MFMA steps (packed and fp8 rows 1 KB, bf16
 // one step, fp8 two).  WIDE, for bf16 rows: 2 KB, 128 bytes = a whole line of
 // every row, the two halves of a line would be asked for twice (16 rows' gate/up
-// launch YY us in place of ZZ).
+// launch 137 us in place of 168).
 template <bool FP8, bool PW, bool WIDE = false>
 struct WChunk {
   static_assert(!WIDE || !(FP8 || PW), "for bf16 rows");
@@ -713,11 +713,13 @@ __device__ __forceinline__ void down_unit_staged(const FewArgs& a, const FewTabl
 //
 // A wave's loads and sums: NT tiles of 16 columns, W2 by way of LDS, h' in
 // registers, both kAhead chunks ahead.
-template <bool FP8, bool PW, int NT>
+template <bool FP8, bool PW, int NT, bool WIDE>
 struct Down {
-  using WC = WChunk<FP8, PW>;
-  static constexpr int kEntry = 1024 * NT, kSets = FP8 || NT == 2 ? 4 : 8, kAhead = kSets - 1;
-  static constexpr int kLoads = NT + 2 * WC::kSteps;   // of a chunk
+  using WC = WChunk<FP8, PW, WIDE>;
+  static constexpr int kEntry = 1024 * NT * WC::kParts;
+  static constexpr int kWaves = WIDE ? 12 : 16;   // of a block
+  static constexpr int kSets = WIDE ? 5 - NT : FP8 ? 4 : 8 / NT, kAhead = kSets - 1;
+  static constexpr int kLoads = NT * WC::kParts + 2 * WC::kSteps;   // of a chunk
   const uint8_t* w2;      // row c0 of expert 0
   const float* s2;
   const uint16_t* h;
@@ -746,7 +748,11 @@ struct Down {
                                         int lane, int set) {
     const __amdgpu_buffer_rsrc_t buf = buffer_at(w2 + e * expert);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) to_lds16<PW>(buf, wl, nt * tile + q * WC::kBytes, to + 1024 * nt);
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int p = 0; p < WC::kParts; ++p)
+        to_lds16<PW>(buf, wl, nt * tile + p * (tile / 2) + q * WC::kBytes,
+                     to + 1024 * (nt * WC::kParts + p));
 #pragma unroll
     for (int u = 0; u < WC::kSteps; ++u) {
       const uint16_t* p = hrow + q * 32 * WC::kSteps + WC::k_of(u, lane / 16);
@@ -777,7 +783,7 @@ struct Down {
     for (int u = 0; u < WC::kSteps; ++u)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const bf16x8 w = WC::get(cur + 1024 * nt, u, lane);
+        const bf16x8 w = WC::get(cur + 1024 * WC::kParts * nt, u, lane);
         floatx4& d = FP8 ? part[nt] : acc[nt];
         d = mfma16x16x32(w, as_bf16x8(hi[set][u]), d);
         d = mfma16x16x32(w, as_bf16x8(lo[set][u]), d);
@@ -799,19 +805,20 @@ struct Down {
   }
 };
 
-constexpr int kDownWaves = 16;
+template <class DN>
 struct DownShared {
   FewTables tb;
-  __attribute__((aligned(16))) uint8_t ring[kDownWaves][8 * 1024];
+  __attribute__((aligned(16))) uint8_t ring[DN::kWaves][DN::kSets * DN::kEntry];
 };
 static_assert(sizeof(FewTables) % 4 == 0 && sizeof(FewTables) <= kFewTableBytes, "copied by words");
 
 // out[t][c0 .. c0 + 16 NT - 1] for every row: as down_unit_staged, by 16 waves.
-template <bool FP8, bool PW, int NT>
-__global__ __launch_bounds__(kDownWaves * kWave) void few_down_kernel(FewArgs a) {
-  using DN = Down<FP8, PW, NT>;
+template <bool FP8, bool PW, int NT, bool WIDE>
+__global__ __launch_bounds__((Down<FP8, PW, NT, WIDE>::kWaves * kWave)) void few_down_kernel(FewArgs a) {
+  using DN = Down<FP8, PW, NT, WIDE>;
   using WC = typename DN::WC;
-  __shared__ DownShared sh;
+  constexpr int kDownWaves = DN::kWaves;
+  __shared__ DownShared<DN> sh;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const int H = a.H, I = a.I, c0 = blockIdx.x * 16 * NT;
   constexpr int kSize = FP8 ? 1 : 2, GC = FP8 ? 2 : 1;   // GC: chunks under one scale
@@ -930,16 +937,22 @@ hipError_t launch_few(int wkind, bool packed, const void* x, const uint8_t* vali
   // The down launch: 32 columns a block, or 16 if that gives fewer rounds of
   // 256 blocks (one a CU) for its columns.
   const bool narrow = (H / 16 + 255) / 256 < (H / 32 + 255) / 256 * 2;
-#define MOE_DOWN(F, P, N)                                                                     \
-  hipLaunchKernelGGL((few_down_kernel<F, P, N>), dim3(H / (16 * N)), dim3(kDownWaves * kWave), 0, s, a)
+#define MOE_DOWN(F, P, N, W)                                                                  \
+  hipLaunchKernelGGL((few_down_kernel<F, P, N, W>), dim3(H / (16 * N)),                       \
+                     dim3(Down<F, P, N, W>::kWaves * kWave), 0, s, a)
 #define MOE_FEW(F, P)                                                                         \
   if (staged) {                                                                               \
     hipLaunchKernelGGL((few_experts_kernel<F, P, true>), grid, dim3(kThreads), 0, s, a);      \
   } else {                                                                                    \
     hipLaunchKernelGGL((few_experts_kernel<F, P, false>), grid, dim3(kThreads), 0, s, a);     \
     if ((err = hipGetLastError()) != hipSuccess) return err;                                  \
-    if (narrow) MOE_DOWN(F, P, 1);                                                            \
-    else MOE_DOWN(F, P, 2);                                                                   \
+    if (narrow) {                                                                             \
+      if (F || P || I % 64 != 0) MOE_DOWN(F, P, 1, false);                                    \
+      else MOE_DOWN(F, P, 1, (!F && !P));                                                     \
+    } else {                                                                                  \
+      if (F || P || I % 64 != 0) MOE_DOWN(F, P, 2, false);                                    \
+      else MOE_DOWN(F, P, 2, (!F && !P));                                                     \
+    }                                                                                         \
   }
   if (wkind == W_FP8) {
     if (packed) { MOE_FEW(true, true); } else { MOE_FEW(true, false); }
