@@ -728,6 +728,7 @@ int quant_rows(const moe_quant_desc* d, const void* in, void* codes, float* scal
       (st = check_stride(d->ld_codes, d->cols, 16)) != MOE_OK ||
       (st = check_stride(d->ld_scales, nb, 1)) != MOE_OK)
     return st;
+  if ((int64_t)d->rows * nb > moe::kMaxQuantBlocks) return MOE_ERR_UNSUPPORTED;
   const moe::QuantRows p{in, static_cast<uint8_t*>(codes), scales, d->rows, d->cols,
                          or_dense(d->ld_in, len), or_dense(d->ld_codes, d->cols),
                          or_dense(d->ld_scales, nb), bf16};

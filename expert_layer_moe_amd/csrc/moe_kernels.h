@@ -244,6 +244,8 @@ struct QuantRows {
   long long ld_in, ld_codes, ld_scales;
   bool bf16;
 };
+// rows x blocks of 128 per row, at most
+constexpr long long kMaxQuantBlocks = (1LL << 31) - 1;
 hipError_t launch_quant(const QuantRows& p, bool silu_mul, hipStream_t s);
 
 }  // namespace moe

@@ -340,7 +340,8 @@ typedef struct moe_quant_desc {
  * A NaN value gives a NaN code and leaves the rest of its block as if it were
  * 0; a block that holds an infinity gets an infinite scale, so that all of it
  * stands for NaN.  Gaps between rows are not written.  Errors as moe_gemm_fp8
- * (MOE_ERR_UNSUPPORTED for cols or strides off their multiples). */
+ * (MOE_ERR_UNSUPPORTED for cols or strides off their multiples, or 2^31 blocks
+ * of 128 or more). */
 int moe_quant_fp8(const moe_quant_desc* desc, const void* x, void* codes, float* scales,
                   moe_stream_t stream);
 
