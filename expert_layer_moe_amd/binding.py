@@ -340,13 +340,14 @@ def alloc_few_workspace(desc: moe_desc, topk: int, device="cuda") -> torch.Tenso
     n = moe_few_workspace_size(desc, topk)
     if n == 0:
         raise MoeError(-2, "not a layer of a few rows (bf16 activations, 1 to "
-                           f"{FEW_MAX_ROWS} rows)")
+                           f"{FEW_MAX_ROWS} rows, a hidden size of 128 n)")
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def moe_forward_few(desc, x, valid_rows, router_w, w13, w2, topk, out, workspace,
                     stream=None):
-    """moe_forward for at most FEW_MAX_ROWS token rows, in two launches."""
+    """moe_forward for at most FEW_MAX_ROWS token rows, in two or three
+    launches."""
     T, H, E, I, ns = desc.T, desc.H, desc.E, desc.I, desc.n_shared
     _dev(router_w, "router_w", _act(desc), (E, H))
     _dev(w13, "w13", _w(desc), (E + ns, 2 * I, H))

@@ -91,7 +91,7 @@ class DeviceLayer:
 
     def forward_few(self, x, valid=None, out=None, workspace=None, stream=None):
         """forward for at most FEW_MAX_ROWS token rows (one or a few sequences
-        decoding), in two launches.  Returns out."""
+        decoding), in two or three launches.  Returns out."""
         T = x.size(0)
         few = self._few.get(T)
         if few is None:

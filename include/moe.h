@@ -262,9 +262,9 @@ int moe_forward_noalloc(const moe_desc* desc, const void* x, const uint8_t* vali
 size_t moe_few_workspace_size(const moe_desc* desc, int32_t topk);
 
 /* moe_forward for a few token rows (T <= MOE_FEW_MAX_ROWS: one or a few
- * sequences decoding) in two launches ("Step3 Inference Optimization on AMD
- * Instinct MI308X", optimisation list: the MoE one-stage kernel).  Same
- * arguments, layouts and routing rule as moe_forward; the workspace is
+ * sequences decoding) in two launches, or three when the rows do not fit on
+ * chip ("Step3 Inference Optimization on AMD Instinct MI308X", optimisation
+ * list: the MoE one-stage kernel).  Same arguments, layouts and routing rule as moe_forward; the workspace is
  * moe_few_workspace_size's.  The arithmetic differs from moe_forward's in two
  * roundings: the routing weight is applied to SiLU(g)*u, which is kept to 16
  * mantissa bits instead of 8, and the expert sums meet in one fp32
@@ -272,9 +272,11 @@ size_t moe_few_workspace_size(const moe_desc* desc, int32_t topk);
  * rows chose: a row's last bit may differ between batches; equal calls give
  * equal bits.  A row whose router logits are NaN gets a NaN output row.
  * desc->block_m is checked and not used.  Errors as moe_forward, plus
- * MOE_ERR_UNSUPPORTED for T > MOE_FEW_MAX_ROWS, fp32 layers or H * I >= 2^30.  Calls must not
- * share a workspace while either runs; its contents need not be kept or
- * cleared between calls. */
+ * MOE_ERR_UNSUPPORTED for T > MOE_FEW_MAX_ROWS, fp32 layers or H * I >= 2^30,
+ * and MOE_ERR_INVALID_ARG for x, router_w, w13, w2 or a workspace that is not
+ * 16-byte aligned.  Calls must not share a workspace
+ * while either runs; its contents need not be kept or cleared between calls.
+ * Rows with valid_rows == 0 are not read and give zeros. */
 int moe_forward_few(const moe_desc* desc, const void* x, const uint8_t* valid_rows,
                     const void* router_w, const void* w13, const void* w2,
                     int32_t topk, void* out, void* workspace,

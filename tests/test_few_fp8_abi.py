@@ -1,0 +1,205 @@
+"""CPU-side checks of the few-row layer, the fp8 block-scale product and the
+token quantisations: arguments that the library or the binding refuses, and
+workspace sizes (no GPU needed: nothing below reaches a launch)."""
+import ctypes
+
+import pytest
+import torch
+
+import expert_layer_moe_amd as moe
+from expert_layer_moe_amd.binding import moe_desc
+
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, -1, -2, -3
+FAKE = 1 << 20   # never dereferenced: validation fails first
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return moe.load_library()
+
+
+def _layer(**kw):
+    base = dict(T=4, H=256, E=8, n_shared=0, I=64, act_dtype=moe.MOE_BF16, w_dtype=moe.MOE_BF16,
+                w13_scale=None, w2_scale=None, block_m=0, w_layout=0)
+    base.update(kw)
+    return moe_desc(**base)
+
+
+def _few(lib, d, topk=2, workspace_bytes=1 << 30, **ptr):
+    p = dict(x=FAKE, valid=None, router=FAKE, w13=FAKE, w2=FAKE, out=FAKE, ws=FAKE)
+    p.update(ptr)
+    return lib.moe_forward_few(None if d is None else ctypes.byref(d), p["x"], p["valid"],
+                               p["router"], p["w13"], p["w2"], topk, p["out"], p["ws"],
+                               workspace_bytes, None)
+
+
+SCALED = dict(w_dtype=moe.MOE_FP8_E4M3, w13_scale=FAKE, w2_scale=FAKE, I=128)
+
+
+@pytest.mark.parametrize("kw, topk, status", [
+    (dict(T=0), 2, INVALID),
+    (dict(T=-1), 2, INVALID),
+    (dict(T=moe.FEW_MAX_ROWS + 1), 2, UNSUPPORTED),
+    (dict(H=0), 2, INVALID),
+    (dict(H=192), 2, UNSUPPORTED),
+    (dict(H=200), 2, UNSUPPORTED),
+    (dict(I=48), 2, UNSUPPORTED),
+    (dict(H=32768, I=32768), 2, UNSUPPORTED),
+    (dict(act_dtype=moe.MOE_F32, w_dtype=moe.MOE_F32), 2, UNSUPPORTED),
+    (dict(), 0, INVALID),
+    (dict(), 9, INVALID),
+    (dict(SCALED, w13_scale=None), 2, INVALID),
+    (dict(SCALED, I=64), 2, UNSUPPORTED),
+])
+def test_few_refuses_layers(lib, kw, topk, status):
+    d = _layer(**kw)
+    assert _few(lib, d, topk) == status
+    assert lib.moe_few_workspace_size(ctypes.byref(d), topk) == 0
+    with pytest.raises(moe.MoeError):
+        moe.alloc_few_workspace(d, topk, "cpu")
+
+
+def test_few_refuses_pointers_and_small_workspaces(lib):
+    d = _layer()
+    assert _few(lib, None) == INVALID
+    for name in ("x", "router", "w13", "w2", "out", "ws"):
+        assert _few(lib, d, **{name: None}) == INVALID, name
+    for name in ("x", "router", "w13", "w2", "ws"):
+        assert _few(lib, d, **{name: FAKE + 8}) == INVALID, name
+    n = moe.moe_few_workspace_size(d, 2)
+    assert n > 0
+    assert _few(lib, d, workspace_bytes=n - 1) == WORKSPACE
+    assert _few(lib, d, workspace_bytes=0) == WORKSPACE
+
+
+def test_few_workspace_sizes():
+    """h' takes 4 bytes for each of T (k + n_shared) + 1 rows of I, the logits
+    4 parts of T rows of 4 E bytes; all but small tables beside that."""
+    for kw, k in ((dict(), 1), (dict(T=16, E=256, n_shared=1, H=7168, I=256), 8),
+                  (dict(SCALED, T=6, E=48), 3)):
+        d = _layer(**kw)
+        need = 4 * d.I * (d.T * (k + d.n_shared) + 1) + 16 * d.T * d.E
+        size = moe.moe_few_workspace_size(d, k)
+        assert need <= size <= need + 16 * d.T * 64 + (20 << 10)
+
+
+def _gemm(lib, d, a=FAKE, sa=FAKE, b=FAKE, sb=FAKE, out=FAKE):
+    return lib.moe_gemm_fp8(None if d is None else ctypes.byref(d), a, sa, b, sb, out, None)
+
+
+def _g(M=4, N=8, K=128, dt=moe.MOE_BF16, lda=0, ldb=0, ld_as=0, ldo=0):
+    return moe.moe_gemm_desc(M, N, K, dt, lda, ldb, ld_as, ldo)
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(M=0), INVALID), (dict(N=0), INVALID), (dict(K=0), INVALID), (dict(M=-1), INVALID),
+    (dict(K=120), UNSUPPORTED), (dict(K=8), UNSUPPORTED),
+    (dict(dt=moe.MOE_FP8_E4M3), INVALID), (dict(dt=99), INVALID),
+    (dict(lda=112), INVALID), (dict(ldb=112), INVALID), (dict(lda=136), UNSUPPORTED),
+    (dict(ldb=136), UNSUPPORTED), (dict(K=256, ld_as=1), INVALID), (dict(ldo=7), INVALID),
+    (dict(lda=-128), INVALID), (dict(ldo=-8), INVALID),
+    (dict(M=(1 << 30) + 1), UNSUPPORTED), (dict(N=(1 << 30) + 1), UNSUPPORTED),
+    (dict(lda=(1 << 23) + 16), UNSUPPORTED), (dict(ldb=(1 << 23) + 16), UNSUPPORTED),
+    (dict(K=(1 << 23) + 16), UNSUPPORTED), (dict(ld_as=(1 << 21) + 1), UNSUPPORTED),
+])
+def test_gemm_refuses(lib, kw, status):
+    assert _gemm(lib, _g(**kw)) == status
+
+
+def test_gemm_refuses_pointers(lib):
+    assert _gemm(lib, None) == INVALID
+    for name in ("a", "sa", "b", "sb", "out"):
+        assert _gemm(lib, _g(), **{name: None}) == INVALID, name
+    for name in ("a", "b"):
+        assert _gemm(lib, _g(), **{name: FAKE + 8}) == INVALID, name
+
+
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("kw, status", [
+    (dict(rows=0), INVALID), (dict(cols=0), INVALID), (dict(rows=-3), INVALID),
+    (dict(cols=24), UNSUPPORTED), (dict(cols=8), UNSUPPORTED),
+    (dict(dt=moe.MOE_FP8_E4M3), INVALID),
+    (dict(ld_in=16), INVALID), (dict(ld_in=516), UNSUPPORTED),
+    (dict(ld_in=514, dt=moe.MOE_F32), UNSUPPORTED),
+    (dict(ld_codes=112), INVALID), (dict(ld_codes=136), UNSUPPORTED),
+    (dict(cols=256, ld_scales=1), INVALID), (dict(ld_in=-512), INVALID),
+    (dict(rows=(1 << 31) - 1, cols=256), UNSUPPORTED),
+])
+def test_quant_refuses(lib, silu, kw, status):
+    v = dict(rows=4, cols=128, dt=moe.MOE_BF16, ld_in=0, ld_codes=0, ld_scales=0)
+    v.update(kw)
+    d = moe.moe_quant_desc(v["rows"], v["cols"], v["dt"], v["ld_in"], v["ld_codes"],
+                           v["ld_scales"])
+    entry = lib.moe_silu_mul_quant_fp8 if silu else lib.moe_quant_fp8
+    assert entry(ctypes.byref(d), FAKE, FAKE, FAKE, None) == status
+
+
+@pytest.mark.parametrize("silu", [False, True])
+def test_quant_refuses_pointers(lib, silu):
+    entry = lib.moe_silu_mul_quant_fp8 if silu else lib.moe_quant_fp8
+    d = moe.moe_quant_desc(4, 128, moe.MOE_BF16, 0, 0, 0)
+    assert entry(None, FAKE, FAKE, FAKE, None) == INVALID
+    for args in ((None, FAKE, FAKE), (FAKE, None, FAKE), (FAKE, FAKE, None),
+                 (FAKE + 8, FAKE, FAKE), (FAKE, FAKE + 8, FAKE)):
+        assert entry(ctypes.byref(d), *args, None) == INVALID
+
+
+def _codes(*shape):
+    return torch.zeros(shape, dtype=torch.uint8)
+
+
+@pytest.mark.parametrize("change", [
+    dict(a=_codes(3, 4, 128)), dict(a=_codes(4, 128).short()), dict(b=_codes(8, 112)),
+    dict(a_scale=torch.ones(4, 2)), dict(a_scale=torch.ones(4, 1).double()),
+    dict(b_scale=torch.ones(2, 1)), dict(out=torch.empty(4, 9)),
+    dict(out=torch.empty(4, 8).half()), dict(out=torch.empty(8, 4).t()),
+    dict(a=_codes(128, 4).t()), dict(),
+])
+def test_binding_refuses_products(change):
+    """Wrong shapes, types and orders; right ones (the last) are refused for
+    not being on a GPU."""
+    args = dict(a=_codes(4, 128), a_scale=torch.ones(4, 1), b=_codes(8, 128),
+                b_scale=torch.ones(1, 1))
+    args.update(change)
+    with pytest.raises(ValueError):
+        moe.moe_gemm_fp8(**args)
+
+
+@pytest.mark.parametrize("fn, x, kw", [
+    (moe.moe_quant_fp8, torch.zeros(128), {}),
+    (moe.moe_quant_fp8, torch.zeros(2, 128).half(), {}),
+    (moe.moe_quant_fp8, torch.zeros(128, 2).t(), {}),
+    (moe.moe_quant_fp8, torch.zeros(2, 128), dict(codes=_codes(2, 64))),
+    (moe.moe_quant_fp8, torch.zeros(2, 128), dict(scales=torch.zeros(2, 2))),
+    (moe.moe_quant_fp8, torch.zeros(2, 128), {}),
+    (moe.moe_silu_mul_quant_fp8, torch.zeros(2, 33), {}),
+    (moe.moe_silu_mul_quant_fp8, torch.zeros(2, 256), {}),
+])
+def test_binding_refuses_quantisations(fn, x, kw):
+    with pytest.raises(ValueError):
+        fn(x, **kw)
+
+
+def test_binding_refuses_layers():
+    bf = torch.bfloat16
+    d = _layer(T=2, E=4, H=128, I=32)
+    good = dict(x=torch.zeros(2, 128, dtype=bf), valid_rows=None,
+                router_w=torch.zeros(4, 128, dtype=bf), w13=torch.zeros(4, 64, 128, dtype=bf),
+                w2=torch.zeros(4, 128, 32, dtype=bf), topk=2, out=torch.zeros(2, 128, dtype=bf),
+                workspace=_codes(1 << 16))
+    for change in (dict(x=torch.zeros(3, 128, dtype=bf)), dict(x=torch.zeros(2, 128)),
+                   dict(out=torch.zeros(2, 256, dtype=bf)[:, ::2]),
+                   dict(valid_rows=torch.ones(2)), dict(valid_rows=_codes(3)),
+                   dict(workspace=torch.zeros(1 << 16)), {}):
+        with pytest.raises(ValueError):
+            moe.moe_forward_few(d, **dict(good, **change))
+
+
+def test_dense_layer_refuses_shapes():
+    w13, w2 = _codes(64, 128), _codes(128, 32)
+    s13, s2 = torch.ones(1, 1), torch.ones(1, 1)
+    moe.DenseFP8(w13, w2, s13, s2, device="cpu")
+    for args in ((w13, _codes(128, 48), s13, s2), (_codes(63, 128), w2, s13, s2),
+                 (w13, w2, torch.ones(2, 1), s2), (w13, w2, s13, torch.ones(1, 2))):
+        with pytest.raises(ValueError):
+            moe.DenseFP8(*args, device="cpu")
