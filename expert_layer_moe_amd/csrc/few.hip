@@ -32,11 +32,16 @@ constexpr int kDownCols = 32;      // output columns of a down unit
 
 // h' is kept as two bf16, the value rounded and the rest rounded: 16 mantissa
 // bits, so that h' adds nothing visible to the rounding of the output, at two
-// MFMAs where the launch waits for HBM anyway.  In memory: the values [T (k +
-// n_shared) + 1][I], then the rests, the last row of both zero; a 32-bit word
-// holds two columns.  A word that no gate/up unit has written yet is kUnset, a
-// pair of NaN that split_h never makes.
+// MFMAs where the launch waits for HBM anyway.  In memory (not STAGED): the
+// values [T (k + n_shared) + 1][I], then the rests, the last row of both zero;
+// a 32-bit word holds two columns.
+
+// STAGED, the gate and up sums themselves are in memory, and a word that no
+// block has written yet is kUnset, a NaN that finished() never gives.
 constexpr uint32_t kUnset = 0xffffffffu;
+__device__ __forceinline__ uint32_t finished(float v) {
+  return __float_as_uint(v) == kUnset ? 0x7fc00000u : __float_as_uint(v);
+}
 
 __device__ __forceinline__ void split_h(float v, uint32_t& hi, uint32_t& lo) {
   hi = f32_to_bf16_bits(v);
@@ -48,8 +53,8 @@ __device__ __forceinline__ void split_h(float v, uint32_t& hi, uint32_t& lo) {
 // part[z][t][e] (rows few_logit_stride(E) apart): router logits over the z-th part of K (the 8 waves of a
 // block split that part again and meet in LDS), 16 experts per block; the
 // second launch adds the parts up.  Rows with valid == 0 are not read.  Also
-// zeroes the ticket counter, the zero rows of h' (rows of I) and, STAGED, marks
-// the other rows unset.
+// zeroes the ticket counter and marks the sums unset (STAGED) or zeroes the
+// zero rows of h' (rows of I).
 __global__ __launch_bounds__(kThreads) void few_logits_kernel(
     const uint16_t* __restrict__ x, const uint8_t* __restrict__ valid,
     const uint16_t* __restrict__ R, float* __restrict__ part, uint32_t* __restrict__ hw,
@@ -58,10 +63,13 @@ __global__ __launch_bounds__(kThreads) void few_logits_kernel(
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
   const int m = lane % 16, g = lane / 16;
   const uint32_t gid = (blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
-  const uint32_t used = (uint32_t)rows * (I / 2), plane = used + I / 2, n = gridDim.x * gridDim.y * kThreads;
-  for (uint32_t i = gid; i < (uint32_t)I; i += n) hw[used + i % (I / 2) + (i < (uint32_t)I / 2 ? 0 : plane)] = 0u;
-  if (staged)
-    for (uint32_t i = gid; i < 2 * used; i += n) hw[i < used ? i : i + I / 2] = kUnset;
+  const uint32_t n = gridDim.x * gridDim.y * kThreads;
+  if (staged) {
+    for (uint32_t i = gid; i < 2u * kFewParts * rows * I; i += n) hw[i] = kUnset;
+  } else {
+    const uint32_t used = (uint32_t)rows * (I / 2), half = I / 2;
+    for (uint32_t i = gid; i < 2 * half; i += n) hw[used + i + (i < half ? 0 : used)] = 0u;
+  }
   if (gid == 0) *ticket = 0;
   const int e = blockIdx.x * 16 + m;
   const bool ev = e < E;
@@ -167,6 +175,8 @@ struct FewTables {
   int16_t act[kMaxSeg];           // segments that some row chose, ascending
   uint32_t chosen[(kMaxSeg + 31) / 32];   // the same as bits
   float w[kRows][kMaxTopk + 1];   // routing weights; the shared slot holds 1
+  int16_t pick[kRows * (kMaxTopk + 1)];   // an assignment's segment
+  int16_t place[kMaxSeg];         // of a segment in act
   uint8_t bad[kRows];             // rows whose logits are NaN
   int n_act;
 };
@@ -175,19 +185,23 @@ struct FewTables {
 // alias scope of its own in place of those of the functions' arguments, and
 // then waits for every load to LDS ahead of any read): the tables, the token
 // rows (gate/up) or h' (down) of calls whose rows fit (STAGED), and a ring of
-// weights per wave, which also holds its sums at the end of a unit.  Half a
-// CU's LDS: two blocks on a CU.
-constexpr int kPad = 64;   // bytes between staged rows: up to four rows on different banks
+// weights per wave, which also holds its sums at the end of a unit.  STAGED:
+// one block a CU, and room for the waves' sums of two segments of its range
+// beside the ring, which stays full; otherwise two blocks a CU, one of which
+// streams while the other adds up.
+constexpr int kPad = kFewPad;   // bytes between staged rows: up to four rows on different banks
 template <bool STAGED>
 struct FewShared {
-  static constexpr int kStage = STAGED ? 22 * 1024 : 16, kRing = STAGED ? 6 * 1024 : 8 * 1024;
+  static constexpr int kStage = STAGED ? kFewStage : 16, kRing = STAGED ? 10 * 1024 : 8 * 1024;
+  static constexpr int kSums = STAGED ? 2 * kWaves * 2 * kWave : 1;
   FewTables tb;
   int tk;   // the block's next ticket
   __attribute__((aligned(16))) uint8_t stage[kStage];
   __attribute__((aligned(16))) uint8_t ring[kWaves][kRing];
+  floatx4 sums[kSums];
 };
-static_assert(sizeof(FewShared<true>) <= 80 * 1024 && sizeof(FewShared<false>) <= 80 * 1024,
-              "two blocks on a CU");
+static_assert(sizeof(FewShared<true>) <= 160 * 1024, "one block on a CU");
+static_assert(sizeof(FewShared<false>) <= 80 * 1024, "two blocks on a CU");
 
 // A logit as an unsigned number of the same order; 0 for NaN (and for experts
 // already taken), below any logit.
@@ -274,6 +288,7 @@ __device__ __forceinline__ void few_topk(const float* __restrict__ part, int t, 
   if (lane < kk) {
     const int e = lane < k ? my_e : E;
     tb.slot[e][t] = (int16_t)(t * kk + lane);
+    tb.pick[t * kk + lane] = (int16_t)e;
     tb.w[t][lane] = lane < k ? my_w : 1.f;
     atomicOr(&tb.chosen[e / 32], 1u << (e % 32));
   }
@@ -295,8 +310,13 @@ struct FewArgs {
   int T, H, I, E, ns, k;
 };
 
+// By one thread.  (An address in vector registers: for a uniform one the
+// compiler adds up the wave's tickets first and waits for the sum, and with it
+// for all loads before it, on the spot.)
 __device__ __forceinline__ int take_ticket(int32_t* ticket) {
-  return __hip_atomic_fetch_add(ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  auto* p = (__attribute__((address_space(1))) int32_t*)ticket;
+  asm volatile("" : "+v"(p));
+  return __hip_atomic_fetch_add(p, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // The tables the units work from and, STAGED, the token rows in LDS (a row of
@@ -338,6 +358,7 @@ __device__ __forceinline__ void few_route(const FewArgs& a, FewTables& tb, uint8
     n += __popc(word & ((1u << (e % 32)) - 1));
     const bool any = word >> (e % 32) & 1;
     if (any) tb.act[n] = (int16_t)e;
+    tb.place[e] = (int16_t)n;
     if (e == nseg - 1) tb.n_act = n + any;
   }
   __syncthreads();
@@ -379,8 +400,9 @@ struct GateUp {
         for (int n = 0; n < NT; ++n) sc[set][n] = sp[n][c / 2];
     }
   }
-  // The sums of the chunk in `cur`, x and scales in set `set`; `second`: the
-  // second half of a 128-wide block.
+  // The sums of the chunk in `cur`, x and scales in set `set`; fp8: scaled up
+  // to here if `second`, the second half of a 128-wide block (STAGED: always,
+  // blocks may be split between waves).
   __device__ __forceinline__ void multiply(const uint8_t* __restrict__ cur, int lane, int set, bool second) {
 #pragma unroll
     for (int u = 0; u < WC::kSteps; ++u)
@@ -398,18 +420,17 @@ struct GateUp {
           part[n][i] = 0.f;
         }
   }
-  // STAGED: chunk c out of `cur`, chunk c + kAhead (if there is one) into `next`.
-  __device__ __forceinline__ void step_staged(const uint8_t* __restrict__ cur, uint8_t* __restrict__ next,
-                                              const uint8_t* __restrict__ xs, int c, int c1, bool xv,
+  // STAGED: chunk c out of `cur`.
+  __device__ __forceinline__ void step_staged(const uint8_t* __restrict__ cur,
+                                              const uint8_t* __restrict__ xs, int c, bool xv,
                                               int lane) {
-    if (c + kAhead < c1) issue(next, c + kAhead, 0);
     if constexpr (FP8)
 #pragma unroll
       for (int n = 0; n < NT; ++n) sc[0][n] = sp[n][c / 2];
 #pragma unroll
     for (int u = 0; u < WC::kSteps; ++u)
       x[0][u] = ld16(xs + (xv ? 2 * (c * 32 * WC::kSteps + WC::k_of(u, lane / 16)) : 0));
-    multiply(cur, lane, 0, c % 2 == 1);
+    multiply(cur, lane, 0, true);
   }
   // Not STAGED: set i's chunk in its place in the wave's ring; LOAD: chunk c
   // takes the place of the one before it.
@@ -425,31 +446,22 @@ struct GateUp {
   }
 };
 
-// h' columns c0 .. c0 + few_cols - 1 of expert e for every row that chose it.
-// bf16: the MFMA A operand holds 8 gate rows and the 8 up rows of the same
-// columns; fp8: 16 gate rows, and 16 up rows in a second one (half a packed
-// fp8 tile is half a line of memory).  The B operand holds the token rows
-// (rows that did not choose e: zeros).  The waves split K = H in 128-wide
-// blocks and meet in LDS.
+// Where a gate/up unit's weights are, for the wave's loads: h' columns c0 ..
+// c0 + few_cols - 1 of expert e.  bf16: the MFMA A operand holds 8 gate rows
+// and the 8 up rows of the same columns; fp8: 16 gate rows, and 16 up rows in
+// a second one (half a packed fp8 tile is half a line of memory).  The B
+// operand holds the token rows (rows that did not choose e: zeros).
 template <bool FP8, bool PW, bool STAGED>
-__device__ __forceinline__ void gate_up_unit(const FewArgs& a, const FewTables* __restrict__ tb,
-                                             const uint8_t* __restrict__ xs,
-                                             uint8_t* __restrict__ ring, int e, int c0, int& next) {
+__device__ __forceinline__ void at_unit(GateUp<FP8, PW, STAGED>& gu, const FewArgs& a, int lane, int e,
+                                        int c0) {
   using GU = GateUp<FP8, PW, STAGED>;
   using WC = typename GU::WC;
-  constexpr int NT = GU::NT, kCols = few_cols(FP8), kRing = FewShared<STAGED>::kRing;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
-  const int m = lane % 16, g = lane / 16;
   const int H = a.H, I = a.I;
   constexpr int kSize = FP8 ? 1 : 2;
-  GU gu;
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
+  for (int n = 0; n < GU::NT; ++n)
     gu.wbuf[n] = buffer_at(static_cast<const uint8_t*>(a.w13) +
                            ((size_t)e * 2 * I + n * I + c0 / 16 * 16) * H * kSize);
-    gu.sp[n] = FP8 ? a.s13 + ((size_t)e * (2 * I / 128) + (n * I + c0) / 128) * (H / 128) : nullptr;
-    gu.acc[n] = gu.part[n] = floatx4{0.f, 0.f, 0.f, 0.f};
-  }
   // bf16: the tile's rows 8 .. 15 are the up rows, I rows on
   const uint32_t up_rows = (uint32_t)I * H * kSize;
   const int lr = WC::load_row(lane);
@@ -457,35 +469,45 @@ __device__ __forceinline__ void gate_up_unit(const FewArgs& a, const FewTables* 
   for (int p = 0; p < WC::kParts; ++p) {
     if constexpr (FP8) gu.wl[p] = WC::load_offset(lane) + (PW ? 0 : lr * H * kSize);
     else if constexpr (PW)   // lane (g, r)'s share lies at 256 g + 16 r
-      gu.wl[p] = 256 * g + 16 * (c0 % 16 + m % 8) + (m >= 8 ? up_rows : 0u);
+      gu.wl[p] = 256 * (lane / 16) + 16 * (c0 % 16 + lane % 8) + (lane % 16 >= 8 ? up_rows : 0u);
     else gu.wl[p] = WC::load_offset(lane) + (c0 % 16 + lr) * H * kSize + p * up_rows;
   }
+}
+// And the scales of its sums, which start at zero.
+template <bool FP8, bool PW, bool STAGED>
+__device__ __forceinline__ void start_sums(GateUp<FP8, PW, STAGED>& gu, const FewArgs& a, int e, int c0) {
+  const int H = a.H, I = a.I;
+#pragma unroll
+  for (int n = 0; n < GateUp<FP8, PW, STAGED>::NT; ++n) {
+    gu.sp[n] = FP8 ? a.s13 + ((size_t)e * (2 * I / 128) + (n * I + c0) / 128) * (H / 128) : nullptr;
+    gu.acc[n] = gu.part[n] = floatx4{0.f, 0.f, 0.f, 0.f};
+  }
+}
+
+// A unit by a block, the waves splitting K = H in 128-wide blocks and meeting
+// in LDS: h' to memory.
+template <bool FP8, bool PW>
+__device__ __forceinline__ void gate_up_unit(const FewArgs& a, const FewTables* __restrict__ tb,
+                                             uint8_t* __restrict__ ring, int e, int c0, int& next) {
+  using GU = GateUp<FP8, PW, false>;
+  using WC = typename GU::WC;
+  constexpr int NT = GU::NT, kCols = few_cols(FP8), kRing = FewShared<false>::kRing;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const int m = lane % 16, g = lane / 16;
+  const int H = a.H, I = a.I;
+  GU gu;
+  at_unit(gu, a, lane, e, c0);
+  start_sums(gu, a, e, c0);
   const bool xv = tb->slot[e][m] >= 0;
   // rows that did not choose e: zeros
   gu.xbuf = buffer_at(a.x, 2 * a.T * H);
 #pragma unroll
   for (int u = 0; u < WC::kSteps; ++u) gu.xl[u] = xv ? 2 * (m * H + WC::k_of(u, g)) : kNowhere;
-  // staged rows: a lane without one reads the 16 zero bytes behind them
-  const uint8_t* xl = xs + (xv ? m * (2 * H + kPad) : a.T * (2 * H + kPad));
   // (rounded so that wave 0, which takes the tickets, has a block)
   const int nb = H / 128, cpb = 4 / WC::kSteps;
   const int s0 = (nb * wave + kWaves - 1) / kWaves * cpb, s1 = (nb * (wave + 1) + kWaves - 1) / kWaves * cpb;
   uint8_t* mine = ring + wave * kRing;
-  if constexpr (STAGED) {
-#pragma unroll
-    for (int i = 0; i < GU::kAhead; ++i)
-      if (s0 + i < s1) gu.issue(mine + i * GU::kEntry, s0 + i, 0);
-    if (threadIdx.x == 0) next = take_ticket(a.ticket);
-    int at = 0;
-#pragma unroll 1
-    for (int c = s0; c < s1; ++c) {
-      if (c + GU::kAhead <= s1) wait_loads<(GU::kAhead - 1) * GU::kLoads>();
-      else wait_loads<0>();
-      const int to = at == 0 ? GU::kSets - 1 : at - 1;
-      gu.step_staged(mine + at * GU::kEntry, mine + to * GU::kEntry, xl, c, s1, xv, lane);
-      at = at + 1 == GU::kSets ? 0 : at + 1;
-    }
-  } else if (s0 < s1) {
+  if (s0 < s1) {
     // (behind the last chunk that one again, unused, so that as many loads are
     // on the way at every step)
 #pragma unroll
@@ -538,6 +560,123 @@ __device__ __forceinline__ void gate_up_unit(const FewArgs& a, const FewTables* 
   }
 }
 
+// A range of the gate/up units' 128-wide blocks of K, unit after unit, STAGED:
+// the calls' few units would not go evenly into the chip's CUs, so each block
+// takes an equal share of all their blocks instead, at most kFewParts of them
+// sharing a unit.  Every wave takes its part of each unit's blocks in the range
+// (a segment) as one stream: the ring runs on from segment to segment, only the
+// sums stop, for the block to add the waves' up and send them to memory.
+struct FewSplit {
+  int nb, total, per, ranges;   // blocks of a unit, of all, of a range; ranges
+  __device__ __forceinline__ FewSplit(int H, int n_gu) {
+    nb = H / 128;
+    total = n_gu * nb;
+    per = max((total + 255) / 256, (nb + kFewParts - 2) / (kFewParts - 1));
+    ranges = (total + per - 1) / per;
+  }
+  // the parts that share unit u: ranges first(u) .. last(u)
+  __device__ __forceinline__ int first(int u) const { return u * nb / per; }
+  __device__ __forceinline__ int last(int u) const { return (u * nb + nb - 1) / per; }
+};
+
+// A wave's place in its chunks of a range.
+struct RangePlace {
+  int u, end;   // unit, end of the range
+  int c, c1;    // chunks of the segment to go
+  // The wave's chunks of the segment of unit u in blocks [from, end).
+  __device__ __forceinline__ void segment(int from, int nb, int cpb, int wave) {
+    const int k0 = max(from - u * nb, 0), k1 = min(end - u * nb, nb), n = (k1 - k0) * cpb;
+    c = k0 * cpb + n * wave / kWaves;
+    c1 = k0 * cpb + n * (wave + 1) / kWaves;
+  }
+};
+
+template <bool FP8, bool PW>
+__device__ __forceinline__ void gate_up_range(const FewArgs& a, const FewTables* __restrict__ tb,
+                                              const uint8_t* __restrict__ xs,
+                                              uint8_t* __restrict__ ring, floatx4* __restrict__ sums,
+                                              const FewSplit& sp, int r, int& next) {
+  using GU = GateUp<FP8, PW, true>;
+  using WC = typename GU::WC;
+  constexpr int NT = GU::NT, kCols = few_cols(FP8), kRing = FewShared<true>::kRing;
+  constexpr int kValues = 16 * NT;   // of a row: gate columns, then up columns
+  constexpr int cpb = 4 / WC::kSteps;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const int m = lane % 16, n_cg = a.I / kCols, nb = sp.nb;
+  const int r0 = r * sp.per, r1 = min(r0 + sp.per, sp.total);
+  uint8_t* mine = ring + wave * kRing;
+  GU gu;
+  RangePlace ld, at;
+  ld.u = at.u = r0 / nb;
+  ld.end = at.end = r1;
+  auto column = [&](int u) { return (u % n_cg) * kCols; };
+  auto expert = [&](int u) { return __builtin_amdgcn_readfirstlane(tb->act[u / n_cg]); };
+  // the next chunk to load: of the first segment from ld.u on that has one
+  auto settle = [&]() {
+    while (ld.c == ld.c1 && (ld.u + 1) * nb < r1) {
+      ++ld.u;
+      ld.segment(r0, nb, cpb, wave);
+      at_unit(gu, a, lane, expert(ld.u), column(ld.u));
+    }
+  };
+  ld.segment(r0, nb, cpb, wave);
+  at_unit(gu, a, lane, expert(ld.u), column(ld.u));
+  settle();
+  int ahead = 0;   // chunks on their way
+#pragma unroll 1
+  for (int i = 0; i < GU::kAhead && ld.c < ld.c1; ++i) {
+    gu.issue(mine + i * GU::kEntry, ld.c++, 0);
+    ++ahead;
+    settle();
+  }
+  if (threadIdx.x == 0) next = take_ticket(a.ticket);
+  int from = 0, side = 0;
+#pragma unroll 1
+  for (; at.u * nb < r1; ++at.u) {
+    const int e = expert(at.u), c0 = column(at.u);
+    at.segment(r0, nb, cpb, wave);
+    start_sums(gu, a, e, c0);
+    const bool xv = tb->slot[e][m] >= 0;
+    // a lane without a row reads the 16 zero bytes behind them
+    const uint8_t* xl = xs + (xv ? m * (2 * a.H + kPad) : a.T * (2 * a.H + kPad));
+#pragma unroll 1
+    for (int c = at.c; c < at.c1; ++c) {
+      if (ahead == GU::kAhead) wait_loads<(GU::kAhead - 1) * GU::kLoads>();
+      else wait_loads<0>();
+      --ahead;
+      if (ld.c < ld.c1) {
+        gu.issue(mine + (from == 0 ? GU::kSets - 1 : from - 1) * GU::kEntry, ld.c++, 0);
+        ++ahead;
+        settle();
+      }
+      gu.step_staged(mine + from * GU::kEntry, xl, c, xv, lane);
+      from = from + 1 == GU::kSets ? 0 : from + 1;
+    }
+    floatx4* red = sums + side * (kWaves * 2 * kWave);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) red[(wave * 2 + n) * kWave + lane] = gu.acc[n];
+    // (no __syncthreads: the loads may stay on their way.  A wave overwrites
+    // this side after the next segment's barrier, when all have read it.)
+    wait_loads<63>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    const int v = threadIdx.x % kValues, t = threadIdx.x / kValues;
+    const int slot = t < a.T ? tb->slot[e][t] : -1;
+    if (slot >= 0) {
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w)
+        s += red[(w * 2 + v / 16) * kWave + v % 16 / 4 * 16 + t][v % 4];
+      // readers wait for the words themselves to change, so nothing has to be
+      // ordered around the stores
+      const size_t at_part = ((size_t)slot * n_cg + at.u % n_cg) * kFewParts + r - sp.first(at.u);
+      __hip_atomic_store(a.hw + at_part * kValues + v, finished(s), __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_AGENT);
+    }
+    side ^= 1;
+  }
+}
+
 __device__ __forceinline__ unsigned long long peek(const uint32_t* p) {
   return __hip_atomic_load(reinterpret_cast<const unsigned long long*>(p), __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_AGENT);
@@ -551,36 +690,61 @@ __device__ __forceinline__ bool unset(const unsigned long long (&v)[N]) {
   return top == kUnset;
 }
 
-// All of h' to LDS: row s (an assignment) of 2 I bytes of values and 2 I of
-// rests every 4 I + kPad bytes, 16 zero bytes behind the last row.  By every
-// thread of the block, 16 bytes of both a turn.  Waits for the words that are
-// unset: the units that write them have smaller tickets, which blocks take in
-// order and only while they run, so each such unit has ended or is running in
-// a block that waits for nothing, and the wait ends.
+// All of h' to LDS, from the sums of its parts: row s (an assignment) of 2 I
+// bytes of values and 2 I of rests every 4 I + kPad bytes, 16 zero bytes behind
+// the last row.  By every thread of the block, a unit of an assignment a turn.
+// Waits for the sums that are unset: the ranges that write them have smaller
+// tickets, which blocks take in order and only while they run, so each such
+// range has ended or is running in a block that waits for nothing, and the wait
+// ends.
+template <bool FP8>
 __device__ __forceinline__ void stage_h(const FewArgs& a, const FewTables* __restrict__ tb,
-                                        uint8_t* __restrict__ hs) {
-  const int I = a.I, pieces = I / 8, total = a.T * (a.k + a.ns) * pieces, row_bytes = 4 * I + kPad;
+                                        const FewSplit& sp, uint8_t* __restrict__ hs) {
+  constexpr int kCols = few_cols(FP8), kValues = 2 * kCols;
+  const int I = a.I, kk = a.k + a.ns, n_cg = I / kCols, total = a.T * kk * n_cg;
+  const int row_bytes = 4 * I + kPad;
 #pragma unroll 1
   for (int j = threadIdx.x; j < total; j += kThreads) {
-    const int slot = j / pieces, t = slot / (a.k + a.ns);
+    const int slot = j / n_cg, cg = j - slot * n_cg, t = slot / kk;
     if (tb->bad[t] || (a.valid != nullptr && a.valid[t] == 0)) continue;
-    const uint32_t* p = a.hw + 4 * (uint32_t)j;
-    unsigned long long v[4];
-    for (;;) {
-      v[0] = peek(p);
-      v[1] = peek(p + 2);
-      v[2] = peek(p + a.plane);
-      v[3] = peek(p + a.plane + 2);
-      if (!unset(v)) break;
+    const int u = tb->place[tb->pick[slot]] * n_cg + cg, parts = sp.last(u) - sp.first(u) + 1;
+    const uint32_t* p = a.hw + (size_t)j * kFewParts * kValues;
+    float sum[kValues];
+#pragma unroll
+    for (int i = 0; i < kValues; ++i) sum[i] = 0.f;
+#pragma unroll 1
+    for (int q = 0; q < parts; ++q, p += kValues) {
+      unsigned long long v[kValues / 2];
+      for (;;) {
+#pragma unroll
+        for (int i = 0; i < kValues / 2; ++i) v[i] = peek(p + 2 * i);
+        if (!unset(v)) break;
+      }
+#pragma unroll
+      for (int i = 0; i < kValues / 2; ++i) {
+        sum[2 * i] += __uint_as_float((uint32_t)v[i]);
+        sum[2 * i + 1] += __uint_as_float((uint32_t)(v[i] >> 32));
+      }
     }
-    uint8_t* to = hs + slot * row_bytes + 16 * (j - slot * pieces);
-    *reinterpret_cast<unsigned long long*>(to) = v[0];
-    *reinterpret_cast<unsigned long long*>(to + 8) = v[1];
-    *reinterpret_cast<unsigned long long*>(to + 2 * I) = v[2];
-    *reinterpret_cast<unsigned long long*>(to + 2 * I + 8) = v[3];
+    const float w = tb->w[t][slot - t * kk];
+    uint8_t* to = hs + slot * row_bytes + 2 * kCols * cg;
+#pragma unroll
+    for (int i = 0; i < kCols; i += 8) {
+      u32x4 hi, lo;
+#pragma unroll
+      for (int c = 0; c < 8; c += 2) {
+        uint32_t h0, l0, h1, l1;
+        split_h(silu_mul(sum[i + c], sum[kCols + i + c]) * w, h0, l0);
+        split_h(silu_mul(sum[i + c + 1], sum[kCols + i + c + 1]) * w, h1, l1);
+        hi[c / 2] = h0 | h1 << 16;
+        lo[c / 2] = l0 | l1 << 16;
+      }
+      *reinterpret_cast<u32x4*>(to + 2 * i) = hi;
+      *reinterpret_cast<u32x4*>(to + 2 * I + 2 * i) = lo;
+    }
   }
   if (threadIdx.x == 0)
-    *reinterpret_cast<u32x4*>(hs + a.T * (a.k + a.ns) * row_bytes) = u32x4{0u, 0u, 0u, 0u};
+    *reinterpret_cast<u32x4*>(hs + a.T * kk * row_bytes) = u32x4{0u, 0u, 0u, 0u};
 }
 
 // A down unit's loads and sums of one wave, W2 by way of LDS.
@@ -663,8 +827,9 @@ __device__ __forceinline__ void store_out(const FewArgs& a, const FewTables* __r
 // block waits for h' (staged: it has it from its unit before).
 template <bool FP8, bool PW>
 __device__ __forceinline__ void down_unit_staged(const FewArgs& a, const FewTables* __restrict__ tb,
-                                                 uint8_t* __restrict__ hs, uint8_t* __restrict__ ring,
-                                                 bool staged, int c0, int& next) {
+                                                 const FewSplit& sp, uint8_t* __restrict__ hs,
+                                                 uint8_t* __restrict__ ring, bool staged, int c0,
+                                                 int& next) {
   using DS = DownStaged<FP8, PW>;
   using WC = typename DS::WC;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
@@ -691,7 +856,7 @@ __device__ __forceinline__ void down_unit_staged(const FewArgs& a, const FewTabl
   for (int i = 0; i < DS::kAhead; ++i)
     if (s0 + i < s1) d.issue(mine + i * DS::kEntry, tb);
   if (threadIdx.x == 0) next = take_ticket(a.ticket);
-  if (!staged) stage_h(a, tb, hs);
+  if (!staged) stage_h<FP8>(a, tb, sp, hs);
   __syncthreads();
   int at = 0;
 #pragma unroll 1
@@ -876,7 +1041,7 @@ __global__ __launch_bounds__((Down<FP8, PW, NT, WIDE>::kWaves * kWave)) void few
 }
 
 template <bool FP8, bool PW, bool STAGED>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4)))
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(STAGED ? 2 : 4)))
 void few_experts_kernel(FewArgs a) {
   static_assert(kThreads >= kRows * kDownCols, "one output per thread");
   __shared__ FewShared<STAGED> sh;
@@ -886,21 +1051,25 @@ void few_experts_kernel(FewArgs a) {
       reinterpret_cast<uint32_t*>(a.tables)[i] = reinterpret_cast<const uint32_t*>(&sh.tb)[i];
   constexpr int kCols = few_cols(FP8);
   const int n_cg = a.I / kCols, n_gu = __builtin_amdgcn_readfirstlane(sh.tb.n_act) * n_cg;
-  const int n_all = n_gu + (STAGED ? a.H / kDownCols : 0);
+  const FewSplit sp(a.H, STAGED ? n_gu : 0);
+  const int n_up = STAGED ? sp.ranges : n_gu, n_all = n_up + (STAGED ? a.H / kDownCols : 0);
   int tk = __builtin_amdgcn_readfirstlane(sh.tk);
   bool h_staged = false;   // the stage holds h' in place of the token rows (tickets grow)
   while (tk < n_all) {
     __syncthreads();   // tk, the ring and the stage are free
     int next = 0;   // the next ticket (thread 0), asked for behind the unit's first loads
-    if (tk < n_gu) {
+    if constexpr (STAGED) {
+      if (tk < n_up) {
+        gate_up_range<FP8, PW>(a, &sh.tb, sh.stage, &sh.ring[0][0], sh.sums, sp, tk, next);
+      } else {
+        down_unit_staged<FP8, PW>(a, &sh.tb, sp, sh.stage, &sh.ring[0][0], h_staged,
+                                  (tk - n_up) * kDownCols, next);
+        h_staged = true;
+      }
+    } else {
       const int ai = tk / n_cg;
-      gate_up_unit<FP8, PW, STAGED>(a, &sh.tb, sh.stage, &sh.ring[0][0],
-                                    __builtin_amdgcn_readfirstlane(sh.tb.act[ai]),
-                                    (tk - ai * n_cg) * kCols, next);
-    } else if constexpr (STAGED) {
-      down_unit_staged<FP8, PW>(a, &sh.tb, sh.stage, &sh.ring[0][0], h_staged, (tk - n_gu) * kDownCols,
-                                next);
-      h_staged = true;
+      gate_up_unit<FP8, PW>(a, &sh.tb, &sh.ring[0][0], __builtin_amdgcn_readfirstlane(sh.tb.act[ai]),
+                            (tk - ai * n_cg) * kCols, next);
     }
     if (threadIdx.x == 0) sh.tk = next;
     __syncthreads();
@@ -918,9 +1087,7 @@ hipError_t launch_few(int wkind, bool packed, const void* x, const uint8_t* vali
       H % 128 != 0 || I % 32 != 0 || (long long)H * I >= kMaxFewArea || (wkind == W_FP8 && I % 128 != 0))
     return hipErrorInvalidValue;
   const int rows = T * (k + n_shared);
-  // rows and h' in LDS where they fit
-  const bool staged = (long long)T * (2 * H + kPad) + 16 <= FewShared<true>::kStage &&
-                      rows * (4LL * I + kPad) + 16 <= FewShared<true>::kStage;
+  const bool staged = few_staged(T, H, I, k + n_shared);
   hipLaunchKernelGGL(few_logits_kernel, dim3((E + 15) / 16, kFewLogitParts), dim3(kThreads), 0, s,
                      static_cast<const uint16_t*>(x), valid, static_cast<const uint16_t*>(R), part,
                      hw, rows, I, staged, ticket, T, H, E);
@@ -929,11 +1096,12 @@ hipError_t launch_few(int wkind, bool packed, const void* x, const uint8_t* vali
   const FewArgs a{static_cast<const uint16_t*>(x), valid, w13, w2, s13, s2, part, hw,
                   (uint32_t)(rows + 1) * (I / 2), ticket, static_cast<FewTables*>(tables),
                   static_cast<uint16_t*>(out), T, H, I, E, n_shared, k};
-  // A block for every gate/up unit, so that they all run at once, from one to
-  // two a CU; blocks loop over the tickets.
+  // Blocks loop over the tickets.  STAGED: one a CU, or fewer if there are
+  // fewer ranges and down units; otherwise a block for every gate/up unit, so
+  // that they all run at once, from one to two a CU.
   const long long n_gu = (long long)(std::min(E, T * k) + n_shared) * (I / few_cols(wkind == W_FP8));
-  const long long units = n_gu + (staged ? H / kDownCols : 0);
-  const dim3 grid((unsigned)std::min(units, std::max(256LL, std::min(n_gu, 512LL))));
+  const dim3 grid((unsigned)(staged ? std::min((kFewParts - 1) * n_gu + H / kDownCols, 256LL)
+                                    : std::min(n_gu, 512LL)));
   // The down launch: 32 columns a block, or 16 if that gives fewer rounds of
   // 256 blocks (one a CU) for its columns.
   const bool narrow = (H / 16 + 255) / 256 < (H / 32 + 255) / 256 * 2;

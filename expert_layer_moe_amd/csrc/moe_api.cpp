@@ -241,7 +241,7 @@ int make_few_plan(const moe_desc* d, int32_t topk, FewPlan* p) {
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t r = o; o = round_up(o + bytes, kAlign); return r; };
   p->off_part = take((size_t)moe::kFewLogitParts * d->T * moe::few_logit_stride(d->E) * 4);
-  p->off_hw = take(((size_t)d->T * (topk + d->n_shared) + 1) * d->I * 4);
+  p->off_hw = take((size_t)moe::few_hw_words(d->T, d->H, d->I, topk + d->n_shared) * 4);
   p->off_ticket = take(4);
   p->off_tables = take(moe::kFewTableBytes);
   p->total = o;

@@ -205,14 +205,28 @@ hipError_t launch_zero_i32(int32_t* a, size_t na, int32_t* b, size_t nb, hipStre
 // ---- few token rows ----------------------------------------------------------
 constexpr int kFewRows = 16;        // most rows of a call
 constexpr size_t kFewTableBytes = 16 * 1024;   // of the tables a launch leaves to the next
-constexpr int kFewLogitParts = 4;   // K parts of the router logits
+constexpr int kFewLogitParts = 8;   // K parts of the router logits
 inline constexpr int few_logit_stride(int E) { return (E + 63) / 64 * 64; }
 constexpr long long kMaxFewArea = 1LL << 30;   // H I below it: 32-bit offsets inside an expert
+// Calls whose token rows and h' fit in a block's LDS (kFewStage bytes, rows
+// kFewPad bytes apart) run in two launches, others in three.
+constexpr int kFewStage = 32 * 1024, kFewPad = 64;
+inline constexpr bool few_staged(int T, int H, int I, int per_row) {
+  return (long long)T * (2LL * H + kFewPad) + 16 <= kFewStage &&
+         (long long)T * per_row * (4LL * I + kFewPad) + 16 <= kFewStage;
+}
+// Blocks that may share a gate/up unit, whose sums (2 I an assignment) each
+// has room for.
+constexpr int kFewParts = 5;
+// Words of hw: those sums, or h' and a row of zeros.
+inline constexpr long long few_hw_words(int T, int H, int I, int per_row) {
+  return few_staged(T, H, I, per_row) ? 2LL * kFewParts * T * per_row * I
+                                      : ((long long)T * per_row + 1) * I;
+}
 // The whole layer for T <= kFewRows rows, bf16 activations, bf16 or fp8
-// weights, in two or three launches.  part: [kFewLogitParts][T]
-// [few_logit_stride(E)] fp32; hw: (T (k + n_shared) + 1) I words; tables:
-// kFewTableBytes; ticket: one int32; all 16-byte aligned.  None of them needs
-// to hold anything on entry.
+// weights.  part: [kFewLogitParts][T][few_logit_stride(E)] fp32; hw:
+// few_hw_words words; tables: kFewTableBytes; ticket: one int32; all 16-byte
+// aligned.  None of them needs to hold anything on entry.
 hipError_t launch_few(int wkind, bool packed, const void* x, const uint8_t* valid, const void* R,
                       const void* w13, const void* w2, const float* s13, const float* s2,
                       float* part, uint32_t* hw, int32_t* ticket, void* tables, void* out, int T,

@@ -73,14 +73,19 @@ def test_few_refuses_pointers_and_small_workspaces(lib):
 
 
 def test_few_workspace_sizes():
-    """h' takes 4 bytes for each of T (k + n_shared) + 1 rows of I, the logits
-    4 parts of T rows of 4 E bytes; all but small tables beside that."""
-    for kw, k in ((dict(), 1), (dict(T=16, E=256, n_shared=1, H=7168, I=256), 8),
-                  (dict(SCALED, T=6, E=48), 3)):
+    """The logits take 8 parts of T rows of 4 E bytes.  Beside small tables:
+    where the rows fit on chip 5 parts of 2 I sums of 4 bytes for each of the T
+    (k + n_shared) assignments, otherwise 4 bytes of h' for each, and a row
+    more."""
+    for kw, k, on_chip in ((dict(), 1, True), (dict(T=2, H=1024, E=48, I=96), 3, True),
+                           (dict(T=16, E=256, n_shared=1, H=7168, I=256), 8, False),
+                           (dict(SCALED, T=6, E=48), 3, True),
+                           (dict(SCALED, T=6, E=48, H=7168), 3, False)):
         d = _layer(**kw)
-        need = 4 * d.I * (d.T * (k + d.n_shared) + 1) + 16 * d.T * d.E
+        rows = d.T * (k + d.n_shared)
+        need = (40 * rows * d.I if on_chip else 4 * (rows + 1) * d.I) + 32 * d.T * d.E
         size = moe.moe_few_workspace_size(d, k)
-        assert need <= size <= need + 16 * d.T * 64 + (20 << 10)
+        assert need <= size <= need + 32 * d.T * 64 + (20 << 10)
 
 
 def _gemm(lib, d, a=FAKE, sa=FAKE, b=FAKE, sb=FAKE, out=FAKE):
