@@ -200,6 +200,7 @@ struct FewShared {
   __attribute__((aligned(16))) uint8_t ring[kWaves][kRing];
   floatx4 sums[kSums];
 };
+static_assert(sizeof(FewShared<true>::sums) >= kFewStage, "gate sums of staged assignments");
 static_assert(sizeof(FewShared<true>) <= 160 * 1024, "one block on a CU");
 static_assert(sizeof(FewShared<false>) <= 80 * 1024, "two blocks on a CU");
 
@@ -665,8 +666,12 @@ __device__ __forceinline__ void gate_up_range(const FewArgs& a, const FewTables*
     if (slot >= 0) {
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w)
-        s += red[(w * 2 + v / 16) * kWave + v % 16 / 4 * 16 + t][v % 4];
+      for (int w = 0; w < kWaves; ++w) {
+        // (one read each: for pairs of them the compiler waits for all loads)
+        int i = (w * 2 + v / 16) * kWave + v % 16 / 4 * 16 + t;
+        asm volatile("" : "+v"(i));
+        s += red[i][v % 4];
+      }
       // readers wait for the words themselves to change, so nothing has to be
       // ordered around the stores
       const size_t at_part = ((size_t)slot * n_cg + at.u % n_cg) * kFewParts + r - sp.first(at.u);
@@ -681,70 +686,104 @@ __device__ __forceinline__ unsigned long long peek(const uint32_t* p) {
   return __hip_atomic_load(reinterpret_cast<const unsigned long long*>(p), __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_AGENT);
 }
-// Whether a word of v is unset.
-template <int N>
-__device__ __forceinline__ bool unset(const unsigned long long (&v)[N]) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) top = max(top, max((uint32_t)v[i], (uint32_t)(v[i] >> 32)));
-  return top == kUnset;
+__device__ __forceinline__ bool unset(unsigned long long v) {
+  return max((uint32_t)v, (uint32_t)(v >> 32)) == kUnset;
 }
 
-// All of h' to LDS, from the sums of its parts: row s (an assignment) of 2 I
-// bytes of values and 2 I of rests every 4 I + kPad bytes, 16 zero bytes behind
-// the last row.  By every thread of the block, a unit of an assignment a turn.
-// Waits for the sums that are unset: the ranges that write them have smaller
-// tickets, which blocks take in order and only while they run, so each such
-// range has ended or is running in a block that waits for nothing, and the wait
-// ends.
+// All of h' to LDS, from the sums of its parts: row s (an assignment) every 4 I
+// + kPad bytes, 8 columns' values (16 bytes), then their rests; 16 zero bytes
+// behind the last row.  Waits for the sums that are unset: the ranges that
+// write them have smaller tickets, which blocks take in order and only while
+// they run, so each such range has ended or is running in a block that waits
+// for nothing, and the wait ends.
+//
+// First the sums, four floats an item, three items and two parts of each at a
+// time, as they come from beyond this XCD's L2: gate sums to `gates`, up sums
+// to where their columns' h' goes; then h', two columns a lane.  Loops that
+// stay loops: all this runs once, and is fetched from memory.
 template <bool FP8>
 __device__ __forceinline__ void stage_h(const FewArgs& a, const FewTables* __restrict__ tb,
-                                        const FewSplit& sp, uint8_t* __restrict__ hs) {
-  constexpr int kCols = few_cols(FP8), kValues = 2 * kCols;
-  const int I = a.I, kk = a.k + a.ns, n_cg = I / kCols, total = a.T * kk * n_cg;
+                                        const FewSplit& sp, uint8_t* __restrict__ hs,
+                                        float* __restrict__ gates) {
+  constexpr int kCols = few_cols(FP8), kValues = 2 * kCols, kPer = kValues / 4, kItems = 3;
+  const int I = a.I, kk = a.k + a.ns, n_cg = I / kCols, total = a.T * kk * n_cg * kPer;
   const int row_bytes = 4 * I + kPad;
 #pragma unroll 1
-  for (int j = threadIdx.x; j < total; j += kThreads) {
-    const int slot = j / n_cg, cg = j - slot * n_cg, t = slot / kk;
-    if (tb->bad[t] || (a.valid != nullptr && a.valid[t] == 0)) continue;
-    const int u = tb->place[tb->pick[slot]] * n_cg + cg, parts = sp.last(u) - sp.first(u) + 1;
-    const uint32_t* p = a.hw + (size_t)j * kFewParts * kValues;
-    float sum[kValues];
+  for (int j0 = threadIdx.x; j0 < total; j0 += kItems * kThreads) {
+    const uint32_t* p[kItems];
+    int parts[kItems];
+    floatx4 sum[kItems];
 #pragma unroll
-    for (int i = 0; i < kValues; ++i) sum[i] = 0.f;
-#pragma unroll 1
-    for (int q = 0; q < parts; ++q, p += kValues) {
-      unsigned long long v[kValues / 2];
-      for (;;) {
-#pragma unroll
-        for (int i = 0; i < kValues / 2; ++i) v[i] = peek(p + 2 * i);
-        if (!unset(v)) break;
-      }
-#pragma unroll
-      for (int i = 0; i < kValues / 2; ++i) {
-        sum[2 * i] += __uint_as_float((uint32_t)v[i]);
-        sum[2 * i + 1] += __uint_as_float((uint32_t)(v[i] >> 32));
+    for (int i = 0; i < kItems; ++i) {
+      const int j = j0 + i * kThreads, s = j / kPer, slot = s / n_cg, t = slot / kk;
+      parts[i] = 0;
+      p[i] = a.hw + (size_t)s * kFewParts * kValues + j % kPer * 4;
+      sum[i] = floatx4{0.f, 0.f, 0.f, 0.f};
+      if (j < total && !tb->bad[t] && (a.valid == nullptr || a.valid[t] != 0)) {
+        const int u = tb->place[tb->pick[slot]] * n_cg + s - slot * n_cg;
+        parts[i] = sp.last(u) - sp.first(u) + 1;
       }
     }
-    const float w = tb->w[t][slot - t * kk];
-    uint8_t* to = hs + slot * row_bytes + 2 * kCols * cg;
+#pragma unroll 1
+    for (int q = 0; q < kFewParts; q += 2) {
+      if (!__any(max(max(parts[0], parts[1]), parts[2]) > q)) break;
+      static_assert(kItems == 3, "of parts");
+      unsigned long long v[kItems][2][2];
+      bool wait;
+#pragma unroll 1
+      do {
+        wait = false;
 #pragma unroll
-    for (int i = 0; i < kCols; i += 8) {
-      u32x4 hi, lo;
+        for (int i = 0; i < kItems; ++i)
+          if (q < parts[i])
 #pragma unroll
-      for (int c = 0; c < 8; c += 2) {
-        uint32_t h0, l0, h1, l1;
-        split_h(silu_mul(sum[i + c], sum[kCols + i + c]) * w, h0, l0);
-        split_h(silu_mul(sum[i + c + 1], sum[kCols + i + c + 1]) * w, h1, l1);
-        hi[c / 2] = h0 | h1 << 16;
-        lo[c / 2] = l0 | l1 << 16;
-      }
-      *reinterpret_cast<u32x4*>(to + 2 * i) = hi;
-      *reinterpret_cast<u32x4*>(to + 2 * I + 2 * i) = lo;
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t* from = p[i] + min(q + h, parts[i] - 1) * kValues;
+              v[i][h][0] = peek(from);
+              v[i][h][1] = peek(from + 2);
+            }
+#pragma unroll
+        for (int i = 0; i < kItems; ++i)
+          if (q < parts[i])
+#pragma unroll
+            for (int h = 0; h < 2; ++h) wait |= unset(v[i][h][0]) || unset(v[i][h][1]);
+      } while (__any(wait));
+#pragma unroll
+      for (int i = 0; i < kItems; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (q + h < parts[i])
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              sum[i][k] += __uint_as_float((uint32_t)(v[i][h][k / 2] >> (k % 2 * 32)));
+    }
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int j = j0 + i * kThreads, s = j / kPer, slot = s / n_cg, c = j % kPer * 4;
+      float* to = c < kCols ? gates + s * kCols + c
+                            : reinterpret_cast<float*>(hs + slot * row_bytes) +
+                                  (s - slot * n_cg) * kCols + c - kCols;
+      if (parts[i] > 0) *reinterpret_cast<floatx4*>(to) = sum[i];
     }
   }
   if (threadIdx.x == 0)
     *reinterpret_cast<u32x4*>(hs + a.T * kk * row_bytes) = u32x4{0u, 0u, 0u, 0u};
+  __syncthreads();
+  // (the four lanes of 8 columns, of one wave, read before they write)
+#pragma unroll 1
+  for (int j = threadIdx.x; j < a.T * kk * (I / 2); j += kThreads) {
+    const int slot = j / (I / 2), c = 2 * (j - slot * (I / 2)), t = slot / kk;
+    uint8_t* row = hs + slot * row_bytes;
+    const float* g = gates + slot * I + c;
+    const float* u = reinterpret_cast<const float*>(row) + c;
+    const float w = tb->w[t][slot - t * kk];
+    uint32_t h0, l0, h1, l1;
+    split_h(silu_mul(g[0], u[0]) * w, h0, l0);
+    split_h(silu_mul(g[1], u[1]) * w, h1, l1);
+    uint32_t* to = reinterpret_cast<uint32_t*>(row) + c / 8 * 8 + c % 8 / 2;
+    to[0] = h0 | h1 << 16;
+    to[4] = l0 | l1 << 16;
+  }
 }
 
 // A down unit's loads and sums of one wave, W2 by way of LDS.
@@ -759,7 +798,7 @@ struct DownStaged {
   uint32_t wl;
   int cpe;             // chunks of an expert
   int ai, q;           // the next chunk to load: chosen expert, chunk of it
-  int row_bytes, zeros, low;
+  int row_bytes, zeros;
   floatx4 acc[2], part[2];
 
   __device__ __forceinline__ void issue(uint8_t* __restrict__ to, const FewTables* __restrict__ tb) {
@@ -780,8 +819,8 @@ struct DownStaged {
     if constexpr (FP8) sc = *scale;
 #pragma unroll
     for (int u = 0; u < WC::kSteps; ++u) {
-      const uint8_t* hr = hs + (slot >= 0 ? slot * row_bytes + 2 * (cq * 32 * WC::kSteps + WC::k_of(u, g)) : zeros);
-      const u32x4 hi = ld16(hr), lo = ld16(hr + (slot >= 0 ? low : 0));
+      const uint8_t* hr = hs + (slot >= 0 ? slot * row_bytes + 4 * (cq * 32 * WC::kSteps + WC::k_of(u, g)) : zeros);
+      const u32x4 hi = ld16(hr), lo = ld16(hr + (slot >= 0 ? 16 : 0));
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
         const bf16x8 w = WC::get(cur + 1024 * nt, u, lane);
@@ -828,8 +867,8 @@ __device__ __forceinline__ void store_out(const FewArgs& a, const FewTables* __r
 template <bool FP8, bool PW>
 __device__ __forceinline__ void down_unit_staged(const FewArgs& a, const FewTables* __restrict__ tb,
                                                  const FewSplit& sp, uint8_t* __restrict__ hs,
-                                                 uint8_t* __restrict__ ring, bool staged, int c0,
-                                                 int& next) {
+                                                 uint8_t* __restrict__ ring, floatx4* __restrict__ sums,
+                                                 bool staged, int c0, int& next) {
   using DS = DownStaged<FP8, PW>;
   using WC = typename DS::WC;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
@@ -843,7 +882,6 @@ __device__ __forceinline__ void down_unit_staged(const FewArgs& a, const FewTabl
   d.cpe = I / (32 * WC::kSteps);
   d.row_bytes = 4 * I + kPad;
   d.zeros = a.T * (a.k + a.ns) * d.row_bytes;
-  d.low = 2 * I;
 #pragma unroll
   for (int nt = 0; nt < 2; ++nt) d.acc[nt] = d.part[nt] = floatx4{0.f, 0.f, 0.f, 0.f};
   const int n = __builtin_amdgcn_readfirstlane(tb->n_act) * (d.cpe / GC);
@@ -856,7 +894,7 @@ __device__ __forceinline__ void down_unit_staged(const FewArgs& a, const FewTabl
   for (int i = 0; i < DS::kAhead; ++i)
     if (s0 + i < s1) d.issue(mine + i * DS::kEntry, tb);
   if (threadIdx.x == 0) next = take_ticket(a.ticket);
-  if (!staged) stage_h<FP8>(a, tb, sp, hs);
+  if (!staged) stage_h<FP8>(a, tb, sp, hs, reinterpret_cast<float*>(sums));
   __syncthreads();
   int at = 0;
 #pragma unroll 1
@@ -1062,7 +1100,7 @@ void few_experts_kernel(FewArgs a) {
       if (tk < n_up) {
         gate_up_range<FP8, PW>(a, &sh.tb, sh.stage, &sh.ring[0][0], sh.sums, sp, tk, next);
       } else {
-        down_unit_staged<FP8, PW>(a, &sh.tb, sp, sh.stage, &sh.ring[0][0], h_staged,
+        down_unit_staged<FP8, PW>(a, &sh.tb, sp, sh.stage, &sh.ring[0][0], sh.sums, h_staged,
                                   (tk - n_up) * kDownCols, next);
         h_staged = true;
       }
