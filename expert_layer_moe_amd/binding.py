@@ -308,10 +308,10 @@ def _enqueue(entry, device: int, stream, *args):
 
 
 def _empty(shape, dtype, device, stream):
-    """A new tensor for a result written on `stream` (its memory is reused in
-    that stream's order)."""
+    """A new tensor [rows, columns] for a result written on `stream` (its
+    memory is reused in that stream's order)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
@@ -319,12 +319,13 @@ def _empty(shape, dtype, device, stream):
 def _row_stride(t: torch.Tensor, name: str, dtypes, rows: int, cols: int) -> int:
     """Row stride of a rows x cols matrix with contiguous rows (0: one row,
     whose stride says nothing)."""
-    if not (t.dtype in dtypes and t.dim() == 2 and t.size(0) == rows and t.size(1) == cols):
+    if t.dtype not in dtypes or t.shape != (rows, cols):
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected "
                          f"{' or '.join(map(str, dtypes))} ({rows}, {cols})")
-    if cols > 1 and t.stride(1) != 1:
+    row, col = t.stride()
+    if col != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.stride(0) if rows > 1 else 0
+    return row if rows > 1 else 0
 
 
 _CODES = (torch.uint8, torch.float8_e4m3fn)
@@ -394,12 +395,14 @@ def moe_gemm_fp8(a, a_scale, b, b_scale, out=None, out_dtype=torch.bfloat16, str
     lda = _row_stride(a, "a", _CODES, M, K)
     ldb = _row_stride(b, "b", _CODES, N, K)
     ld_as = _row_stride(a_scale, "a_scale", _F32, M, nb)
-    _row_stride(b_scale, "b_scale", _F32, (N + 127) // 128, nb)
-    if not b_scale.is_contiguous():
+    if _row_stride(b_scale, "b_scale", _F32, (N + 127) // 128, nb) not in (0, nb):
         raise ValueError("b_scale must be contiguous")
     if out is None:
-        out = _empty((M, N), out_dtype, a.device, stream)
-    ldo = _row_stride(out, "out", _FLOATS, M, N)
+        if out_dtype not in _FLOATS:
+            raise ValueError(f"out_dtype {out_dtype}: float32 or bfloat16 expected")
+        out, ldo = _empty((M, N), out_dtype, a.device, stream), 0
+    else:
+        ldo = _row_stride(out, "out", _FLOATS, M, N)
     _enqueue(load_library().moe_gemm_fp8, _device_of(a, a_scale, b, b_scale, out), stream,
              moe_gemm_desc(M, N, K, _DT[out.dtype], lda, ldb, ld_as, ldo), a.data_ptr(),
              a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), out.data_ptr())
@@ -413,11 +416,13 @@ def _quant(entry, x, per_col, codes, scales, stream):
     nb = (cols + 127) // 128
     ld_in = _row_stride(x, "input", _FLOATS, M, cols * per_col)
     if codes is None:
-        codes = _empty((M, cols), torch.uint8, x.device, stream)
+        codes, ld_codes = _empty((M, cols), torch.uint8, x.device, stream), 0
+    else:
+        ld_codes = _row_stride(codes, "codes", _CODES, M, cols)
     if scales is None:
-        scales = _empty((M, nb), torch.float32, x.device, stream)
-    ld_codes = _row_stride(codes, "codes", _CODES, M, cols)
-    ld_scales = _row_stride(scales, "scales", _F32, M, nb)
+        scales, ld_scales = _empty((M, nb), torch.float32, x.device, stream), 0
+    else:
+        ld_scales = _row_stride(scales, "scales", _F32, M, nb)
     _enqueue(entry, _device_of(x, codes, scales), stream,
              moe_quant_desc(M, cols, _DT[x.dtype], ld_in, ld_codes, ld_scales), x.data_ptr(),
              codes.data_ptr(), scales.data_ptr())
