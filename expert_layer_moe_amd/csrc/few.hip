@@ -1,17 +1,27 @@
-// The whole expert layer for a few token rows (at most 16) in two launches.
+// The whole expert layer for a few token rows (at most 16) in two launches, or
+// three.
 //
 // A decode step of one or a few sequences reads each chosen expert's weights
-// once for one or two rows: k experts of 3 I H weights a token, a few tens of
-// MB, a few microseconds of HBM time, so launches and dependences count as
-// much as bytes.  few_logits_kernel computes the router logits (and clears
-// what the second launch counts in); few_experts_kernel does the rest: every
-// block forms the top-k itself (T rows of E logits, cheaper than another
-// launch), then takes units from a ticket counter, first the gate/up units
-//   h'(t, j)[c] = w(t, j) SiLU(W_gate x_t)[c] (W_up x_t)[c]   (8 columns c)
-// and then the down units
-//   out[t][n] = sum over experts and c of W2_e[n][c] h'(t, j)[c]  (32 columns n).
+// once for one or two rows: k experts of 3 I H weights a token, tens of MB, so
+// launches and dependences count as much as bytes.  few_logits_kernel computes
+// the router logits (and clears what the next launch counts in).  In
+// few_experts_kernel every block forms the top-k itself (T rows of E logits,
+// cheaper than another launch), then takes work from a ticket counter:
+//   h'(t, j)[c] = w(t, j) SiLU(W_gate x_t)[c] (W_up x_t)[c]
+//   out[t][n]   = sum over experts and c of W2_e[n][c] h'(t, j)[c]
 // The routing weight is applied to h', so one accumulator runs over all
 // experts and no per-expert output rows exist.
+//
+// STAGED, the rows and h' fit in a block's LDS (one or two rows of 7168): both products in one launch, the down units waiting for the sums
+// they read.  Otherwise the gate/up units alone, and few_down_kernel after
+// them: with many rows the waits cost more than a launch (16 rows of the 256-
+// expert layer: 248 us in two launches, 199 in three).
+//
+// Bound by HBM.  One row, bf16: 48 experts of I = 640 top-3 (83 MB) 27.8 us,
+// 256 of I = 256 top-8 and a shared one (103 MB) 30.4 us, of which the weights
+// take 16 and 20 at the rate of a large copy; the logits and their launch
+// take 5, the top-k in every block 4, the handover of h' 3.  16 rows, row-major
+// (1.14 GB): 207 us, 5.5 TB/s.
 #include "moe_common.h"
 #include "moe_kernels.h"
 
@@ -50,9 +60,10 @@ __device__ __forceinline__ void split_h(float v, uint32_t& hi, uint32_t& lo) {
   else if (hi & 0x7fu) hi = 0x7fc0u;   // NaN
 }
 
-// part[z][t][e] (rows few_logit_stride(E) apart): router logits over the z-th part of K (the 8 waves of a
-// block split that part again and meet in LDS), 16 experts per block; the
-// second launch adds the parts up.  Rows with valid == 0 are not read.  Also
+// part[z][t][e] (rows few_logit_stride(E) apart): router logits over the z-th
+// part of K (the 8 waves of a block split that part again and meet in LDS), 16
+// experts per block; the second launch adds the parts up.  (8 parts, 128 blocks
+// for 256 experts: with 4, one row took 36.7 us in all in place of 34.8.)  Rows with valid == 0 are not read.  Also
 // zeroes the ticket counter and marks the sums unset (STAGED) or zeroes the
 // zero rows of h' (rows of I).
 __global__ __launch_bounds__(kThreads) void few_logits_kernel(
@@ -562,8 +573,9 @@ __device__ __forceinline__ void gate_up_unit(const FewArgs& a, const FewTables* 
 }
 
 // A range of the gate/up units' 128-wide blocks of K, unit after unit, STAGED:
-// the calls' few units would not go evenly into the chip's CUs, so each block
-// takes an equal share of all their blocks instead, at most kFewParts of them
+// the calls' few units would not go evenly into the chip's CUs (288 into 256
+// for one row of the 256-expert layer: 34.8 us, with equal shares 30.4), so each
+// block takes an equal share of all their blocks instead, at most kFewParts of them
 // sharing a unit.  Every wave takes its part of each unit's blocks in the range
 // (a segment) as one stream: the ring runs on from segment to segment, only the
 // sums stop, for the block to add the waves' up and send them to memory.
@@ -912,7 +924,8 @@ __device__ __forceinline__ void down_unit_staged(const FewArgs& a, const FewTabl
 }
 
 // Calls whose rows and h' do not fit in LDS have their down product in a
-// launch of its own, where h' is read like any other memory.
+// launch of its own, where h' is read like any other memory: 16 rows of the
+// 256-expert layer, 378 MB of W2, 58 us packed (6.5 TB/s), 64 row-major.
 //
 // A wave's loads and sums: NT tiles of 16 columns, W2 by way of LDS, h' in
 // registers, both kAhead chunks ahead.

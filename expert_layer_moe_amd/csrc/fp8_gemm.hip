@@ -14,6 +14,12 @@
 // (measured: 1.5e-5 of a random sum, up to 7e-5 of a sum of one sign), far
 // below the rounding of a bf16 result.  For fp32 results the codes become
 // bf16, exactly, and four bf16 MFMAs add up the block in fp32 (F32 below).
+//
+// Measured (bf16 results): 8192 x 4096 x 7168 219 us, 2.19 PFLOP/s, where the
+// card's library product of the same size, with one scale for all, takes 169:
+// the matrix cores are busy 49 % of the cycles.  Without the FMAs it would take
+// a tenth less, without the loads a fifth, with zeros for operands 200 us.
+// 1000 x 7168 x 2048 20.5 us; 1 x 4096 x 7168, 29 MB, 8.5 us (3.4 TB/s).
 #include "moe_common.h"
 #include "moe_kernels.h"
 
