@@ -325,7 +325,11 @@ def _row_stride(t: torch.Tensor, name: str, dtypes, rows: int, cols: int) -> int
     row, col = t.stride()
     if col != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return row if rows > 1 else 0
+    if rows == 1:
+        return 0
+    if row < cols:
+        raise ValueError(f"{name} has rows that overlap (stride {row})")
+    return row
 
 
 _CODES = (torch.uint8, torch.float8_e4m3fn)

@@ -3,6 +3,7 @@ moe_forward calls (memory management only; the math is in the kernels)."""
 from __future__ import annotations
 
 import ctypes
+import threading
 from typing import Optional
 
 import torch
@@ -50,7 +51,7 @@ class DeviceLayer:
         self.device = device
         self.block_m = block_m
         self._ws = {}
-        self._few_ws, self._few = {}, {}
+        self._few_ws, self._few, self._few_lock = {}, {}, threading.Lock()
         self.layout = MOE_LAYOUT_ROW_MAJOR
         if packed:
             self.w13, self.w2 = moe_pack_weights(self.desc(1), self.w13, self.w2)
@@ -78,15 +79,16 @@ class DeviceLayer:
         """Workspace of forward_few, one per row count and stream (calls on one
         stream follow each other); a new one while a graph is captured, so that
         graphs do not share it with each other or with eager calls."""
-        if torch.cuda.is_current_stream_capturing():
+        if stream is not None:
             with torch.cuda.stream(stream):
-                return alloc_few_workspace(self.desc(T), self.topk, self.router.device)
-        raw = torch._C._cuda_getCurrentRawStream(self.router.get_device()) if stream is None \
-            else stream.cuda_stream
-        ws = self._few_ws.get((T, raw))
+                return self.few_workspace(T)
+        if torch.cuda.is_current_stream_capturing():
+            return alloc_few_workspace(self.desc(T), self.topk, self.router.device)
+        key = T, torch._C._cuda_getCurrentRawStream(self.router.get_device())
+        ws = self._few_ws.get(key)
         if ws is None:
-            ws = alloc_few_workspace(self.desc(T), self.topk, self.router.device)
-            self._few_ws[T, raw] = ws
+            ws = self._few_ws[key] = alloc_few_workspace(self.desc(T), self.topk,
+                                                         self.router.device)
         return ws
 
     def forward_few(self, x, valid=None, out=None, workspace=None, stream=None):
@@ -99,10 +101,13 @@ class DeviceLayer:
             few = self._few[T] = (d, ctypes.byref(d))
         if out is None:
             out = _empty((T, self.H), x.dtype, x.device, stream)
-        ws = workspace if workspace is not None else self.few_workspace(T, stream)
-        _forward_few(few[1], T, self.H, self.router.dtype, self.router.get_device(), x, valid,
-                     self.router.data_ptr(), self.w13.data_ptr(), self.w2.data_ptr(), self.topk,
-                     out, ws, stream)
+        # threads that call on one stream share its workspace: a call's launches
+        # stay together
+        with self._few_lock:
+            ws = workspace if workspace is not None else self.few_workspace(T, stream)
+            _forward_few(few[1], T, self.H, self.router.dtype, self.router.get_device(), x, valid,
+                         self.router.data_ptr(), self.w13.data_ptr(), self.w2.data_ptr(),
+                         self.topk, out, ws, stream)
         return out
 
     def block_signals(self, T: int) -> torch.Tensor:

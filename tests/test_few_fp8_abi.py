@@ -158,16 +158,20 @@ def _codes(*shape):
     dict(a_scale=torch.ones(4, 2)), dict(a_scale=torch.ones(4, 1).double()),
     dict(b_scale=torch.ones(2, 1)), dict(out=torch.empty(4, 9)),
     dict(out=torch.empty(4, 8).half()), dict(out=torch.empty(8, 4).t()),
-    dict(a=_codes(128, 4).t()), dict(),
+    dict(a=_codes(128, 4).t()), dict(a=_codes(1, 128).expand(4, 128)),
+    dict(a_scale=torch.ones(1, 1).expand(4, 1)), dict(out=torch.empty(1, 8).expand(4, 8)),
+    dict(b=_codes(1, 128).expand(8, 128)), dict(),
 ])
 def test_binding_refuses_products(change):
-    """Wrong shapes, types and orders; right ones (the last) are refused for
+    """Wrong shapes, types and orders, broadcast rows (a stride of 0, which the
+    descriptor reads as dense); right ones (the last) are refused for
     not being on a GPU."""
     args = dict(a=_codes(4, 128), a_scale=torch.ones(4, 1), b=_codes(8, 128),
                 b_scale=torch.ones(1, 1))
     args.update(change)
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError) as refusal:
         moe.moe_gemm_fp8(**args)
+    assert ("on the GPU" in str(refusal.value)) == (not change)
 
 
 @pytest.mark.parametrize("fn, x, kw", [
@@ -177,12 +181,19 @@ def test_binding_refuses_products(change):
     (moe.moe_quant_fp8, torch.zeros(2, 128), dict(codes=_codes(2, 64))),
     (moe.moe_quant_fp8, torch.zeros(2, 128), dict(scales=torch.zeros(2, 2))),
     (moe.moe_quant_fp8, torch.zeros(2, 128), {}),
+    (moe.moe_quant_fp8, torch.zeros(1, 128).expand(4, 128), {}),
+    (moe.moe_quant_fp8, torch.zeros(600).as_strided((4, 128), (64, 1)), {}),
+    (moe.moe_quant_fp8, torch.zeros(4, 128), dict(codes=_codes(1, 128).expand(4, 128))),
+    (moe.moe_silu_mul_quant_fp8, torch.zeros(1, 256).expand(4, 256), {}),
     (moe.moe_silu_mul_quant_fp8, torch.zeros(2, 33), {}),
     (moe.moe_silu_mul_quant_fp8, torch.zeros(2, 256), {}),
 ])
 def test_binding_refuses_quantisations(fn, x, kw):
-    with pytest.raises(ValueError):
+    good = not kw and x.is_contiguous() and x.dim() == 2 and x.dtype == torch.float32 \
+        and x.shape[1] % 2 == 0
+    with pytest.raises(ValueError) as refusal:
         fn(x, **kw)
+    assert ("on the GPU" in str(refusal.value)) == good
 
 
 def test_binding_refuses_layers():

@@ -281,6 +281,55 @@ def test_two_graphs_of_a_layer(T):
             assert torch.equal(o, e)
 
 
+def test_graph_captured_on_a_stream_given_by_name():
+    """A capture on a stream that is passed along while it is not the current
+    one: its workspace is not the one of eager calls there."""
+    layer = Layer(13, 1024, 12, 64, 3)
+    x = layer.rows(5).cuda()
+    s = torch.cuda.Stream()
+    want = layer.dev.forward_few(x)
+    layer.dev.forward_few(x, stream=s)
+    torch.cuda.synchronize()
+    out = torch.empty_like(x)
+    eager_ws = layer.dev.few_workspace(5, s).data_ptr()
+    seen = []
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        ws = layer.dev.few_workspace(5, s)
+        seen.append(ws.data_ptr())
+        layer.dev.forward_few(x, out=out, workspace=ws, stream=s)
+    assert seen[0] != eager_ws
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        other = layer.dev.forward_few(x, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(other, want)
+
+
+def test_threads_on_one_stream():
+    """Calls of one layer from several threads, all on one stream."""
+    import threading
+    layer = Layer(14, 1024, 24, 96, 3, packed=True)
+    xs = [layer.rows(4).cuda() for _ in range(4)]
+    want = [layer.dev.forward_few(x) for x in xs]
+    torch.cuda.synchronize()
+    got = [[] for _ in xs]
+
+    def work(i):
+        for _ in range(50):
+            got[i].append(layer.dev.forward_few(xs[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(4):
+        assert len(got[i]) == 50 and all(torch.equal(o, want[i]) for o in got[i])
+
+
 def test_binding_call():
     """moe_forward_few as the C ABI has it: descriptor, weights, workspace."""
     layer = Layer(12, 256, 6, 64, 2, 1)
