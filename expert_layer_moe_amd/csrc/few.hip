@@ -172,6 +172,16 @@ __device__ __forceinline__ void to_lds16(__amdgpu_buffer_rsrc_t src, uint32_t la
                                              lane_offset, offset, 0, 0);
 }
 
+// A float at buffer + offset, the same for all lanes, by way of the vector
+// cache: a scalar load would have to be waited for with the next LDS read.
+__device__ __forceinline__ float load_float(__amdgpu_buffer_rsrc_t src, uint32_t offset) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(src, offset, 0, 0));
+}
+__device__ __forceinline__ void to_lds4(__amdgpu_buffer_rsrc_t src, uint32_t lane_offset, void* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)dst, 4,
+                                           lane_offset, 0, 0, 0);
+}
+
 // Waits until at most N of the wave's loads are outstanding and its LDS reads
 // are done; no memory access moves across.
 template <int N>
@@ -179,6 +189,15 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt((N & 15) | 7 << 4 | (N >> 4) << 14);
   asm volatile("" ::: "memory");
+}
+
+// For chunk set i, with AHEAD chunks of N loads behind it, and MORE in every odd
+// set (the scales, of two chunks each); i a constant.
+template <int AHEAD, int N, int MORE>
+__device__ __forceinline__ void wait_chunk(int i) {
+  static_assert(MORE == 0 || AHEAD % 2 == 1, "sets in pairs");
+  if (i % 2 == 0) wait_loads<AHEAD * N + (AHEAD + 1) / 2 * MORE>();
+  else wait_loads<AHEAD * N + AHEAD / 2 * MORE>();
 }
 
 struct FewTables {
@@ -205,11 +224,16 @@ template <bool STAGED>
 struct FewShared {
   static constexpr int kStage = STAGED ? kFewStage : 16, kRing = STAGED ? 10 * 1024 : 8 * 1024;
   static constexpr int kSums = STAGED ? 2 * kWaves * 2 * kWave : 1;
+  // fp8: scales of the units of a range (kFewStage bounds them: at most 512
+  // units of at most 127 blocks, 256 ranges), and of a down unit's experts
+  static constexpr int kUnits = 3, kBlocks = 128, kDown = kFewStage / 4 / 128;
   FewTables tb;
   int tk;   // the block's next ticket
   __attribute__((aligned(16))) uint8_t stage[kStage];
   __attribute__((aligned(16))) uint8_t ring[kWaves][kRing];
   floatx4 sums[kSums];
+  float up_scales[STAGED ? kUnits : 1][2][STAGED ? kBlocks : 1];
+  float down_scales[STAGED ? kDown : 1];
 };
 static_assert(sizeof(FewShared<true>::sums) >= kFewStage, "gate sums of staged assignments");
 static_assert(sizeof(FewShared<true>) <= 160 * 1024, "one block on a CU");
@@ -388,9 +412,9 @@ struct GateUp {
   static constexpr int kLoads = NT * WC::kParts, kEntry = 1024 * kLoads;   // of a chunk's weights
   static constexpr int kSets = FewShared<STAGED>::kRing / kEntry, kAhead = kSets - 1;
   static constexpr int kXSets = STAGED ? 1 : kSets;
-  __amdgpu_buffer_rsrc_t wbuf[NT], xbuf;
+  __amdgpu_buffer_rsrc_t wbuf[NT], xbuf, sbuf;
   uint32_t wl[WC::kParts], xl[WC::kSteps];
-  const float* sp[NT];
+  uint32_t so[NT];   // byte offsets of the unit's scales in sbuf
   floatx4 acc[NT], part[NT];
   u32x4 x[kXSets][WC::kSteps];
   float sc[kXSets][NT];
@@ -407,9 +431,9 @@ struct GateUp {
       for (int u = 0; u < WC::kSteps; ++u)
         x[set][u] = __builtin_bit_cast(
             u32x4, __builtin_amdgcn_raw_buffer_load_b128(xbuf, xl[u], c * (64 * WC::kSteps), 0));
-      if constexpr (FP8)
+      if (FP8 && set % 2 == 1)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) sc[set][n] = sp[n][c / 2];
+        for (int n = 0; n < NT; ++n) sc[set][n] = load_float(sbuf, so[n] + c / 2 * 4);
     }
   }
   // The sums of the chunk in `cur`, x and scales in set `set`; fp8: scaled up
@@ -434,11 +458,12 @@ struct GateUp {
   }
   // STAGED: chunk c out of `cur`.
   __device__ __forceinline__ void step_staged(const uint8_t* __restrict__ cur,
-                                              const uint8_t* __restrict__ xs, int c, bool xv,
+                                              const uint8_t* __restrict__ xs,
+                                              const float* __restrict__ scales, int c, bool xv,
                                               int lane) {
     if constexpr (FP8)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) sc[0][n] = sp[n][c / 2];
+      for (int n = 0; n < NT; ++n) sc[0][n] = scales[n * FewShared<true>::kBlocks + c / 2];
 #pragma unroll
     for (int u = 0; u < WC::kSteps; ++u)
       x[0][u] = ld16(xs + (xv ? 2 * (c * 32 * WC::kSteps + WC::k_of(u, lane / 16)) : 0));
@@ -452,7 +477,7 @@ struct GateUp {
     if constexpr (LOAD) {
       wait_loads<63>();   // the reads of the chunk that is loaded over
       issue(to, c, (i + kAhead) % kSets);
-      wait_loads<kAhead * (kLoads + WC::kSteps)>();
+      wait_chunk<kAhead, kLoads + WC::kSteps, FP8 ? NT : 0>(i);
     }
     multiply(cur, lane, i, i % 2 == 1);
   }
@@ -485,15 +510,9 @@ __device__ __forceinline__ void at_unit(GateUp<FP8, PW, STAGED>& gu, const FewAr
     else gu.wl[p] = WC::load_offset(lane) + (c0 % 16 + lr) * H * kSize + p * up_rows;
   }
 }
-// And the scales of its sums, which start at zero.
-template <bool FP8, bool PW, bool STAGED>
-__device__ __forceinline__ void start_sums(GateUp<FP8, PW, STAGED>& gu, const FewArgs& a, int e, int c0) {
-  const int H = a.H, I = a.I;
-#pragma unroll
-  for (int n = 0; n < GateUp<FP8, PW, STAGED>::NT; ++n) {
-    gu.sp[n] = FP8 ? a.s13 + ((size_t)e * (2 * I / 128) + (n * I + c0) / 128) * (H / 128) : nullptr;
-    gu.acc[n] = gu.part[n] = floatx4{0.f, 0.f, 0.f, 0.f};
-  }
+// Index of the scales of those columns' gate (n = 0) or up (1) rows.
+__device__ __forceinline__ uint32_t scales_at(const FewArgs& a, int e, int c0, int n) {
+  return (e * (2 * a.I / 128) + (n * a.I + c0) / 128) * (a.H / 128);
 }
 
 // A unit by a block, the waves splitting K = H in 128-wide blocks and meeting
@@ -509,7 +528,12 @@ __device__ __forceinline__ void gate_up_unit(const FewArgs& a, const FewTables* 
   const int H = a.H, I = a.I;
   GU gu;
   at_unit(gu, a, lane, e, c0);
-  start_sums(gu, a, e, c0);
+  gu.sbuf = buffer_at(a.s13);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    gu.so[n] = 4 * scales_at(a, e, c0, n);
+    gu.acc[n] = gu.part[n] = floatx4{0.f, 0.f, 0.f, 0.f};
+  }
   const bool xv = tb->slot[e][m] >= 0;
   // rows that did not choose e: zeros
   gu.xbuf = buffer_at(a.x, 2 * a.T * H);
@@ -523,7 +547,10 @@ __device__ __forceinline__ void gate_up_unit(const FewArgs& a, const FewTables* 
     // (behind the last chunk that one again, unused, so that as many loads are
     // on the way at every step)
 #pragma unroll
-    for (int i = 0; i < GU::kAhead; ++i) gu.issue(mine + i * GU::kEntry, min(s0 + i, s1 - 1), i);
+    for (int i = 0; i < GU::kAhead; ++i) {
+      gu.issue(mine + i * GU::kEntry, min(s0 + i, s1 - 1), i);
+      __builtin_amdgcn_sched_barrier(0);   // chunk after chunk, as the waits count
+    }
     if (threadIdx.x == 0) next = take_ticket(a.ticket);
     int c = s0;
 #pragma unroll 1
@@ -608,7 +635,8 @@ template <bool FP8, bool PW>
 __device__ __forceinline__ void gate_up_range(const FewArgs& a, const FewTables* __restrict__ tb,
                                               const uint8_t* __restrict__ xs,
                                               uint8_t* __restrict__ ring, floatx4* __restrict__ sums,
-                                              const FewSplit& sp, int r, int& next) {
+                                              float* __restrict__ scales, const FewSplit& sp, int r,
+                                              int& next) {
   using GU = GateUp<FP8, PW, true>;
   using WC = typename GU::WC;
   constexpr int NT = GU::NT, kCols = few_cols(FP8), kRing = FewShared<true>::kRing;
@@ -632,6 +660,15 @@ __device__ __forceinline__ void gate_up_range(const FewArgs& a, const FewTables*
       at_unit(gu, a, lane, expert(ld.u), column(ld.u));
     }
   };
+  constexpr int kUnits = FewShared<true>::kUnits, kBlocks = FewShared<true>::kBlocks;
+  if constexpr (FP8) {
+    // the scales of the range's units, gate or up of one by a wave
+    const int u = min(ld.u + wave / 2, (r1 - 1) / nb);
+    const uint32_t first = scales_at(a, expert(u), column(u), wave % 2);
+    if (wave < 2 * kUnits)
+      for (int i = 0; i < nb; i += kWave)
+        to_lds4(buffer_at(a.s13), 4 * (first + min(i + lane, nb - 1)), scales + wave * kBlocks + i);
+  }
   ld.segment(r0, nb, cpb, wave);
   at_unit(gu, a, lane, expert(ld.u), column(ld.u));
   settle();
@@ -642,13 +679,22 @@ __device__ __forceinline__ void gate_up_range(const FewArgs& a, const FewTables*
     ++ahead;
     settle();
   }
+  if constexpr (FP8) {
+    // (what is behind a wave's scales: its ring)
+    if (ahead == GU::kAhead) wait_loads<GU::kAhead * GU::kLoads>();
+    else wait_loads<0>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  }
   if (threadIdx.x == 0) next = take_ticket(a.ticket);
   int from = 0, side = 0;
+  const int u0 = at.u;
 #pragma unroll 1
   for (; at.u * nb < r1; ++at.u) {
-    const int e = expert(at.u), c0 = column(at.u);
+    const int e = expert(at.u);
     at.segment(r0, nb, cpb, wave);
-    start_sums(gu, a, e, c0);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) gu.acc[n] = gu.part[n] = floatx4{0.f, 0.f, 0.f, 0.f};
     const bool xv = tb->slot[e][m] >= 0;
     // a lane without a row reads the 16 zero bytes behind them
     const uint8_t* xl = xs + (xv ? m * (2 * a.H + kPad) : a.T * (2 * a.H + kPad));
@@ -662,7 +708,7 @@ __device__ __forceinline__ void gate_up_range(const FewArgs& a, const FewTables*
         ++ahead;
         settle();
       }
-      gu.step_staged(mine + from * GU::kEntry, xl, c, xv, lane);
+      gu.step_staged(mine + from * GU::kEntry, xl, scales + (at.u - u0) * 2 * kBlocks, c, xv, lane);
       from = from + 1 == GU::kSets ? 0 : from + 1;
     }
     floatx4* red = sums + side * (kWaves * 2 * kWave);
@@ -880,7 +926,8 @@ template <bool FP8, bool PW>
 __device__ __forceinline__ void down_unit_staged(const FewArgs& a, const FewTables* __restrict__ tb,
                                                  const FewSplit& sp, uint8_t* __restrict__ hs,
                                                  uint8_t* __restrict__ ring, floatx4* __restrict__ sums,
-                                                 bool staged, int c0, int& next) {
+                                                 float* __restrict__ scales, bool staged, int c0,
+                                                 int& next) {
   using DS = DownStaged<FP8, PW>;
   using WC = typename DS::WC;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
@@ -902,10 +949,18 @@ __device__ __forceinline__ void down_unit_staged(const FewArgs& a, const FewTabl
   d.ai = ai;
   d.q = q;
   uint8_t* mine = ring + wave * FewShared<true>::kRing;
+  // fp8: the scales of the columns' blocks, expert after expert
+  const int n_scales = FP8 ? __builtin_amdgcn_readfirstlane(tb->n_act) * (I / 128) : 0;
+  float sc = 0.f;
+  if (FP8 && threadIdx.x < n_scales) {
+    const int i = threadIdx.x / (I / 128);
+    sc = a.s2[((size_t)tb->act[i] * (H / 128) + c0 / 128) * (I / 128) + threadIdx.x - i * (I / 128)];
+  }
 #pragma unroll
   for (int i = 0; i < DS::kAhead; ++i)
     if (s0 + i < s1) d.issue(mine + i * DS::kEntry, tb);
   if (threadIdx.x == 0) next = take_ticket(a.ticket);
+  if (FP8 && threadIdx.x < n_scales) scales[threadIdx.x] = sc;
   if (!staged) stage_h<FP8>(a, tb, sp, hs, reinterpret_cast<float*>(sums));
   __syncthreads();
   int at = 0;
@@ -916,7 +971,7 @@ __device__ __forceinline__ void down_unit_staged(const FewArgs& a, const FewTabl
     const int to = at == 0 ? DS::kEntries - 1 : at - 1;
     const int e = __builtin_amdgcn_readfirstlane(tb->act[ai]);
     d.step(mine + at * DS::kEntry, mine + to * DS::kEntry, hs, tb, e, q, s + DS::kAhead < s1, lane,
-           a.s2 + ((size_t)e * (H / 128) + c0 / 128) * (I / 128) + q / 2);
+           scales + ai * (I / 128) + q / 2);
     if (++q == d.cpe) q = 0, ++ai;
     at = at + 1 == DS::kEntries ? 0 : at + 1;
   }
@@ -937,7 +992,7 @@ struct Down {
   static constexpr int kSets = WIDE ? 5 - NT : FP8 ? 4 : 8 / NT, kAhead = kSets - 1;
   static constexpr int kLoads = NT * WC::kParts + 2 * WC::kSteps;   // of a chunk
   const uint8_t* w2;      // row c0 of expert 0
-  const float* s2;
+  __amdgpu_buffer_rsrc_t s2;
   const uint16_t* h;
   size_t expert, plane;   // bytes of an expert, values of a plane of h'
   uint32_t tile;          // bytes of 16 rows
@@ -975,7 +1030,8 @@ struct Down {
       hi[set][u] = ld16(p);
       lo[set][u] = ld16(p + plane);
     }
-    if constexpr (FP8) sc[set] = s2[((size_t)e * (H / 128) + c0 / 128) * (I / 128) + q / 2];
+    if (FP8 && set % 2 == 1)
+      sc[set] = load_float(s2, 4 * ((e * (H / 128) + c0 / 128) * (I / 128) + q / 2));
     if (left > 0) {
       --left;
       if (++q == cpe) {
@@ -993,7 +1049,7 @@ struct Down {
     if constexpr (LOAD) {
       wait_loads<63>();   // the reads of the chunk that is loaded over
       issue(to, tb, lane, (set + kAhead) % kSets);
-      wait_loads<kAhead * kLoads>();
+      wait_chunk<kAhead, kLoads, FP8 ? 1 : 0>(set);
     }
 #pragma unroll
     for (int u = 0; u < WC::kSteps; ++u)
@@ -1043,7 +1099,7 @@ __global__ __launch_bounds__((Down<FP8, PW, NT, WIDE>::kWaves * kWave)) void few
   __syncthreads();
   DN d;
   d.w2 = static_cast<const uint8_t*>(a.w2) + (size_t)c0 * I * kSize;
-  d.s2 = a.s2;
+  d.s2 = buffer_at(a.s2);
   d.h = reinterpret_cast<const uint16_t*>(a.hw);
   d.expert = (size_t)H * I * kSize;
   d.plane = 2 * (size_t)a.plane;
@@ -1065,7 +1121,10 @@ __global__ __launch_bounds__((Down<FP8, PW, NT, WIDE>::kWaves * kWave)) void few
     d.left = s1 - s0 - 1;
     d.enter(&sh.tb, lane);
 #pragma unroll
-    for (int i = 0; i < DN::kAhead; ++i) d.issue(mine + i * DN::kEntry, &sh.tb, lane, i);
+    for (int i = 0; i < DN::kAhead; ++i) {
+      d.issue(mine + i * DN::kEntry, &sh.tb, lane, i);
+      __builtin_amdgcn_sched_barrier(0);   // chunk after chunk, as the waits count
+    }
     // whole rounds of the sets, then the rest, which is all loaded
     int s = s0;
 #pragma unroll 1
@@ -1111,9 +1170,11 @@ void few_experts_kernel(FewArgs a) {
     int next = 0;   // the next ticket (thread 0), asked for behind the unit's first loads
     if constexpr (STAGED) {
       if (tk < n_up) {
-        gate_up_range<FP8, PW>(a, &sh.tb, sh.stage, &sh.ring[0][0], sh.sums, sp, tk, next);
+        gate_up_range<FP8, PW>(a, &sh.tb, sh.stage, &sh.ring[0][0], sh.sums,
+                               &sh.up_scales[0][0][0], sp, tk, next);
       } else {
-        down_unit_staged<FP8, PW>(a, &sh.tb, sp, sh.stage, &sh.ring[0][0], sh.sums, h_staged,
+        down_unit_staged<FP8, PW>(a, &sh.tb, sp, sh.stage, &sh.ring[0][0], sh.sums,
+                                  sh.down_scales, h_staged,
                                   (tk - n_up) * kDownCols, next);
         h_staged = true;
       }
