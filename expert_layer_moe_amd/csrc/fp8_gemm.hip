@@ -19,7 +19,8 @@
 // card's library product of the same size, with one scale for all, takes 169:
 // the matrix cores are busy 49 % of the cycles.  Without the FMAs it would take
 // a tenth less, without the loads a fifth, with zeros for operands 200 us.
-// 1000 x 7168 x 2048 20.5 us; 1 x 4096 x 7168, 29 MB, 8.5 us (3.4 TB/s).
+// 1000 x 7168 x 2048 20.5 us; 1 x 4096 x 7168, 29 MB, 7.0 us (4.2
+// TB/s).
 #include "moe_common.h"
 #include "moe_kernels.h"
 
@@ -29,6 +30,7 @@ namespace moe {
 namespace {
 
 typedef __attribute__((__vector_size__(8 * sizeof(int)))) int i32x8;
+typedef __attribute__((__vector_size__(4 * sizeof(int)))) int i32x4;
 
 constexpr int kBK = 128;   // K block
 
@@ -44,6 +46,7 @@ struct Operand;
 template <>
 struct Operand<false> {
   i32x8 v;
+  __device__ __forceinline__ void set(const i32x8& f) { v = f; }
   __device__ __forceinline__ void read(const uint8_t* row, int at0, int at1) {
     set(Frag{{ld16(row + at0), ld16(row + at1)}});
   }
@@ -54,6 +57,10 @@ struct Operand<false> {
 };
 template <>
 struct Operand<true> {
+  __device__ __forceinline__ void set(const i32x8& f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = fp8x8_to_bf16x8((uint32_t)f[2 * i], (uint32_t)f[2 * i + 1]);
+  }
   bf16x8 v[4];
   __device__ __forceinline__ void read(const uint8_t* row, int at0, int at1) {
     set(Frag{{ld16(row + at0), ld16(row + at1)}});
@@ -89,105 +96,27 @@ __device__ __forceinline__ void store4(const Fp8Gemm& p, int m, int n, floatx4 v
   }
 }
 
-// ---- few rows: the weights stream through registers -------------------------------
-// One block per 16 columns and 16 MT rows; its W waves split the K blocks and
-// meet in LDS.  A wave asks for U K blocks at once (past its last one: that
-// one again, not used).  Rows and columns past the end read the last ones,
-// unstored.
-template <int MT, int W, int U, bool F32>
-__global__ __launch_bounds__(W * kWave) void fp8_gemm_rows_kernel(Fp8Gemm p) {
-  __shared__ floatx4 red[W][MT][kWave];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
-  const int r = lane % 16, g = lane / 16;
-  const int blocks_n = (p.N + 15) / 16;
-  const int n0 = (int)(blockIdx.x % blocks_n) * 16, m0 = (int)(blockIdx.x / blocks_n) * (16 * MT);
-  const int nb = (p.K + kBK - 1) / kBK;
-  const uint8_t* wp = p.b + (size_t)min(n0 + r, p.N - 1) * p.ldb + 16 * g;
-  const float* sb = p.sb + (size_t)(n0 / kBK) * nb;
-  const uint8_t* ap[MT];
-  const float* sa[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const size_t m = min(m0 + 16 * t + r, p.M - 1);
-    ap[t] = p.a + m * p.lda + 16 * g;
-    sa[t] = p.sa + m * p.ldsa;
-  }
-  const u32x4 zero = {0u, 0u, 0u, 0u};
-  floatx4 acc[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) acc[t] = floatx4{0.f, 0.f, 0.f, 0.f};
-  const int b0 = (int)((long long)nb * wave / W), b1 = (int)((long long)nb * (wave + 1) / W);
-  for (int b = b0; b < b1; b += U) {
-    Frag wf[U], af[U][MT];
-    float ws[U], as[U][MT];
-    if (min(b + U, b1) * kBK <= p.K) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const size_t k = (size_t)min(b + u, b1 - 1) * kBK;
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          wf[u].p[q] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wp + k + 64 * q));
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const size_t k = (size_t)min(b + u, b1 - 1) * kBK;
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-          for (int q = 0; q < 2; ++q) af[u][t].p[q] = ld16(ap[t] + k + 64 * q);
-      }
-    } else {
-      // K ends inside the last block: its missing pieces are zero
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = min(b + u, b1 - 1) * kBK;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const bool in = k + 64 * q + 16 * g < p.K;
-          wf[u].p[q] = in ? ld16(wp + k + 64 * q) : zero;
-#pragma unroll
-          for (int t = 0; t < MT; ++t) af[u][t].p[q] = in ? ld16(ap[t] + k + 64 * q) : zero;
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int kb = min(b + u, b1 - 1);
-      ws[u] = sb[kb];
-#pragma unroll
-      for (int t = 0; t < MT; ++t) as[u][t] = sa[t][kb];
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (b + u >= b1) break;
-      Operand<F32> wo;
-      wo.set(wf[u]);
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        Operand<F32> ao;
-        ao.set(af[u][t]);
-        const floatx4 d = mfma_block(wo, ao);
-        const float sc = ws[u] * as[u][t];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(sc, d[i], acc[t][i]);
-      }
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < MT; ++t) red[wave][t][lane] = acc[t];
-  __syncthreads();
-  for (int t = wave; t < MT; t += W) {
-    floatx4 s = red[0][t][lane];
-#pragma unroll
-    for (int w = 1; w < W; ++w)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] += red[w][t][lane][i];
-    const int m = m0 + 16 * t + r;
-    if (m < p.M) store4<F32>(p, m, n0 + 4 * g, s);
-  }
+// A buffer from p on (unbounded: the kernels keep their offsets in range).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p, int bytes = -1) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);
+}
+// An offset behind the end of every buffer of less than 2 GB: loads give 0.
+constexpr uint32_t kNowhere = 0x80000000u;
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t src, uint32_t lane_offset, uint32_t offset) {
+  return __builtin_bit_cast(u32x4,
+                            __builtin_amdgcn_raw_buffer_load_b128(src, lane_offset, offset, 0));
 }
 
-// ---- tiles ---------------------------------------------------------------------------
+// Waits until at most N of this wave's loads are outstanding and its LDS
+// accesses are done, then for the block; no memory access moves across.
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | 7 << 4 | (N >> 4) << 14);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // Loads straight to LDS: lane l's 4 or 16 bytes go to dst + 4 l or + 16 l.
 // (As buffer loads: the compiler takes global ones for accesses that may
 // complete out of order with LDS reads, and waits for all of either at each
@@ -202,22 +131,165 @@ __device__ __forceinline__ void to_lds16(__amdgpu_buffer_rsrc_t src, uint32_t la
   __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)dst, 16,
                                            lane_offset, offset, 0, 0);
 }
-
-// A buffer from p on (unbounded: the kernels keep their offsets in range).
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, -1, 0x00020000);
+// The same of data that no other block reads.
+__device__ __forceinline__ void to_lds16_once(__amdgpu_buffer_rsrc_t src, uint32_t lane_offset,
+                                              uint32_t offset, void* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)dst, 16,
+                                           lane_offset, offset, 0, 2);
 }
-
-// Waits until at most N of this wave's loads are outstanding and its LDS
-// accesses are done, then for the block; no memory access moves across.
+// Waits until at most N of the wave's loads are outstanding and its LDS reads
+// are done; no memory access moves across.
 template <int N>
-__device__ __forceinline__ void wait_and_meet() {
+__device__ __forceinline__ void wait_loads() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt((N & 15) | 7 << 4 | (N >> 4) << 14);
-  __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
 
+// ---- few rows --------------------------------------------------------------------
+// One block per 16 columns and 16 MT rows; its 8 waves split the K blocks and
+// meet in LDS.  Bound by reading the weights: they stream through rings in LDS,
+// whole 128-byte lines of 8 rows a load, kAhead K blocks ahead, and with them
+// the scales; the token rows, from L2, through registers as far ahead.  (Weights by way of
+// registers, in half lines: 1 x 4096 x 7168 9.0 us, 7.0 so; 16 x 18432 x 7168 49
+// and 38.  16 waves with half the blocks each: 7.9 and 53.)
+//
+// Rows and columns past the end read the last ones, unstored.  Pieces of K past
+// the end: the tokens' lie outside the buffer and are 0, the weights' are those
+// of the block's first piece (whose NaN the sum has anyway).
+template <int MT, bool F32>
+struct Rows {
+  static constexpr int W = 8, kSets = MT == 1 ? 4 : 3, kAhead = kSets - 1;
+  // of a K block: 16 weight rows, token scales, weight scale (64 times)
+  static constexpr int kAs = 16 * kBK, kWs = kAs + 256, kEntry = kWs + 256;
+  static constexpr int kLoads = 4 + 2 * MT;
+  int K;
+  __amdgpu_buffer_rsrc_t wbuf, wsbuf, abuf, asbuf;
+  uint32_t wrow[2], arow[MT], srow;   // this lane's rows
+  int wpiece;                             // byte place of its weights in a row's block
+  i32x8 a[kSets][MT];   // a Frag's pieces
+  floatx4 acc[MT];
+
+  __device__ __forceinline__ void issue(uint8_t* __restrict__ to, int kb, int lane, int set) {
+    const int k0 = kb * kBK, g = lane / 16;
+    const uint32_t at = k0 + wpiece < K ? wpiece : 0;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) to_lds16_once(wbuf, wrow[p] + at, k0, to + 1024 * p);
+    to_lds4(asbuf, srow, 4 * kb, to + kAs);
+    to_lds4(wsbuf, 0, 4 * kb, to + kWs);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const u32x4 f0 = load16(abuf, k0 + 16 * g < K ? arow[t] : kNowhere, k0);
+      const u32x4 f1 = load16(abuf, k0 + 64 + 16 * g < K ? arow[t] + 64 : kNowhere, k0);
+      a[set][t] = __builtin_shufflevector(__builtin_bit_cast(i32x4, f0), __builtin_bit_cast(i32x4, f1),
+                                          0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  }
+
+  // The K block in set i and `cur`; LOAD: block `ahead` goes to `to`.
+  template <bool LOAD>
+  __device__ __forceinline__ void step(const uint8_t* __restrict__ cur, uint8_t* __restrict__ to,
+                                       int ahead, int lane, int i) {
+    if constexpr (LOAD) {
+      wait_loads<63>();   // the reads of the block that is loaded over
+      issue(to, ahead, lane, (i + kAhead) % kSets);
+      wait_loads<kAhead * kLoads>();
+    }
+    const int r = lane % 16, g = lane / 16;
+    const float ws = *reinterpret_cast<const float*>(cur + kWs);
+    Operand<F32> wo;
+    wo.read(cur + r * kBK, 16 * (g ^ r % 8), 16 * ((g + 4) ^ r % 8));
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      Operand<F32> ao;
+      ao.set(a[i][t]);
+      const floatx4 d = mfma_block(wo, ao);
+      const float sc = ws * reinterpret_cast<const float*>(cur + kAs)[16 * t + r];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[t][j] = fmaf(sc, d[j], acc[t][j]);
+    }
+  }
+};
+
+template <int MT, bool F32>
+__global__ __launch_bounds__(8 * kWave) __attribute__((amdgpu_waves_per_eu(4)))
+void fp8_gemm_rows_kernel(Fp8Gemm p) {
+  using RW = Rows<MT, F32>;
+  constexpr int W = RW::W;
+  __shared__ __attribute__((aligned(16))) uint8_t ring[W][RW::kSets * RW::kEntry];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const int r = lane % 16, g = lane / 16;
+  const int blocks_n = (p.N + 15) / 16;
+  const int n0 = (int)(blockIdx.x % blocks_n) * 16, m0 = (int)(blockIdx.x / blocks_n) * (16 * MT);
+  const int nb = (p.K + kBK - 1) / kBK;
+  RW rw;
+  rw.K = p.K;
+  rw.wbuf = buffer_at(p.b + (size_t)n0 * p.ldb);
+  rw.wsbuf = buffer_at(p.sb + (size_t)(n0 / kBK) * nb);
+  // (of the block's rows: pieces behind them read as 0)
+  rw.abuf = buffer_at(p.a + (size_t)m0 * p.lda, min(16 * MT, p.M - m0) * (int)p.lda);
+  rw.asbuf = buffer_at(p.sa + (size_t)m0 * p.ldsa);
+  rw.wpiece = 16 * (lane % 8 ^ lane / 8);
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    rw.wrow[q] = (uint32_t)min(8 * q + lane / 8, p.N - 1 - n0) * (uint32_t)p.ldb;
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const uint32_t m = min(16 * t + r, p.M - 1 - m0);
+    rw.arow[t] = m * (uint32_t)p.lda + 16 * g;
+    rw.acc[t] = floatx4{0.f, 0.f, 0.f, 0.f};
+  }
+  rw.srow = 4u * (uint32_t)min(lane % (16 * MT), p.M - 1 - m0) * (uint32_t)p.ldsa;
+  const int b0 = (int)((long long)nb * wave / W), n = (int)((long long)nb * (wave + 1) / W) - b0;
+  uint8_t* mine = ring[wave];
+  int j = 0;   // blocks done
+  if (n >= RW::kSets) {
+#pragma unroll
+    for (int i = 0; i < RW::kAhead; ++i) {
+      rw.issue(mine + i * RW::kEntry, b0 + i, lane, i);
+      __builtin_amdgcn_sched_barrier(0);   // block after block, as the waits count
+    }
+    // whole rounds of the sets (behind the last block that one again, unused,
+    // so that as many loads are on the way at every step), then the rest,
+    // which is all loaded
+#pragma unroll 1
+    for (; j + RW::kSets <= n; j += RW::kSets)
+#pragma unroll
+      for (int i = 0; i < RW::kSets; ++i)
+        rw.template step<true>(mine + i * RW::kEntry,
+                               mine + (i + RW::kAhead) % RW::kSets * RW::kEntry,
+                               b0 + min(j + i + RW::kAhead, n - 1), lane, i);
+    wait_loads<0>();
+#pragma unroll
+    for (int i = 0; i < RW::kAhead; ++i)
+      if (j + i < n) rw.template step<false>(mine + i * RW::kEntry, nullptr, 0, lane, i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < RW::kAhead; ++i)
+      if (i < n) rw.issue(mine + i * RW::kEntry, b0 + i, lane, i);
+    wait_loads<0>();
+#pragma unroll
+    for (int i = 0; i < RW::kAhead; ++i)
+      if (i < n) rw.template step<false>(mine + i * RW::kEntry, nullptr, 0, lane, i);
+  }
+  floatx4* red = reinterpret_cast<floatx4*>(mine);
+#pragma unroll
+  for (int t = 0; t < MT; ++t) red[t * kWave + lane] = rw.acc[t];
+  __syncthreads();
+  for (int t = wave; t < MT; t += W) {
+    floatx4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const floatx4 v = reinterpret_cast<const floatx4*>(ring[w])[t * kWave + lane];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] += v[i];
+    }
+    const int m = m0 + 16 * t + r;
+    if (m < p.M) store4<F32>(p, m, n0 + 4 * g, s);
+  }
+}
+
+// ---- tiles ---------------------------------------------------------------------------
 // acc += s d, here: left to itself the compiler moves all FMAs of a K block
 // behind its last MFMA (and the sums of all tiles into registers of their own).
 __device__ __forceinline__ void add_scaled(floatx4& acc, const floatx4& d, float s) {
@@ -535,15 +607,15 @@ hipError_t launch_tile(const Fp8Gemm& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int MT, int U>
+template <int MT>
 hipError_t launch_rows(const Fp8Gemm& p, hipStream_t s) {
   const long long blocks = ((long long)p.M + 16 * MT - 1) / (16 * MT) * (((long long)p.N + 15) / 16);
   if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks);
   if (p.out_f32)
-    hipLaunchKernelGGL((fp8_gemm_rows_kernel<MT, 8, U, true>), grid, dim3(8 * kWave), 0, s, p);
+    hipLaunchKernelGGL((fp8_gemm_rows_kernel<MT, true>), grid, dim3(8 * kWave), 0, s, p);
   else
-    hipLaunchKernelGGL((fp8_gemm_rows_kernel<MT, 8, U, false>), grid, dim3(8 * kWave), 0, s, p);
+    hipLaunchKernelGGL((fp8_gemm_rows_kernel<MT, false>), grid, dim3(8 * kWave), 0, s, p);
   return hipGetLastError();
 }
 
@@ -568,9 +640,9 @@ constexpr Shape kTiles[] = {
 
 hipError_t launch_fp8_gemm(const Fp8Gemm& p, hipStream_t s) {
   // The kernel with the least expected time.  Rows kernels: their waves split
-  // K, so a wave takes nb / 8 blocks, in 1.5 us a block with 16 rows, 1.9 with
+  // K, so a wave takes nb / 8 blocks, in 1.4 us a block with 16 rows, 1.8 with
   // 32, while at most one block a CU runs, in proportion to the blocks beyond
-  // (24 x 4096 x 7168: 32-row blocks 15.7 us, the best tile 19.3; 64 x 4096 x
+  // (24 x 4096 x 7168: 32-row blocks 12.3 us, the best tile 19.3; 64 x 4096 x
   // 7168: 24.4 against 19.9).  Tiles: rounds of the blocks that the chip
   // holds, 3 K blocks' worth of start and end.
   const int nb = (p.K + kBK - 1) / kBK;
@@ -580,9 +652,9 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& p, hipStream_t s) {
     return (float)ceil_div(nb, 8) * us * std::max(1.f, blocks / 256.f);
   };
   int best = -2;
-  float least = rows_us(16, 1.5f);
+  float least = rows_us(16, 1.4f);
   if (p.M > 16) {
-    if (const float t = rows_us(32, 1.9f); t < least) least = t, best = -1;
+    if (const float t = rows_us(32, 1.8f); t < least) least = t, best = -1;
     for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
       const Shape& k = kTiles[i];
       const long long blocks = ceil_div(p.M, k.bm) * ceil_div(p.N, k.bn);
@@ -592,8 +664,8 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& p, hipStream_t s) {
     }
   }
   switch (best) {
-    case -2: return launch_rows<1, 1>(p, s);
-    case -1: return launch_rows<2, 2>(p, s);
+    case -2: return launch_rows<1>(p, s);
+    case -1: return launch_rows<2>(p, s);
     case 0: return launch_tile<2, 1, 2, 2, 3, 2>(p, s);
     case 1: return launch_tile<2, 2, 2, 2, 4>(p, s);
     case 2: return launch_tile<2, 2, 2, 4, 4>(p, s);
