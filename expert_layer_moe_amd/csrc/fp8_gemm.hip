@@ -120,22 +120,17 @@ __device__ __forceinline__ void wait_and_meet() {
 // Loads straight to LDS: lane l's 4 or 16 bytes go to dst + 4 l or + 16 l.
 // (As buffer loads: the compiler takes global ones for accesses that may
 // complete out of order with LDS reads, and waits for all of either at each
-// use.)
+// use.)  ONCE: data that no other block reads.
 __device__ __forceinline__ void to_lds4(__amdgpu_buffer_rsrc_t src, uint32_t lane_offset,
                                           uint32_t offset, void* dst) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)dst, 4,
                                            lane_offset, offset, 0, 0);
 }
+template <bool ONCE = false>
 __device__ __forceinline__ void to_lds16(__amdgpu_buffer_rsrc_t src, uint32_t lane_offset,
-                                          uint32_t offset, void* dst) {
+                                         uint32_t offset, void* dst) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)dst, 16,
-                                           lane_offset, offset, 0, 0);
-}
-// The same of data that no other block reads.
-__device__ __forceinline__ void to_lds16_once(__amdgpu_buffer_rsrc_t src, uint32_t lane_offset,
-                                              uint32_t offset, void* dst) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)dst, 16,
-                                           lane_offset, offset, 0, 2);
+                                           lane_offset, offset, 0, ONCE ? 2 : 0);
 }
 // Waits until at most N of the wave's loads are outstanding and its LDS reads
 // are done; no memory access moves across.
@@ -157,7 +152,7 @@ __device__ __forceinline__ void wait_loads() {
 // Rows and columns past the end read the last ones, unstored.  Pieces of K past
 // the end: the tokens' lie outside the buffer and are 0, the weights' are those
 // of the block's first piece (whose NaN the sum has anyway).
-template <int MT, bool F32>
+template <int MT, bool F32, bool ONCE>
 struct Rows {
   static constexpr int W = 8, kSets = MT == 1 ? 4 : 3, kAhead = kSets - 1;
   // of a K block: 16 weight rows, token scales, weight scale (64 times)
@@ -174,7 +169,7 @@ struct Rows {
     const int k0 = kb * kBK, g = lane / 16;
     const uint32_t at = k0 + wpiece < K ? wpiece : 0;
 #pragma unroll
-    for (int p = 0; p < 2; ++p) to_lds16_once(wbuf, wrow[p] + at, k0, to + 1024 * p);
+    for (int p = 0; p < 2; ++p) to_lds16<ONCE>(wbuf, wrow[p] + at, k0, to + 1024 * p);
     to_lds4(asbuf, srow, 4 * kb, to + kAs);
     to_lds4(wsbuf, 0, 4 * kb, to + kWs);
 #pragma unroll
@@ -211,10 +206,10 @@ struct Rows {
   }
 };
 
-template <int MT, bool F32>
+template <int MT, bool F32, bool ONCE>
 __global__ __launch_bounds__(8 * kWave) __attribute__((amdgpu_waves_per_eu(4)))
 void fp8_gemm_rows_kernel(Fp8Gemm p) {
-  using RW = Rows<MT, F32>;
+  using RW = Rows<MT, F32, ONCE>;
   constexpr int W = RW::W;
   __shared__ __attribute__((aligned(16))) uint8_t ring[W][RW::kSets * RW::kEntry];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
@@ -612,10 +607,17 @@ hipError_t launch_rows(const Fp8Gemm& p, hipStream_t s) {
   const long long blocks = ((long long)p.M + 16 * MT - 1) / (16 * MT) * (((long long)p.N + 15) / 16);
   if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks);
-  if (p.out_f32)
-    hipLaunchKernelGGL((fp8_gemm_rows_kernel<MT, true>), grid, dim3(8 * kWave), 0, s, p);
-  else
-    hipLaunchKernelGGL((fp8_gemm_rows_kernel<MT, false>), grid, dim3(8 * kWave), 0, s, p);
+#define MOE_ROWS(F, O) \
+  hipLaunchKernelGGL((fp8_gemm_rows_kernel<MT, F, O>), grid, dim3(8 * kWave), 0, s, p)
+  const bool once = p.M <= 16 * MT;   // each weight is read by one block
+  if (p.out_f32) {
+    if (once) MOE_ROWS(true, true);
+    else MOE_ROWS(true, false);
+  } else {
+    if (once) MOE_ROWS(false, true);
+    else MOE_ROWS(false, false);
+  }
+#undef MOE_ROWS
   return hipGetLastError();
 }
 
