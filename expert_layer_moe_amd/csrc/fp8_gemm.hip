@@ -15,7 +15,7 @@
 // below the rounding of a bf16 result.  For fp32 results the codes become
 // bf16, exactly, and four bf16 MFMAs add up the block in fp32 (F32 below).
 //
-// Measured (bf16 results): 8192 x 4096 x 7168 219 us, 2.19 PFLOP/s, where the
+// Measured (bf16 results): 8192 x 4096 x 7168 219 to 225 us, 2.2 PFLOP/s, where the
 // card's library product of the same size, with one scale for all, takes 169:
 // the matrix cores are busy 49 % of the cycles.  Without the FMAs it would take
 // a tenth less, without the loads a fifth, with zeros for operands 200 us.
@@ -609,7 +609,9 @@ hipError_t launch_rows(const Fp8Gemm& p, hipStream_t s) {
   const dim3 grid((unsigned)blocks);
 #define MOE_ROWS(F, O) \
   hipLaunchKernelGGL((fp8_gemm_rows_kernel<MT, F, O>), grid, dim3(8 * kWave), 0, s, p)
-  const bool once = p.M <= 16 * MT;   // each weight is read by one block
+  // each weight is read by one block: past the caches (where three blocks read
+  // them, 37 x 1001 x 5136, that took 12.0 us in place of 8.0)
+  const bool once = p.M <= 16 * MT;
   if (p.out_f32) {
     if (once) MOE_ROWS(true, true);
     else MOE_ROWS(true, false);
