@@ -143,6 +143,9 @@ def _check(layer, T, padding=()):
     (9, 1152, 256, 32, 8, 1),     # most segments
     (16, 2048, 24, 128, 3, 0),
     (16, 128, 2, 32, 2, 0),
+    (3, 640, 64, 256, 8, 1),      # several units to a block's share, rows on chip
+    (1, 16256, 3, 32, 2, 0),      # the longest row that is kept on chip
+    (1, 16384, 3, 32, 2, 0),      # and the first that is not
 ])
 def test_bf16(T, H, E, I, k, ns, packed):
     _check(Layer(T * 1000 + H, H, E, I, k, ns, packed=packed), T)
@@ -156,6 +159,9 @@ def test_bf16(T, H, E, I, k, ns, packed):
     (6, 2176, 16, 128, 4, 1),
     (16, 640, 8, 256, 2, 1),
     (16, 4224, 4, 128, 1, 0),
+    (3, 640, 64, 256, 8, 1),
+    (1, 16256, 3, 128, 2, 0),
+    (4, 384, 64, 128, 8, 1),
 ])
 def test_fp8(T, H, E, I, k, ns, packed):
     _check(Layer(T * 1000 + H + 1, H, E, I, k, ns, fp8=True, packed=packed), T)

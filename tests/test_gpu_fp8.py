@@ -72,6 +72,8 @@ def _check_product(out, a, sa, b, sb):
     (17, 1, 272), (31, 65, 128), (33, 1001, 656), (64, 64, 112), (65, 257, 1152),
     (100, 384, 1040), (129, 640, 512), (257, 255, 912), (300, 2048, 256), (1000, 520, 368),
     (2049, 130, 160), (520, 4100, 144),
+    (4096, 4090, 272),            # the largest tiles
+    (16, 9000, 2064), (1, 600, 2320), (40, 1000, 1040),
 ])
 def test_product(M, N, K, dtype):
     a, sa, b, sb = _operands(M * 7 + N * 3 + K, M, N, K)
