@@ -69,7 +69,7 @@ __device__ __forceinline__ void split_h(float v, uint32_t& hi, uint32_t& lo) {
 __global__ __launch_bounds__(kThreads) void few_logits_kernel(
     const uint16_t* __restrict__ x, const uint8_t* __restrict__ valid,
     const uint16_t* __restrict__ R, float* __restrict__ part, uint32_t* __restrict__ hw,
-    int rows, int I, bool staged, int32_t* __restrict__ ticket, int T, int H, int E) {
+    int rows, int I, bool staged, int32_t* __restrict__ ticket, int first_ticket, int T, int H, int E) {
   __shared__ floatx4 red[kWaves][kWave];
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
   const int m = lane % 16, g = lane / 16;
@@ -81,7 +81,7 @@ __global__ __launch_bounds__(kThreads) void few_logits_kernel(
     const uint32_t used = (uint32_t)rows * (I / 2), half = I / 2;
     for (uint32_t i = gid; i < 2 * half; i += n) hw[used + i + (i < half ? 0 : used)] = 0u;
   }
-  if (gid == 0) *ticket = 0;
+  if (gid == 0) *ticket = first_ticket;
   const int e = blockIdx.x * 16 + m;
   const bool ev = e < E;
   const bool rv = m < T && (valid == nullptr || valid[m] != 0);
@@ -380,9 +380,11 @@ __device__ __forceinline__ void few_route(const FewArgs& a, FewTables& tb, uint8
     if (threadIdx.x == kThreads - 1)
       *reinterpret_cast<u32x4*>(xs + a.T * (2 * a.H + kPad)) = u32x4{0u, 0u, 0u, 0u};
   }
-  // the block's first ticket, behind this wave's loads (one counter serves a
-  // ticket every 10 ns, so the last of 512 blocks waits 5 us)
-  if (threadIdx.x == kThreads - 1) s_tk = take_ticket(a.ticket);
+  // The block's first ticket, behind this wave's loads.  Not STAGED, where no
+  // unit waits for another, it is the block's index and the counter starts
+  // behind those (one counter serves a ticket every 10 ns, so the last of 512
+  // blocks would wait 5 us).
+  if (threadIdx.x == kThreads - 1) s_tk = STAGED ? take_ticket(a.ticket) : blockIdx.x;
   for (int t = wave; t < a.T; t += kWaves)
     if (a.valid == nullptr || a.valid[t] != 0) few_topk(a.part, t, a.T, a.E, a.ns, a.k, tb);
   __syncthreads();
@@ -1200,20 +1202,20 @@ hipError_t launch_few(int wkind, bool packed, const void* x, const uint8_t* vali
     return hipErrorInvalidValue;
   const int rows = T * (k + n_shared);
   const bool staged = few_staged(T, H, I, k + n_shared);
-  hipLaunchKernelGGL(few_logits_kernel, dim3((E + 15) / 16, kFewLogitParts), dim3(kThreads), 0, s,
-                     static_cast<const uint16_t*>(x), valid, static_cast<const uint16_t*>(R), part,
-                     hw, rows, I, staged, ticket, T, H, E);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
-  const FewArgs a{static_cast<const uint16_t*>(x), valid, w13, w2, s13, s2, part, hw,
-                  (uint32_t)(rows + 1) * (I / 2), ticket, static_cast<FewTables*>(tables),
-                  static_cast<uint16_t*>(out), T, H, I, E, n_shared, k};
   // Blocks loop over the tickets.  STAGED: one a CU, or fewer if there are
   // fewer ranges and down units; otherwise a block for every gate/up unit, so
   // that they all run at once, from one to two a CU.
   const long long n_gu = (long long)(std::min(E, T * k) + n_shared) * (I / few_cols(wkind == W_FP8));
   const dim3 grid((unsigned)(staged ? std::min((kFewParts - 1) * n_gu + H / kDownCols, 256LL)
                                     : std::min(n_gu, 512LL)));
+  hipLaunchKernelGGL(few_logits_kernel, dim3((E + 15) / 16, kFewLogitParts), dim3(kThreads), 0, s,
+                     static_cast<const uint16_t*>(x), valid, static_cast<const uint16_t*>(R), part,
+                     hw, rows, I, staged, ticket, staged ? 0 : (int)grid.x, T, H, E);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  const FewArgs a{static_cast<const uint16_t*>(x), valid, w13, w2, s13, s2, part, hw,
+                  (uint32_t)(rows + 1) * (I / 2), ticket, static_cast<FewTables*>(tables),
+                  static_cast<uint16_t*>(out), T, H, I, E, n_shared, k};
   // The down launch: 32 columns a block, or 16 if that gives fewer rounds of
   // 256 blocks (one a CU) for its columns.
   const bool narrow = (H / 16 + 255) / 256 < (H / 32 + 255) / 256 * 2;
