@@ -12,10 +12,11 @@
 // The routing weight is applied to h', so one accumulator runs over all
 // experts and no per-expert output rows exist.
 //
-// STAGED, the rows and h' fit in a block's LDS (one or two rows of 7168): both products in one launch, the down units waiting for the sums
-// they read.  Otherwise the gate/up units alone, and few_down_kernel after
-// them: with many rows the waits cost more than a launch (16 rows of the 256-
-// expert layer: 248 us in two launches, 199 in three).
+// STAGED, the rows and h' fit in a block's LDS (one or two rows of 7168): both
+// products in one launch, the down units waiting for the sums they read.
+// Otherwise the gate/up units alone, and few_down_kernel after them: with many
+// rows the waits cost more than a launch (16 rows of the 256-expert layer: 248
+// us in two launches, 199 in three).
 //
 // Bound by HBM.  One row, bf16: 48 experts of I = 640 top-3 (83 MB) 27.8 us,
 // 256 of I = 256 top-8 and a shared one (103 MB) 30.4 us, of which the weights
@@ -63,9 +64,9 @@ __device__ __forceinline__ void split_h(float v, uint32_t& hi, uint32_t& lo) {
 // part[z][t][e] (rows few_logit_stride(E) apart): router logits over the z-th
 // part of K (the 8 waves of a block split that part again and meet in LDS), 16
 // experts per block; the second launch adds the parts up.  (8 parts, 128 blocks
-// for 256 experts: with 4, one row took 36.7 us in all in place of 34.8.)  Rows with valid == 0 are not read.  Also
-// zeroes the ticket counter and marks the sums unset (STAGED) or zeroes the
-// zero rows of h' (rows of I).
+// for 256 experts: with 4, one row took 36.7 us in all in place of 34.8.)  Rows
+// with valid == 0 are not read.  Also sets the ticket counter and marks the
+// sums unset (STAGED) or zeroes the zero rows of h' (rows of I).
 __global__ __launch_bounds__(kThreads) void few_logits_kernel(
     const uint16_t* __restrict__ x, const uint8_t* __restrict__ valid,
     const uint16_t* __restrict__ R, float* __restrict__ part, uint32_t* __restrict__ hw,
@@ -91,7 +92,7 @@ __global__ __launch_bounds__(kThreads) void few_logits_kernel(
   const uint16_t* rp = R + (size_t)(ev ? e : 0) * H + 8 * g;
   const u32x4 zero = {0u, 0u, 0u, 0u};
   floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-  constexpr int U = 8;   // steps loaded at once (a wave has 7 at H = 7168)
+  constexpr int U = 4;   // steps loaded at once (a wave has 3 or 4 at H = 7168)
   for (int s = s0; s < s1; s += U) {
     u32x4 xa[U], rb[U];
 #pragma unroll
