@@ -317,11 +317,13 @@ def _empty(shape, dtype, device, stream):
 
 
 def _row_stride(t: torch.Tensor, name: str, dtypes, rows: int, cols: int) -> int:
-    """Row stride of a rows x cols matrix with contiguous rows (0: one row,
-    whose stride says nothing)."""
+    """Row stride of a rows x cols matrix with contiguous rows (0: dense, or one
+    row, whose stride says nothing)."""
     if t.dtype not in dtypes or t.shape != (rows, cols):
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected "
                          f"{' or '.join(map(str, dtypes))} ({rows}, {cols})")
+    if t.is_contiguous():
+        return 0
     row, col = t.stride()
     if col != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
@@ -394,7 +396,7 @@ def moe_gemm_fp8(a, a_scale, b, b_scale, out=None, out_dtype=torch.bfloat16, str
     if a.dim() != 2 or b.dim() != 2:
         raise ValueError("a and b are matrices")
     M, K = a.shape
-    N = b.size(0)
+    N = b.shape[0]
     nb = (K + 127) // 128
     lda = _row_stride(a, "a", _CODES, M, K)
     ldb = _row_stride(b, "b", _CODES, N, K)
@@ -414,20 +416,25 @@ def moe_gemm_fp8(a, a_scale, b, b_scale, out=None, out_dtype=torch.bfloat16, str
 
 
 def _quant(entry, x, per_col, codes, scales, stream):
-    if x.dim() != 2 or x.size(1) % per_col != 0:
+    if x.dim() != 2:
+        raise ValueError(f"a matrix expected, not {tuple(x.shape)}")
+    M, n = x.shape
+    if n % per_col != 0:
         raise ValueError(f"a matrix of {per_col} n columns expected, not {tuple(x.shape)}")
-    M, cols = x.size(0), x.size(1) // per_col
+    cols = n // per_col
     nb = (cols + 127) // 128
-    ld_in = _row_stride(x, "input", _FLOATS, M, cols * per_col)
+    ld_in = _row_stride(x, "input", _FLOATS, M, n)
+    given = codes, scales
+    ld_codes = ld_scales = 0
     if codes is None:
-        codes, ld_codes = _empty((M, cols), torch.uint8, x.device, stream), 0
+        codes = _empty((M, cols), torch.uint8, x.device, stream)
     else:
         ld_codes = _row_stride(codes, "codes", _CODES, M, cols)
     if scales is None:
-        scales, ld_scales = _empty((M, nb), torch.float32, x.device, stream), 0
+        scales = _empty((M, nb), torch.float32, x.device, stream)
     else:
         ld_scales = _row_stride(scales, "scales", _F32, M, nb)
-    _enqueue(entry, _device_of(x, codes, scales), stream,
+    _enqueue(entry, _device_of(x, *given), stream,
              moe_quant_desc(M, cols, _DT[x.dtype], ld_in, ld_codes, ld_scales), x.data_ptr(),
              codes.data_ptr(), scales.data_ptr())
     return codes, scales
