@@ -901,10 +901,54 @@ struct DownStaged {
   }
 };
 
+// out[t][n] of a row whose sum came out as NaN, from that row's experts alone.
+// The MFMAs multiply every chosen expert's weights with all rows, by zeros for
+// the rows without it, and by h' in two parts: a weight or scale that is not
+// finite makes NaN of the rows without its expert (0 x inf) and of sums that are
+// infinite (inf x a rest of 0 or of the other sign).  Only NaN can come of
+// either, so every other sum stands.  hi(slot, c), lo(slot, c): 8 columns of h'.
+template <bool FP8, bool PW, class HI, class LO>
+__device__ __forceinline__ float row_alone(const FewArgs& a, const FewTables* __restrict__ tb, int t, int n,
+                                           HI hi, LO lo) {
+  if (a.valid != nullptr && a.valid[t] == 0) return 0.f;
+  const int kk = a.k + a.ns, H = a.H, I = a.I;
+  constexpr int kBlock = FP8 ? 128 : 32;   // columns under one scale (bf16: none)
+  float sum = 0.f;
+#pragma unroll 1
+  for (int j = 0; j < kk; ++j) {
+    const int slot = t * kk + j, e = tb->pick[slot];
+#pragma unroll 1
+    for (int c0 = 0; c0 < I; c0 += kBlock) {
+      float part = FP8 ? 0.f : sum;
+#pragma unroll 1
+      for (int c = c0; c < c0 + kBlock; c += 8) {
+        const size_t at = (size_t)e * H * I + (PW ? frag_index(n, c, I) : (size_t)n * I + c);
+        bf16x8 w;
+        if constexpr (FP8) {
+          const u32x2 v = ld8(static_cast<const uint8_t*>(a.w2) + at);
+          w = fp8x8_to_bf16x8(v[0], v[1]);
+        } else {
+          w = as_bf16x8(ld16(static_cast<const uint16_t*>(a.w2) + at));
+        }
+        const bf16x8 h = as_bf16x8(hi(slot, c)), l = as_bf16x8(lo(slot, c));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) part = fmaf((float)w[i], (float)h[i] + (float)l[i], part);
+      }
+      if constexpr (FP8)
+        sum = fmaf(a.s2[((size_t)e * (H / 128) + n / 128) * (I / 128) + c0 / 128], part, sum);
+      else sum = part;
+    }
+    if (sum != sum) break;   // it stays NaN
+  }
+  return sum;
+}
+
 // The sums of the waves (each at the start of its part of the ring) to
 // out[t][c0 .. c0 + 31].
+template <bool FP8, bool PW>
 __device__ __forceinline__ void store_out(const FewArgs& a, const FewTables* __restrict__ tb,
-                                          uint8_t* __restrict__ ring, int c0, const floatx4 (&acc)[2]) {
+                                          const uint8_t* __restrict__ hs, uint8_t* __restrict__ ring,
+                                          int c0, const floatx4 (&acc)[2]) {
   constexpr int kRing = FewShared<true>::kRing;
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
   floatx4* red = reinterpret_cast<floatx4*>(ring + wave * kRing);
@@ -917,6 +961,12 @@ __device__ __forceinline__ void store_out(const FewArgs& a, const FewTables* __r
 #pragma unroll
     for (int w = 0; w < kWaves; ++w)
       s += reinterpret_cast<const floatx4*>(ring + w * kRing)[c / 16 * kWave + (c % 16) / 4 * 16 + t][c % 4];
+    if (s != s && !tb->bad[t]) {
+      const int row_bytes = 4 * a.I + kPad;
+      const auto hi = [&](int slot, int i) { return ld16(hs + slot * row_bytes + 4 * i); };
+      const auto lo = [&](int slot, int i) { return ld16(hs + slot * row_bytes + 4 * i + 16); };
+      s = row_alone<FP8, PW>(a, tb, t, c0 + c, hi, lo);
+    }
     a.out[(size_t)t * a.H + c0 + c] = tb->bad[t] ? 0x7fc0u : f32_to_bf16_bits(s);
   }
 }
@@ -978,7 +1028,7 @@ __device__ __forceinline__ void down_unit_staged(const FewArgs& a, const FewTabl
     if (++q == d.cpe) q = 0, ++ai;
     at = at + 1 == DS::kEntries ? 0 : at + 1;
   }
-  store_out(a, tb, ring, c0, d.acc);
+  store_out<FP8, PW>(a, tb, hs, ring, c0, d.acc);
 }
 
 // Calls whose rows and h' do not fit in LDS have their down product in a
@@ -1149,6 +1199,11 @@ __global__ __launch_bounds__((Down<FP8, PW, NT, WIDE>::kWaves * kWave)) void few
 #pragma unroll
     for (int w = 0; w < kDownWaves; ++w)
       sum += reinterpret_cast<const floatx4*>(sh.ring[w])[c / 16 * kWave + (c % 16) / 4 * 16 + t][c % 4];
+    if (sum != sum && !sh.tb.bad[t]) {
+      const auto hi = [&](int slot, int i) { return ld16(d.h + (size_t)slot * I + i); };
+      const auto lo = [&](int slot, int i) { return ld16(d.h + d.plane + (size_t)slot * I + i); };
+      sum = row_alone<FP8, PW>(a, &sh.tb, t, c0 + c, hi, lo);
+    }
     a.out[(size_t)t * H + c0 + c] = sh.tb.bad[t] ? 0x7fc0u : f32_to_bf16_bits(sum);
   }
 }

@@ -271,6 +271,8 @@ size_t moe_few_workspace_size(const moe_desc* desc, int32_t topk);
  * accumulator.  The order of the sums depends on the experts that the call's
  * rows chose: a row's last bit may differ between batches; equal calls give
  * equal bits.  A row whose router logits are NaN gets a NaN output row.
+ * Weights and scales of an expert that are not finite reach the rows that
+ * chose it, and no others.
  * desc->block_m is checked and not used.  Errors as moe_forward, plus
  * MOE_ERR_UNSUPPORTED for T > MOE_FEW_MAX_ROWS, fp32 layers or H * I >= 2^30,
  * and MOE_ERR_INVALID_ARG for x, router_w, w13, w2 or a workspace that is not

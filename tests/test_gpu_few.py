@@ -352,3 +352,58 @@ def test_binding_call():
         d.forward_few(x.cpu())
     with pytest.raises(moe.MoeError):
         d.forward_few(torch.zeros(17, 256, dtype=torch.bfloat16, device="cuda"))
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("kind", ["bf16 nan", "bf16 inf", "fp8 nan", "fp8 scale inf", "fp8 scale nan"])
+@pytest.mark.parametrize("T, H, I", [
+    (2, 256, 128),       # on chip
+    (5, 4224, 128),      # a down launch of 32 columns a block
+    (16, 2048, 256),     # and one of 16
+])
+def test_weights_that_are_not_finite_stay_with_their_rows(T, H, I, kind, packed):
+    """A down weight or scale of one expert that is NaN or infinite: rows that
+    chose the expert take the formula's value in its columns, the others and
+    padding rows what they had (to the rounding of a sum in any order)."""
+    E, k, fp8 = 32, 3, kind.startswith("fp8")
+    layer = Layer(300 + T, H, E, I, k, fp8=fp8)
+    x = layer.rows(T)
+    valid = torch.ones(T, dtype=torch.uint8)
+    valid[T - 1] = 0
+    picks = [set((layer.router.double() @ r.double()).topk(k).indices.tolist()) for r in x]
+    chosen = [e for t in range(T - 1) for e in picks[t]]
+    e = min(c for c in chosen if chosen.count(c) == 1)
+    owner = next(t for t in range(T - 1) if e in picks[t])
+    ref, tol = layer.reference(x, valid)
+    xr = x[owner].double()
+    g, u = (layer.w13[e] @ xr).split(I)
+    h = g * torch.sigmoid(g) * u
+    dev, n, c = layer.dev, 77, 21
+    cols = slice(n, n + 1)
+    want = torch.tensor(float("nan"))
+    if kind == "bf16 nan":
+        dev.w2[e, n, c] = float("nan")
+    elif kind == "bf16 inf":
+        dev.w2[e, n, c] = float("inf")
+        want = torch.sign(h[c]) * float("inf")
+    elif kind == "fp8 nan":
+        dev.w2[e, n, c] = 0xFF
+    else:
+        dev.s2[e, 1, 0] = float(kind.split()[-1])
+        cols = slice(128, 256)
+    if packed:
+        dev = moe.DeviceLayer(dev.router, dev.w13, dev.w2, k, 0, dev.s13, dev.s2, packed=True)
+    x[T - 1] = float("nan")
+    got = dev.forward_few(x.cuda(), valid.cuda()).double().cpu()
+    inside = torch.zeros(T, H, dtype=torch.bool)
+    inside[owner, cols] = True
+    off = (got - ref).abs()
+    assert (off <= tol)[~inside].all()
+    assert (got[T - 1] == 0).all()
+    bad = got[inside]
+    if kind == "fp8 scale inf":
+        # a block's sum of either sign, times infinity
+        assert (~torch.isfinite(bad)).all()
+    else:
+        assert torch.equal(bad.isnan(), want.isnan().expand(bad.shape))
+        assert want.isnan() or (bad == want).all()
