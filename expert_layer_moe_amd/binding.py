@@ -355,37 +355,34 @@ def moe_forward_few(desc, x, valid_rows, router_w, w13, w2, topk, out, workspace
                     stream=None):
     """moe_forward for at most FEW_MAX_ROWS token rows, in two or three
     launches."""
-    T, H, E, I, ns = desc.T, desc.H, desc.E, desc.I, desc.n_shared
-    _dev(router_w, "router_w", _act(desc), (E, H))
-    _dev(w13, "w13", _w(desc), (E + ns, 2 * I, H))
-    _dev(w2, "w2", _w(desc), (E + ns, H, I))
-    _forward_few(ctypes.byref(desc), T, H, _act(desc), _device_of(router_w, w13, w2), x,
-                 valid_rows, router_w.data_ptr(), w13.data_ptr(), w2.data_ptr(), topk, out,
-                 workspace, stream)
+    _forward_few(desc, ctypes.byref(desc), x, valid_rows, router_w, w13, w2, topk, out, workspace,
+                 stream)
 
 
-def _forward_few(desc, T, H, act, device, x, valid_rows, router_w, w13, w2, topk, out,
-                 workspace, stream):
-    """moe_forward_few with the layer's own arrays checked before (a reference
-    to the descriptor, the GPU and the addresses of the weights)."""
-    for t, name in ((x, "x"), (out, "out")):
-        if t.dtype != act or t.dim() != 2 or t.size(0) != T or t.size(1) != H or \
-                not t.is_contiguous():
-            raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected contiguous {act} "
-                             f"({T}, {H})")
+def _dense(t, name: str, dtype, *shape):
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected contiguous {dtype} {shape}")
+
+
+def _forward_few(desc, ref, x, valid_rows, router_w, w13, w2, topk, out, workspace, stream):
+    """moe_forward_few with a reference to the descriptor at hand."""
+    T, H, E, I, ne = desc.T, desc.H, desc.E, desc.I, desc.E + desc.n_shared
+    act, w = _act(desc), _w(desc)
+    _dense(x, "x", act, T, H)
+    _dense(out, "out", act, T, H)
+    _dense(router_w, "router_w", act, E, H)
+    _dense(w13, "w13", w, ne, 2 * I, H)
+    _dense(w2, "w2", w, ne, H, I)
     valid = None
     if valid_rows is not None:
-        if valid_rows.dtype != torch.uint8 or valid_rows.dim() != 1 or \
-                valid_rows.size(0) != T or not valid_rows.is_contiguous():
-            raise ValueError(f"valid_rows: {valid_rows.dtype} {tuple(valid_rows.shape)}, "
-                             f"expected contiguous torch.uint8 ({T},)")
+        _dense(valid_rows, "valid_rows", torch.uint8, T)
         valid = valid_rows.data_ptr()
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace: contiguous torch.uint8 expected")
-    if _device_of(x, valid_rows, out, workspace) != device:
-        raise ValueError(f"tensors on {x.device}, the layer on cuda:{device}")
-    _enqueue(load_library().moe_forward_few, device, stream, desc, x.data_ptr(), valid, router_w,
-             w13, w2, topk, out.data_ptr(), workspace.data_ptr(), workspace.numel())
+    _enqueue(load_library().moe_forward_few,
+             _device_of(router_w, w13, w2, x, valid_rows, out, workspace), stream, ref,
+             x.data_ptr(), valid, router_w.data_ptr(), w13.data_ptr(), w2.data_ptr(), topk,
+             out.data_ptr(), workspace.data_ptr(), workspace.numel())
 
 
 def moe_gemm_fp8(a, a_scale, b, b_scale, out=None, out_dtype=torch.bfloat16, stream=None):

@@ -105,9 +105,7 @@ class DeviceLayer:
         # stay together
         with self._few_lock:
             ws = workspace if workspace is not None else self.few_workspace(T, stream)
-            _forward_few(few[1], T, self.H, self.router.dtype, self.router.get_device(), x, valid,
-                         self.router.data_ptr(), self.w13.data_ptr(), self.w2.data_ptr(),
-                         self.topk, out, ws, stream)
+            _forward_few(*few, x, valid, self.router, self.w13, self.w2, self.topk, out, ws, stream)
         return out
 
     def block_signals(self, T: int) -> torch.Tensor:

@@ -219,3 +219,38 @@ def test_dense_layer_refuses_shapes():
                  (w13, w2, torch.ones(2, 1), s2), (w13, w2, s13, torch.ones(1, 2))):
         with pytest.raises(ValueError):
             moe.DenseFP8(*args, device="cpu")
+
+
+def _bf16_layer(E=4, H=128, I=32, n_shared=0, experts=None):
+    n = E + n_shared if experts is None else experts
+    zeros = lambda *shape: torch.zeros(shape, dtype=torch.bfloat16)  # noqa: E731
+    return moe.DeviceLayer(zeros(E, H), zeros(n, 2 * I, H), zeros(n, H, I), 2, n_shared, device="cpu")
+
+
+def _forward_few(layer, T=2):
+    x = torch.zeros(T, layer.H, dtype=torch.bfloat16)
+    return layer.forward_few(x, out=torch.empty_like(x), workspace=_codes(1 << 20))
+
+
+@pytest.mark.parametrize("make, named", [
+    # a shared expert whose weights are not there
+    (lambda: _bf16_layer(n_shared=1, experts=4), "w13: "),
+    (lambda: _with(_bf16_layer(), w13=torch.zeros(4, 64, 256, dtype=torch.bfloat16)), "w13: "),
+    (lambda: _with(_bf16_layer(), w2=torch.zeros(4, 128, 16, dtype=torch.bfloat16)), "w2: "),
+    (lambda: _with(_bf16_layer(), w2=torch.zeros(4, 64, 32, dtype=torch.bfloat16)), "w2: "),
+    (lambda: _with(_bf16_layer(), w2=torch.zeros(4, 128, 32, dtype=torch.uint8)), "w2: "),
+    (lambda: _with(_bf16_layer(), w2=torch.zeros(4, 32, 128, dtype=torch.bfloat16).mT), "w2: "),
+    (lambda: _with(_bf16_layer(), router=torch.zeros(3, 128, dtype=torch.bfloat16)), "router_w: "),
+    (_bf16_layer, "on the GPU"),
+])
+def test_layer_of_few_rows_checks_its_weights(make, named):
+    """Weights of other shapes, types or orders than the layer's are refused on
+    every call; right ones (the last) for not being on a GPU."""
+    with pytest.raises(ValueError, match=named):
+        _forward_few(make())
+
+
+def _with(layer, **arrays):
+    for name, t in arrays.items():
+        setattr(layer, name, t)
+    return layer
