@@ -351,21 +351,15 @@ def alloc_few_workspace(desc: moe_desc, topk: int, device="cuda") -> torch.Tenso
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def moe_forward_few(desc, x, valid_rows, router_w, w13, w2, topk, out, workspace,
-                    stream=None):
-    """moe_forward for at most FEW_MAX_ROWS token rows, in two or three
-    launches."""
-    _forward_few(desc, ctypes.byref(desc), x, valid_rows, router_w, w13, w2, topk, out, workspace,
-                 stream)
-
-
 def _dense(t, name: str, dtype, *shape):
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected contiguous {dtype} {shape}")
 
 
-def _forward_few(desc, ref, x, valid_rows, router_w, w13, w2, topk, out, workspace, stream):
-    """moe_forward_few with a reference to the descriptor at hand."""
+def moe_forward_few(desc, x, valid_rows, router_w, w13, w2, topk, out, workspace,
+                    stream=None):
+    """moe_forward for at most FEW_MAX_ROWS token rows, in two or three
+    launches."""
     T, H, E, I, ne = desc.T, desc.H, desc.E, desc.I, desc.E + desc.n_shared
     act, w = _act(desc), _w(desc)
     _dense(x, "x", act, T, H)
@@ -380,9 +374,9 @@ def _forward_few(desc, ref, x, valid_rows, router_w, w13, w2, topk, out, workspa
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace: contiguous torch.uint8 expected")
     _enqueue(load_library().moe_forward_few,
-             _device_of(router_w, w13, w2, x, valid_rows, out, workspace), stream, ref,
-             x.data_ptr(), valid, router_w.data_ptr(), w13.data_ptr(), w2.data_ptr(), topk,
-             out.data_ptr(), workspace.data_ptr(), workspace.numel())
+             _device_of(router_w, w13, w2, x, valid_rows, out, workspace), stream,
+             ctypes.byref(desc), x.data_ptr(), valid, router_w.data_ptr(), w13.data_ptr(),
+             w2.data_ptr(), topk, out.data_ptr(), workspace.data_ptr(), workspace.numel())
 
 
 def moe_gemm_fp8(a, a_scale, b, b_scale, out=None, out_dtype=torch.bfloat16, stream=None):

@@ -2,15 +2,14 @@
 moe_forward calls (memory management only; the math is in the kernels)."""
 from __future__ import annotations
 
-import ctypes
 import threading
 from typing import Optional
 
 import torch
 
 from .binding import (MOE_BF16, MOE_F32, MOE_FP8_E4M3, MOE_LAYOUT_FRAG16,
-                      MOE_LAYOUT_ROW_MAJOR, _empty, _forward_few, alloc_few_workspace,
-                      alloc_workspace, make_desc, moe_forward, moe_forward_signaled,
+                      MOE_LAYOUT_ROW_MAJOR, _empty, alloc_few_workspace, alloc_workspace,
+                      make_desc, moe_forward, moe_forward_few, moe_forward_signaled,
                       moe_gemm_fp8, moe_pack_weights, moe_quant_fp8, moe_route,
                       moe_silu_mul_quant_fp8)
 
@@ -51,7 +50,7 @@ class DeviceLayer:
         self.device = device
         self.block_m = block_m
         self._ws = {}
-        self._few_ws, self._few, self._few_lock = {}, {}, threading.Lock()
+        self._few_ws, self._few_lock = {}, threading.Lock()
         self.layout = MOE_LAYOUT_ROW_MAJOR
         if packed:
             self.w13, self.w2 = moe_pack_weights(self.desc(1), self.w13, self.w2)
@@ -95,17 +94,14 @@ class DeviceLayer:
         """forward for at most FEW_MAX_ROWS token rows (one or a few sequences
         decoding), in two or three launches.  Returns out."""
         T = x.size(0)
-        few = self._few.get(T)
-        if few is None:
-            d = self.desc(T)
-            few = self._few[T] = (d, ctypes.byref(d))
         if out is None:
             out = _empty((T, self.H), x.dtype, x.device, stream)
         # threads that call on one stream share its workspace: a call's launches
         # stay together
         with self._few_lock:
             ws = workspace if workspace is not None else self.few_workspace(T, stream)
-            _forward_few(*few, x, valid, self.router, self.w13, self.w2, self.topk, out, ws, stream)
+            moe_forward_few(self.desc(T), x, valid, self.router, self.w13, self.w2, self.topk, out,
+                            ws, stream)
         return out
 
     def block_signals(self, T: int) -> torch.Tensor:

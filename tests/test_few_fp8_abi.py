@@ -254,3 +254,30 @@ def _with(layer, **arrays):
     for name, t in arrays.items():
         setattr(layer, name, t)
     return layer
+
+
+def test_layer_of_few_rows_takes_its_arrays_as_they_are(monkeypatch):
+    """Weights, scales and router put in the layer's place after a call are
+    those of the next one."""
+    from expert_layer_moe_amd import binding
+    E, H, I = 4, 128, 128
+    scales = lambda: (torch.ones(E, 2, 1), torch.ones(E, 1, 1))  # noqa: E731
+    layer = moe.DeviceLayer(torch.zeros(E, H, dtype=torch.bfloat16), _codes(E, 2 * I, H),
+                            _codes(E, H, I), 2, 0, *scales(), device="cpu")
+    calls = []
+
+    def enqueue(entry, device, stream, desc, x, valid, router, w13, w2, *rest):
+        d = desc._obj
+        calls.append((d.T, d.w13_scale, d.w2_scale, router, w13, w2))
+
+    monkeypatch.setattr(binding, "_device_of", lambda *tensors: 0)
+    monkeypatch.setattr(binding, "_enqueue", enqueue)
+    held = []
+    for _ in range(3):
+        _forward_few(layer)
+        assert calls[-1] == (2, *(t.data_ptr() for t in (layer.s13, layer.s2, layer.router,
+                                                         layer.w13, layer.w2)))
+        held.append((layer.s13, layer.s2, layer.w13, layer.w2, layer.router))
+        layer.s13, layer.s2 = scales()
+        layer.w13, layer.w2, layer.router = layer.w13.clone(), layer.w2.clone(), layer.router.clone()
+    assert len(set(calls)) == 3

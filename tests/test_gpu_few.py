@@ -407,3 +407,11 @@ def test_weights_that_are_not_finite_stay_with_their_rows(T, H, I, kind, packed)
     else:
         assert torch.equal(bad.isnan(), want.isnan().expand(bad.shape))
         assert want.isnan() or (bad == want).all()
+
+
+def test_scales_put_in_place_after_a_call():
+    layer = Layer(15, 512, 8, 128, 2, fp8=True)
+    x = layer.rows(3).cuda()
+    first = layer.dev.forward_few(x)
+    layer.dev.s13, layer.dev.s2 = layer.dev.s13.clone(), 4 * layer.dev.s2
+    assert torch.equal(layer.dev.forward_few(x), 4 * first)
