@@ -41,12 +41,7 @@ class DeviceLayer:
         self.topk = topk
         self.act = _ACT[self.router.dtype]
         self.wd = _W[self.w13.dtype]
-        if self.wd == MOE_FP8_E4M3:
-            ne, I, H = self.E + n_shared, self.I, self.H
-            if self.s13 is None or tuple(self.s13.shape) != (ne, 2 * I // 128, H // 128):
-                raise ValueError("fp8 weights need s13 [E+ns, 2I/128, H/128]")
-            if self.s2 is None or tuple(self.s2.shape) != (ne, H // 128, I // 128):
-                raise ValueError("fp8 weights need s2 [E+ns, H/128, I/128]")
+        self._check_scales()
         self.device = device
         self.block_m = block_m
         self._ws = {}
@@ -56,7 +51,20 @@ class DeviceLayer:
             self.w13, self.w2 = moe_pack_weights(self.desc(1), self.w13, self.w2)
             self.layout = MOE_LAYOUT_FRAG16
 
+    def _check_scales(self):
+        if self.wd != MOE_FP8_E4M3:
+            return
+        ne, I, H = self.E + self.n_shared, self.I, self.H
+        for s, name, shape, said in (
+                (self.s13, "s13", (ne, 2 * I // 128, H // 128), "[E+ns, 2I/128, H/128]"),
+                (self.s2, "s2", (ne, H // 128, I // 128), "[E+ns, H/128, I/128]")):
+            if s is None or s.shape != shape or s.dtype != torch.float32 or \
+                    not s.is_contiguous() or s.device != self.w13.device:
+                raise ValueError(f"fp8 weights need {name} {said}, contiguous fp32 on "
+                                 f"{self.w13.device}")
+
     def desc(self, T: int):
+        self._check_scales()
         return make_desc(T, self.H, self.E, self.I, self.n_shared, self.act, self.wd,
                          self.s13, self.s2, block_m=self.block_m, w_layout=self.layout)
 

@@ -281,3 +281,23 @@ def test_layer_of_few_rows_takes_its_arrays_as_they_are(monkeypatch):
         layer.s13, layer.s2 = scales()
         layer.w13, layer.w2, layer.router = layer.w13.clone(), layer.w2.clone(), layer.router.clone()
     assert len(set(calls)) == 3
+
+
+@pytest.mark.parametrize("arrays, named", [
+    (dict(s13=torch.ones(4, 1, 1)), "s13"), (dict(s13=None), "s13"),
+    (dict(s2=torch.ones(4, 2, 1)), "s2"), (dict(s2=torch.ones(4, 1, 1).double()), "s2"),
+    (dict(s13=torch.ones(1, 2, 1).expand(4, 2, 1)), "s13"),
+    (dict(s2=torch.ones(4, 1, 1, device="meta")), "s2"),
+])
+def test_layer_checks_scales_put_in_place_later(arrays, named):
+    """The descriptor holds addresses only, so the layer checks what is behind
+    them whenever it makes one."""
+    layer = moe.DeviceLayer(torch.zeros(4, 128, dtype=torch.bfloat16), _codes(4, 256, 128),
+                            _codes(4, 128, 128), 2, 0, torch.ones(4, 2, 1), torch.ones(4, 1, 1),
+                            device="cpu")
+    layer.desc(1)
+    _with(layer, **arrays)
+    with pytest.raises(ValueError, match=named):
+        layer.desc(1)
+    with pytest.raises(ValueError, match=named):
+        _forward_few(layer)
