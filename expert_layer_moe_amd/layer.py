@@ -51,6 +51,15 @@ class DeviceLayer:
             self.w13, self.w2 = moe_pack_weights(self.desc(1), self.w13, self.w2)
             self.layout = MOE_LAYOUT_FRAG16
 
+    # Copies and pickles: the workspaces of forward_few belong to this process's
+    # streams, and a lock is not copied.
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k not in ("_few_ws", "_few_lock")}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self._few_ws, self._few_lock = {}, threading.Lock()
+
     def _check_scales(self):
         if self.wd != MOE_FP8_E4M3:
             return

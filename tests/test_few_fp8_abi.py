@@ -301,3 +301,25 @@ def test_layer_checks_scales_put_in_place_later(arrays, named):
         layer.desc(1)
     with pytest.raises(ValueError, match=named):
         _forward_few(layer)
+
+
+def test_layers_are_copied_and_pickled():
+    import copy
+    import io
+    import pickle
+    layer = _bf16_layer()
+    layer.w2.normal_()
+    layer._few_ws[2, 0] = _codes(16)
+    file = io.BytesIO()
+    torch.save(layer, file)
+    file.seek(0)
+    for other in (copy.copy(layer), copy.deepcopy(layer), pickle.loads(pickle.dumps(layer)),
+                  torch.load(file, weights_only=False)):
+        assert torch.equal(other.w2, layer.w2) and other.topk == 2
+        # what calls share is each layer's own
+        assert other._few_ws == {} and other._few_lock is not layer._few_lock
+        with pytest.raises(ValueError, match="on the GPU"):
+            _forward_few(other)
+    dense = moe.DenseFP8(_codes(64, 128), _codes(128, 32), torch.ones(1, 1), torch.ones(1, 1),
+                         device="cpu")
+    assert torch.equal(pickle.loads(pickle.dumps(dense)).w13, copy.deepcopy(dense).w13)
