@@ -351,7 +351,8 @@ int moe_quant_fp8(const moe_quant_desc* desc, const void* x, void* codes, float*
 
 /* The same of v = SiLU(g) * u for gu [rows, 2 cols]: g the first cols values
  * of a row, u the last (the gate/up product of a dense FFN, rows of w13
- * order), v kept in fp32. */
+ * order), SiLU(g) = g / (1 + exp(-g)), every step rounded to fp32 (the
+ * exponential to a unit in the last place). */
 int moe_silu_mul_quant_fp8(const moe_quant_desc* desc, const void* gu, void* codes,
                            float* scales, moe_stream_t stream);
 

@@ -348,3 +348,19 @@ def test_calls_on_another_stream():
         q = moe.moe_quant_fp8(x, stream=s)
         s.synchronize()
         assert torch.equal(out, want) and torch.equal(q[0], wq[0]) and torch.equal(q[1], wq[1])
+
+
+@pytest.mark.parametrize("lo, hi", [(-40, -8), (-8, 0), (0, 8), (8, 40), (-1e-3, 1e-3)])
+def test_silu_in_fp32(lo, hi):
+    """A scale is its block's largest v / 448: one gate a block, an up value of
+    2^40, and SiLU shows in it.  exp to one unit in the last place (2 u), 1 + exp,
+    the quotient and the one by 448 (u each): 5 u, and products of them."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    n = 1 << 22
+    gate = lo + (hi - lo) * torch.rand(n, generator=g, device="cuda")
+    gu = torch.zeros(n, 32, device="cuda")
+    gu[:, 0], gu[:, 16] = gate, 2.0 ** 40
+    _, scales = moe.moe_silu_mul_quant_fp8(gu)
+    want = (gate.double() * torch.sigmoid(gate.double())).abs() * 2.0 ** 40 / 448
+    off = (scales[:, 0].double() - want).abs() / want.clamp(min=1e-300)
+    assert off.max().item() <= 5 * U * (1 + 10 * U)
