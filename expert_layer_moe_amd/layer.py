@@ -155,10 +155,17 @@ class DenseFP8:
 
     w13 [2I, H] (gate rows, then up rows) and w2 [H, I]: uint8 e4m3fn codes,
     with fp32 block scales s13 [ceil(2I/128), ceil(H/128)], s2 [ceil(H/128),
-    ceil(I/128)].  H and I multiples of 16.
+    ceil(I/128)].  H and I multiples of 16.  gate_up: the type of the gate/up
+    product between the kernels, torch.bfloat16 (its rounding, 2^-8, is little
+    beside that of the codes made of it, 2^-4) or torch.float32.
     """
 
-    def __init__(self, w13, w2, s13, s2, device="cuda"):
+    gate_up = torch.bfloat16   # of layers that were saved without it
+
+    def __init__(self, w13, w2, s13, s2, device="cuda", gate_up=torch.bfloat16):
+        if gate_up not in _ACT:
+            raise ValueError(f"gate_up {gate_up}: torch.float32 or torch.bfloat16 expected")
+        self.gate_up = gate_up
         self.w13 = w13.to(device).contiguous()
         self.w2 = w2.to(device).contiguous()
         self.s13 = s13.to(device, torch.float32).contiguous()
@@ -172,10 +179,8 @@ class DenseFP8:
             raise ValueError("s13 is [ceil(2I/128), ceil(H/128)], s2 [ceil(H/128), ceil(I/128)]")
 
     def forward(self, x, out=None, stream=None):
-        """x [T, H] bf16 or fp32 -> out [T, H], bf16 unless `out` is fp32.  The
-        gate/up product is bf16 between the kernels: its rounding, 2^-9, is
-        nothing beside that of the codes made of it, 2^-4."""
+        """x [T, H] bf16 or fp32 -> out [T, H], bf16 unless `out` is fp32."""
         xq, xs = moe_quant_fp8(x, stream=stream)
-        gu = moe_gemm_fp8(xq, xs, self.w13, self.s13, stream=stream)
+        gu = moe_gemm_fp8(xq, xs, self.w13, self.s13, out_dtype=self.gate_up, stream=stream)
         hq, hs = moe_silu_mul_quant_fp8(gu, stream=stream)
         return moe_gemm_fp8(hq, hs, self.w2, self.s2, out=out, stream=stream)

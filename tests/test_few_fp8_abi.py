@@ -323,3 +323,11 @@ def test_layers_are_copied_and_pickled():
     dense = moe.DenseFP8(_codes(64, 128), _codes(128, 32), torch.ones(1, 1), torch.ones(1, 1),
                          device="cpu")
     assert torch.equal(pickle.loads(pickle.dumps(dense)).w13, copy.deepcopy(dense).w13)
+
+
+def test_dense_layer_takes_the_type_of_its_gate_up_product():
+    arrays = _codes(64, 128), _codes(128, 32), torch.ones(1, 1), torch.ones(1, 1)
+    assert moe.DenseFP8(*arrays, device="cpu").gate_up == torch.bfloat16
+    assert moe.DenseFP8(*arrays, device="cpu", gate_up=torch.float32).gate_up == torch.float32
+    with pytest.raises(ValueError, match="gate_up"):
+        moe.DenseFP8(*arrays, device="cpu", gate_up=torch.float16)

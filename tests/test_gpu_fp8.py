@@ -364,3 +364,16 @@ def test_silu_in_fp32(lo, hi):
     want = (gate.double() * torch.sigmoid(gate.double())).abs() * 2.0 ** 40 / 448
     off = (scales[:, 0].double() - want).abs() / want.clamp(min=1e-300)
     assert off.max().item() <= 5 * U * (1 + 10 * U)
+
+
+@pytest.mark.parametrize("T, H, I", [(3, 400, 208), (130, 512, 656)])
+def test_dense_layer_with_its_gate_up_product_in_fp32(T, H, I):
+    weights, g = _dense(T * H, H, I)
+    dense = moe.DenseFP8(*weights, gate_up=torch.float32)
+    x = torch.randn(T, H, generator=g).cuda()
+    a, sa = moe.moe_quant_fp8(x)
+    gu = moe.moe_gemm_fp8(a, sa, dense.w13, dense.s13, out_dtype=torch.float32)
+    _check_product(gu, a.cpu(), sa.cpu(), *[w.cpu() for w in (dense.w13, dense.s13)])
+    h, sh = moe.moe_silu_mul_quant_fp8(gu)
+    want = moe.moe_gemm_fp8(h, sh, dense.w2, dense.s2, out_dtype=torch.float32)
+    assert torch.equal(dense.forward(x, out=torch.empty_like(x)), want)
