@@ -377,3 +377,28 @@ def test_dense_layer_with_its_gate_up_product_in_fp32(T, H, I):
     h, sh = moe.moe_silu_mul_quant_fp8(gu)
     want = moe.moe_gemm_fp8(h, sh, dense.w2, dense.s2, out_dtype=torch.float32)
     assert torch.equal(dense.forward(x, out=torch.empty_like(x)), want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M, N, K", [(16, 48, 384), (200, 256, 640)])
+@pytest.mark.parametrize("cancel", [False, True])
+def test_product_of_few_large_codes_among_small_ones(M, N, K, cancel, dtype):
+    """In every eight codes of K one of 256, the others' products near 2^-13 of
+    its: bf16 results lose up to 2^-13 of each eight's largest product for each of
+    the other seven (and the roundings of fp32, and half a step); fp32 results
+    nothing of that.  CANCEL: the large ones cancel."""
+    g = torch.Generator().manual_seed(M + K)
+    small = lambda rows, e: (1 + torch.randint(0, 8, (rows, K), generator=g) / 8) * 2.0 ** e  # noqa: E731
+    a, b = small(M, 1), small(N, 1)
+    a[:, ::8] = b[:, ::8] = 256
+    if cancel:
+        b[:, 8::16] = -256
+    a, b = [t.to(F8).view(torch.uint8) for t in (a, b)]
+    sa, sb = torch.ones(M, _blocks(K)), torch.ones(_blocks(N), _blocks(K))
+    out = moe.moe_gemm_fp8(a.cuda(), sa.cuda(), b.cuda(), sb.cuda(), out_dtype=dtype)
+    ref, mag = _product(a, sa, b, sb)
+    tol = (K + 2 * _blocks(K) + 8) * U * mag
+    if dtype == torch.bfloat16:
+        tol = tol + K // 8 * 7 * 2.0 ** -13 * 65536
+        tol = BF16 * (ref.abs() + tol) + tol
+    assert ((out.double().cpu() - ref).abs() <= tol).all()
