@@ -144,6 +144,16 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("" ::: "memory");
 }
 
+// The blocks of a call, at most kGridX of them along x (a multiple of the 8 XCDs;
+// a dimension holds less than 2^32 threads): block block_index(), and behind the
+// last one some without work.
+constexpr unsigned kGridX = 1u << 22;
+__device__ __forceinline__ unsigned block_index() { return blockIdx.y * gridDim.x + blockIdx.x; }
+dim3 grid_of(long long blocks) {
+  const long long y = (blocks + kGridX - 1) / kGridX;
+  return dim3((unsigned)std::min<long long>(blocks, kGridX), (unsigned)y);
+}
+
 // ---- few rows --------------------------------------------------------------------
 // One block per 16 columns and 16 MT rows; its 8 waves split the K blocks and
 // meet in LDS.  Bound by reading the weights: they stream through rings in LDS,
@@ -218,7 +228,8 @@ void fp8_gemm_rows_kernel(Fp8Gemm p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const int r = lane % 16, g = lane / 16;
   const int blocks_n = (p.N + 15) / 16;
-  const int n0 = (int)(blockIdx.x % blocks_n) * 16, m0 = (int)(blockIdx.x / blocks_n) * (16 * MT);
+  const int n0 = (int)(block_index() % blocks_n) * 16, m0 = (int)(block_index() / blocks_n) * (16 * MT);
+  if (m0 >= p.M) return;
   const int nb = (p.K + kBK - 1) / kBK;
   RW rw;
   rw.K = p.K;
@@ -487,7 +498,7 @@ void fp8_gemm_tile_kernel(Fp8Gemm p, int tiles_m, int tiles_n) {
   // of tiles, and walk them in groups of 8 rows of tiles, column by column,
   // so that its tiles share operands in its L2.
   const int total = tiles_m * tiles_n;
-  const int xcd = blockIdx.x % 8, at = blockIdx.x / 8;
+  const int xcd = block_index() % 8, at = block_index() / 8;
   const int tile = total / 8 * xcd + min(xcd, total % 8) + at;
   if (at >= total / 8 + (xcd < total % 8 ? 1 : 0)) return;
   constexpr int GM = 8;
@@ -589,8 +600,8 @@ template <int TM, int TN, int WM, int WN, int S, int KB = 1>
 hipError_t launch_tile(const Fp8Gemm& p, hipStream_t s) {
   constexpr int BM = 16 * TM * WM, BN = 16 * TN * WN;
   const long long tm = ((long long)p.M + BM - 1) / BM, tn = ((long long)p.N + BN - 1) / BN;
-  if (tm * tn > 0x7ffffff0LL) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)((tm * tn + 7) / 8 * 8));
+  if (tm * tn > kMaxGemmBlocks) return hipErrorInvalidValue;
+  const dim3 grid = grid_of((tm * tn + 7) / 8 * 8);
   if (p.out_f32) {
     // (the bf16 operands of a 256 x 256 tile do not fit the registers)
     if constexpr (TM < 8)
@@ -608,8 +619,8 @@ hipError_t launch_tile(const Fp8Gemm& p, hipStream_t s) {
 template <int MT>
 hipError_t launch_rows(const Fp8Gemm& p, hipStream_t s) {
   const long long blocks = ((long long)p.M + 16 * MT - 1) / (16 * MT) * (((long long)p.N + 15) / 16);
-  if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)blocks);
+  if (blocks > kMaxGemmBlocks) return hipErrorInvalidValue;
+  const dim3 grid = grid_of(blocks);
 #define MOE_ROWS(F, O) \
   hipLaunchKernelGGL((fp8_gemm_rows_kernel<MT, F, O>), grid, dim3(8 * kWave), 0, s, p)
   // each weight is read by one block: past the caches (where three blocks read

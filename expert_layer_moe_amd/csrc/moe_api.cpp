@@ -701,7 +701,9 @@ int moe_gemm_fp8(const moe_gemm_desc* desc, const void* a, const float* a_scale,
       (st = check_stride(desc->ldo, desc->N, 1)) != MOE_OK)
     return st;
   if (desc->K % 16 != 0) return MOE_ERR_UNSUPPORTED;
-  if (desc->M > kMaxGemmRows || desc->N > kMaxGemmRows) return MOE_ERR_UNSUPPORTED;
+  if (desc->M > kMaxGemmRows || desc->N > kMaxGemmRows ||
+      (int64_t)desc->M * desc->N > moe::kMaxGemmArea)
+    return MOE_ERR_UNSUPPORTED;
   // the tile kernels' offsets from a tile's first row have 32 bits (256 rows)
   if (std::max(or_dense(desc->lda, desc->K), or_dense(desc->ldb, desc->K)) > kMaxGemmStride ||
       or_dense(desc->ld_as, nb) > kMaxGemmStride / 4)

@@ -290,8 +290,8 @@ int moe_forward_few(const moe_desc* desc, const void* x, const uint8_t* valid_ro
  * block-scale GEMM).
  *
  * Descriptor of moe_gemm_fp8 (host struct).
- *   M, N, K    >= 1; M and N at most 2^30; K a multiple of 16 (it may end
- *              inside a 128-wide block)
+ *   M, N, K    >= 1; M and N at most 2^30, M N at most 2^38; K a multiple of
+ *              16 (it may end inside a 128-wide block)
  *   out_dtype  MOE_F32 or MOE_BF16
  *   lda, ldb   row strides of a and b in elements (bytes): 0 = K, else at
  *              least K, a multiple of 16, at most 2^23

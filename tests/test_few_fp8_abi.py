@@ -331,3 +331,8 @@ def test_dense_layer_takes_the_type_of_its_gate_up_product():
     assert moe.DenseFP8(*arrays, device="cpu", gate_up=torch.float32).gate_up == torch.float32
     with pytest.raises(ValueError, match="gate_up"):
         moe.DenseFP8(*arrays, device="cpu", gate_up=torch.float16)
+
+
+@pytest.mark.parametrize("M, N", [(1 << 20, (1 << 18) + 1), (1 << 30, 1 << 9), (1 << 9, 1 << 30)])
+def test_gemm_refuses_more_results_than_it_has_blocks_for(lib, M, N):
+    assert _gemm(lib, _g(M=M, N=N)) == UNSUPPORTED

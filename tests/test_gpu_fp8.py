@@ -402,3 +402,23 @@ def test_product_of_few_large_codes_among_small_ones(M, N, K, cancel, dtype):
         tol = tol + K // 8 * 7 * 2.0 ** -13 * 65536
         tol = BF16 * (ref.abs() + tol) + tol
     assert ((out.double().cpu() - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("M, N", [
+    (1, (1 << 27) + 3),     # blocks of 512 threads for 16 columns
+    (1 << 30, 1),           # the most rows: 2^24 tiles of 64 rows
+])
+def test_product_of_more_blocks_than_a_grid_dimension_holds(M, N):
+    """Operands that repeat every 1024 rows: so must the result."""
+    K, P = 16, 1024
+    a, sa, b, sb = _operands(6, min(M, P), min(N, P), K)
+    repeat = lambda t, n, p: t.cuda().repeat((n + p - 1) // p, 1)[:n]  # noqa: E731
+    blocks = sb[:, :1].repeat(8, 1)[:8]   # 128 columns each
+    out = moe.moe_gemm_fp8(repeat(a, M, P), repeat(sa, M, P), repeat(b, N, P),
+                           repeat(blocks, _blocks(N), 8))
+    first = out[:P, :P].clone()
+    _check_product(first, a, sa, b, blocks[:_blocks(min(N, P))])
+    flat, first = out.view(-1), first.view(-1)
+    whole = flat.numel() // P * P
+    assert torch.equal(flat[:whole].view(-1, P), first.expand(whole // P, P))
+    assert torch.equal(flat[whole:], first[:flat.numel() - whole])
