@@ -60,7 +60,7 @@ __device__ __forceinline__ void load(const void* base, size_t off, float (&v)[kP
 // 8192 x 7168 bf16: 32 us, 5.6 TB/s; with a division per value 43.
 template <bool BF16, bool SILU>
 __global__ __launch_bounds__(256) void quant_kernel(QuantRows p) {
-  const uint32_t nb = (p.cols + 127) / 128, total = (uint32_t)p.rows * nb;   // < 2^31
+  const uint32_t nb = (p.cols + 127u) / 128, total = (uint32_t)p.rows * nb;   // < 2^31
   const int part = threadIdx.x % kLanes;
   // every lane of a wave stays in the loop as long as any has a block (the
   // maximum is taken across lanes)
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantRows p) {
 }  // namespace
 
 hipError_t launch_quant(const QuantRows& p, bool silu_mul, hipStream_t s) {
-  const long long blocks = (long long)p.rows * ((p.cols + 127) / 128);
+  const long long blocks = p.rows * ((p.cols + 127LL) / 128);
   if (blocks > kMaxQuantBlocks) return hipErrorInvalidValue;
   const dim3 grid((unsigned)std::min((blocks + kGroups - 1) / kGroups, 1LL << 20));
 #define MOE_Q(B, S) hipLaunchKernelGGL((quant_kernel<B, S>), grid, dim3(256), 0, s, p)

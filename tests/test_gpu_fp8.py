@@ -422,3 +422,18 @@ def test_product_of_more_blocks_than_a_grid_dimension_holds(M, N):
     whole = flat.numel() // P * P
     assert torch.equal(flat[:whole].view(-1, P), first.expand(whole // P, P))
     assert torch.equal(flat[whole:], first[:flat.numel() - whole])
+
+
+def test_quantisation_of_the_longest_row():
+    """One row of 2^31 - 16 values, which repeat every 2048."""
+    n, P = (1 << 31) - 16, 2048
+    base = torch.randn(1, P, generator=torch.Generator().manual_seed(9)).bfloat16()
+    want, scale = _quant64(base)
+    end, end_scale = _quant64(base[:, :n % P])   # its last block has 112 values
+    codes, scales = moe.moe_quant_fp8(base.cuda().repeat(1, (n + P - 1) // P)[:, :n])
+    want, scale = want.cuda(), scale.cuda()
+    whole = n // P * P
+    assert torch.equal(codes[0, :whole].view(-1, P), want.expand(whole // P, P))
+    assert torch.equal(codes[0, whole:].cpu(), end[0])
+    assert torch.equal(scales[0, :-16].view(-1, 16), scale.expand(n // P, 16))
+    assert torch.equal(scales[0, -16:].cpu(), end_scale[0])
