@@ -334,6 +334,12 @@ def _row_stride(t: torch.Tensor, name: str, dtypes, rows: int, cols: int) -> int
     return row
 
 
+def _sizes(*sizes):
+    """The descriptors hold 32 bits, and ctypes would keep the low ones of more."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"sizes {sizes}: less than 2^31 expected")
+
+
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 _F32 = (torch.float32,)
 _FLOATS = (torch.float32, torch.bfloat16)
@@ -388,6 +394,7 @@ def moe_gemm_fp8(a, a_scale, b, b_scale, out=None, out_dtype=torch.bfloat16, str
         raise ValueError("a and b are matrices")
     M, K = a.shape
     N = b.shape[0]
+    _sizes(M, N, K)
     nb = (K + 127) // 128
     lda = _row_stride(a, "a", _CODES, M, K)
     ldb = _row_stride(b, "b", _CODES, N, K)
@@ -413,6 +420,7 @@ def _quant(entry, x, per_col, codes, scales, stream):
     if n % per_col != 0:
         raise ValueError(f"a matrix of {per_col} n columns expected, not {tuple(x.shape)}")
     cols = n // per_col
+    _sizes(M, cols)
     nb = (cols + 127) // 128
     ld_in = _row_stride(x, "input", _FLOATS, M, n)
     given = codes, scales

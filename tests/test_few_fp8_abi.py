@@ -336,3 +336,20 @@ def test_dense_layer_takes_the_type_of_its_gate_up_product():
 @pytest.mark.parametrize("M, N", [(1 << 20, (1 << 18) + 1), (1 << 30, 1 << 9), (1 << 9, 1 << 30)])
 def test_gemm_refuses_more_results_than_it_has_blocks_for(lib, M, N):
     assert _gemm(lib, _g(M=M, N=N)) == UNSUPPORTED
+
+
+def test_binding_refuses_sizes_beyond_the_descriptors():
+    """More rows or columns than 32 bits hold: their low bits are small sizes that
+    the library would take."""
+    big = (1 << 32) + 128
+    meta = lambda *shape, dtype=torch.uint8: torch.empty(shape, dtype=dtype, device="meta")  # noqa: E731
+    f32 = dict(dtype=torch.float32)
+    for M, N, K in ((big, 8, 128), (4, big, 128), (4, 8, big)):
+        nb = (K + 127) // 128
+        with pytest.raises(ValueError, match="2\\^31"):
+            moe.moe_gemm_fp8(meta(M, K), meta(M, nb, **f32), meta(N, K),
+                             meta((N + 127) // 128, nb, **f32))
+    for M, K in ((big, 128), (4, big), (1 << 31, 16)):
+        for fn, per_col in ((moe.moe_quant_fp8, 1), (moe.moe_silu_mul_quant_fp8, 2)):
+            with pytest.raises(ValueError, match="2\\^31"):
+                fn(meta(M, per_col * K, **f32))
