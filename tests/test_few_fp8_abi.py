@@ -353,3 +353,30 @@ def test_binding_refuses_sizes_beyond_the_descriptors():
         for fn, per_col in ((moe.moe_quant_fp8, 1), (moe.moe_silu_mul_quant_fp8, 2)):
             with pytest.raises(ValueError, match="2\\^31"):
                 fn(meta(M, per_col * K, **f32))
+
+
+@pytest.mark.parametrize("change, named", [
+    (dict(x=torch.zeros(3, 128, dtype=torch.bfloat16)), "x: "), (dict(x=torch.zeros(2, 128)), "x: "),
+    (dict(x=torch.zeros(2, 256, dtype=torch.bfloat16)[:, ::2]), "x: "),
+    (dict(x=torch.zeros(256, dtype=torch.bfloat16)), "x: "),
+    (dict(out=torch.zeros(2, 256, dtype=torch.bfloat16)[:, ::2]), "out: "),
+    (dict(out=torch.zeros(2, 128)), "out: "), (dict(out=torch.zeros(2, 64).bfloat16()), "out: "),
+    (dict(valid_rows=torch.ones(2)), "valid_rows: "), (dict(valid_rows=_codes(3)), "valid_rows: "),
+    (dict(valid_rows=_codes(4)[::2]), "valid_rows: "),
+    (dict(workspace=torch.zeros(1 << 16)), "workspace: "),
+    (dict(workspace=_codes(1 << 17)[::2]), "workspace: "),
+    (dict(router_w=torch.zeros(3, 128, dtype=torch.bfloat16)), "router_w: "),
+    (dict(w13=torch.zeros(4, 32, 128, dtype=torch.bfloat16)), "w13: "),
+    (dict(w2=torch.zeros(4, 128, 32)), "w2: "),
+    ({}, "on the GPU"),
+])
+def test_binding_names_what_it_refuses_of_a_layer(change, named):
+    """Each argument's own check (nothing here is on a GPU, which is all that is
+    wrong with the last)."""
+    bf = torch.bfloat16
+    good = dict(x=torch.zeros(2, 128, dtype=bf), valid_rows=None,
+                router_w=torch.zeros(4, 128, dtype=bf), w13=torch.zeros(4, 64, 128, dtype=bf),
+                w2=torch.zeros(4, 128, 32, dtype=bf), topk=2, out=torch.zeros(2, 128, dtype=bf),
+                workspace=_codes(1 << 16))
+    with pytest.raises(ValueError, match="^" + named if change else named):
+        moe.moe_forward_few(_layer(T=2, E=4, H=128, I=32), **dict(good, **change))
