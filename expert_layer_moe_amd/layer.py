@@ -98,9 +98,14 @@ class DeviceLayer:
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.few_workspace(T)
+        device = self.router.get_device()
+        if device != torch._C._cuda_getDevice():
+            # (whether a capture is on is asked of the current device's stream)
+            with torch.cuda.device(device):
+                return self.few_workspace(T)
         if torch.cuda.is_current_stream_capturing():
             return alloc_few_workspace(self.desc(T), self.topk, self.router.device)
-        key = T, torch._C._cuda_getCurrentRawStream(self.router.get_device())
+        key = T, torch._C._cuda_getCurrentRawStream(device)
         ws = self._few_ws.get(key)
         if ws is None:
             ws = self._few_ws[key] = alloc_few_workspace(self.desc(T), self.topk,

@@ -380,3 +380,32 @@ def test_binding_names_what_it_refuses_of_a_layer(change, named):
                 workspace=_codes(1 << 16))
     with pytest.raises(ValueError, match="^" + named if change else named):
         moe.moe_forward_few(_layer(T=2, E=4, H=128, I=32), **dict(good, **change))
+
+
+def test_workspace_of_a_capture_on_the_layer_s_device(monkeypatch):
+    """A layer on device 1, whose current stream is being captured, while device 0
+    is the current one: the capture gets workspaces of its own."""
+    import contextlib
+    from types import SimpleNamespace
+    current = [0]
+
+    @contextlib.contextmanager
+    def on(device):
+        current.append(device)
+        yield
+        current.pop()
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[-1])
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 100 + device)
+    monkeypatch.setattr(torch.cuda, "device", on)
+    capturing = []
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: current[-1] in capturing)
+    layer = _bf16_layer()
+    layer.router = SimpleNamespace(get_device=lambda: 1, device="cpu")
+    eager = layer.few_workspace(2)
+    assert layer.few_workspace(2) is eager
+    capturing.append(1)
+    graphs = [layer.few_workspace(2) for _ in range(2)]
+    assert len({t.data_ptr() for t in (eager, *graphs)}) == 3
+    capturing.clear()
+    assert layer.few_workspace(2) is eager and current == [0]
