@@ -9,8 +9,8 @@ from .binding import (MOE_BF16, MOE_F32, MOE_FP8_E4M3, MOE_LAYOUT_FRAG16,
                       moe_profile_enable, moe_profile_read, moe_route,
                       moe_status_str, moe_workspace_size, stage_names,
                       FEW_MAX_ROWS, alloc_few_workspace, moe_few_workspace_size,
-                      moe_forward_few, moe_gemm_desc, moe_gemm_fp8, moe_quant_desc,
-                      moe_quant_fp8, moe_silu_mul_quant_fp8)
+                      moe_forward_few, moe_gemm_desc, moe_gemm_fp8, moe_gemm_fp8_kernel,
+                      moe_quant_desc, moe_quant_fp8, moe_silu_mul_quant_fp8)
 from .layer import DeviceLayer, DenseFP8
 
 __all__ = [
@@ -21,6 +21,6 @@ __all__ = [
     "moe_profile_enable", "moe_profile_read", "moe_route", "moe_status_str",
     "moe_workspace_size", "stage_names", "DeviceLayer",
     "FEW_MAX_ROWS", "alloc_few_workspace", "moe_few_workspace_size", "moe_forward_few",
-    "moe_gemm_desc", "moe_gemm_fp8", "moe_quant_desc", "moe_quant_fp8",
+    "moe_gemm_desc", "moe_gemm_fp8", "moe_gemm_fp8_kernel", "moe_quant_desc", "moe_quant_fp8",
     "moe_silu_mul_quant_fp8", "DenseFP8",
 ]

@@ -22,8 +22,8 @@ _STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED",
            -3: "MOE_ERR_WORKSPACE", -4: "MOE_ERR_HIP"}
 
 EXPORTS = ["moe_workspace_size", "moe_route", "moe_align", "moe_forward",
-           "moe_forward_few", "moe_few_workspace_size", "moe_gemm_fp8", "moe_quant_fp8",
-           "moe_silu_mul_quant_fp8",
+           "moe_forward_few", "moe_few_workspace_size", "moe_gemm_fp8",
+           "moe_gemm_fp8_kernel", "moe_quant_fp8", "moe_silu_mul_quant_fp8",
            "moe_forward_noalloc", "moe_forward_signaled", "moe_block_signal_count", "moe_set_signal_wait_us", "moe_set_one_launch",
            "moe_pack_weights", "moe_set_path_thresholds", "moe_set_fp8_mfma", "moe_status_str", "moe_num_stages", "moe_stage_name",
            "moe_profile_enable", "moe_profile_read"]
@@ -93,6 +93,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_forward_few.restype = ctypes.c_int
     lib.moe_gemm_fp8.argtypes = [ctypes.POINTER(moe_gemm_desc), P, P, P, P, P, P]
     lib.moe_gemm_fp8.restype = ctypes.c_int
+    lib.moe_gemm_fp8_kernel.argtypes = [ctypes.POINTER(moe_gemm_desc)]
+    lib.moe_gemm_fp8_kernel.restype = ctypes.c_char_p
     for name in ("moe_quant_fp8", "moe_silu_mul_quant_fp8"):
         getattr(lib, name).argtypes = [ctypes.POINTER(moe_quant_desc), P, P, P, P]
         getattr(lib, name).restype = ctypes.c_int
@@ -411,6 +413,19 @@ def moe_gemm_fp8(a, a_scale, b, b_scale, out=None, out_dtype=torch.bfloat16, str
              moe_gemm_desc(M, N, K, _DT[out.dtype], lda, ldb, ld_as, ldo), a.data_ptr(),
              a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), out.data_ptr())
     return out
+
+
+def moe_gemm_fp8_kernel(M: int, N: int, K: int, out_dtype=torch.bfloat16) -> str:
+    """The kernel that moe_gemm_fp8 takes for these sizes ("rows 16", "tile 64 x
+    32", ...)."""
+    _sizes(M, N, K)
+    if out_dtype not in _FLOATS:
+        raise ValueError(f"out_dtype {out_dtype}: float32 or bfloat16 expected")
+    name = load_library().moe_gemm_fp8_kernel(
+        ctypes.byref(moe_gemm_desc(M, N, K, _DT[out_dtype], 0, 0, 0, 0)))
+    if name is None:
+        raise MoeError(-2, "sizes that moe_gemm_fp8 does not take")
+    return name.decode()
 
 
 def _quant(entry, x, per_col, codes, scales, stream):

@@ -655,36 +655,49 @@ constexpr Shape kTiles[] = {
     {256, 256, 1, {1.65f, 1e9f}, {1.75f, 1e9f}},
 };
 
-}  // namespace
-
-hipError_t launch_fp8_gemm(const Fp8Gemm& p, hipStream_t s) {
-  // The kernel with the least expected time.  Rows kernels: their waves split
-  // K, so a wave takes nb / 8 blocks, in 1.4 us a block with 16 rows, 1.8 with
-  // 32, while at most one block a CU runs, in proportion to the blocks beyond
-  // (24 x 4096 x 7168: 32-row blocks 12.3 us, the best tile 19.3; 64 x 4096 x
-  // 7168: 24.4 against 19.9).  Tiles: rounds of the blocks that the chip
-  // holds, 3 K blocks' worth of start and end.
-  const int nb = (p.K + kBK - 1) / kBK;
+// The kernel with the least expected time: an index of kTiles, or kRows16 or
+// kRows32.  Rows kernels: their waves split K, so a wave takes nb / 8 blocks, in
+// 1.4 us a block with 16 rows, 1.8 with 32, while at most one block a CU runs, in
+// proportion to the blocks beyond (24 x 4096 x 7168: 32-row blocks 12.3 us, the
+// best tile 19.3; 64 x 4096 x 7168: 24.4 against 19.9).  Tiles: rounds of the
+// blocks that the chip holds, 3 K blocks' worth of start and end.
+constexpr int kRows16 = -2, kRows32 = -1;
+int choose(int M, int N, int K, bool out_f32) {
+  const int nb = (K + kBK - 1) / kBK;
   const auto ceil_div = [](long long a, long long b) { return (a + b - 1) / b; };
   const auto rows_us = [&](int rows, float us) {
-    const float blocks = (float)(ceil_div(p.N, 16) * ceil_div(p.M, rows));
+    const float blocks = (float)(ceil_div(N, 16) * ceil_div(M, rows));
     return (float)ceil_div(nb, 8) * us * std::max(1.f, blocks / 256.f);
   };
-  int best = -2;
+  int best = kRows16;
   float least = rows_us(16, 1.4f);
-  if (p.M > 16) {
-    if (const float t = rows_us(32, 1.8f); t < least) least = t, best = -1;
+  if (M > 16) {
+    if (const float t = rows_us(32, 1.8f); t < least) least = t, best = kRows32;
     for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
       const Shape& k = kTiles[i];
-      const long long blocks = ceil_div(p.M, k.bm) * ceil_div(p.N, k.bn);
-      const float step = blocks <= 256 ? k.one[p.out_f32] : k.full[p.out_f32];
+      const long long blocks = ceil_div(M, k.bm) * ceil_div(N, k.bn);
+      const float step = blocks <= 256 ? k.one[out_f32] : k.full[out_f32];
       const float t = (float)(nb + 3) * step * (float)ceil_div(blocks, 256 * k.per_cu);
       if (t < least) least = t, best = i;
     }
   }
-  switch (best) {
-    case -2: return launch_rows<1>(p, s);
-    case -1: return launch_rows<2>(p, s);
+  return best;
+}
+
+}  // namespace
+
+const char* fp8_gemm_kernel_name(int M, int N, int K, bool out_f32) {
+  static const char* const kNames[] = {"rows 16",       "rows 32",        "tile 64 x 32",
+                                       "tile 64 x 64",  "tile 64 x 128",  "tile 128 x 128",
+                                       "tile 128 x 256", "tile 256 x 256"};
+  static_assert(sizeof(kNames) / sizeof(kNames[0]) == sizeof(kTiles) / sizeof(kTiles[0]) + 2, "names");
+  return kNames[choose(M, N, K, out_f32) - kRows16];
+}
+
+hipError_t launch_fp8_gemm(const Fp8Gemm& p, hipStream_t s) {
+  switch (choose(p.M, p.N, p.K, p.out_f32)) {
+    case kRows16: return launch_rows<1>(p, s);
+    case kRows32: return launch_rows<2>(p, s);
     case 0: return launch_tile<2, 1, 2, 2, 3, 2>(p, s);
     case 1: return launch_tile<2, 2, 2, 2, 4>(p, s);
     case 2: return launch_tile<2, 2, 2, 4, 4, 1, false>(p, s);

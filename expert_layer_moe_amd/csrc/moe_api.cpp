@@ -687,27 +687,44 @@ int moe_forward_few(const moe_desc* desc, const void* x, const uint8_t* valid_ro
   return MOE_OK;
 }
 
-int moe_gemm_fp8(const moe_gemm_desc* desc, const void* a, const float* a_scale, const void* b,
-                 const float* b_scale, void* out, moe_stream_t stream) {
-  if (desc == nullptr || desc->M < 1 || desc->N < 1 || desc->K < 1) return MOE_ERR_INVALID_ARG;
-  if (desc->out_dtype != MOE_F32 && desc->out_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
-  if (!a || !a_scale || !b || !b_scale || !out) return MOE_ERR_INVALID_ARG;
-  if (!aligned16(a) || !aligned16(b)) return MOE_ERR_INVALID_ARG;
-  const int64_t nb = ((int64_t)desc->K + 127) / 128;
+namespace {
+int check_gemm_sizes(const moe_gemm_desc* d) {
+  if (d == nullptr || d->M < 1 || d->N < 1 || d->K < 1) return MOE_ERR_INVALID_ARG;
+  if (d->out_dtype != MOE_F32 && d->out_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+int check_gemm_limits(const moe_gemm_desc* d) {
+  const int64_t nb = ((int64_t)d->K + 127) / 128;
   int st;
-  if ((st = check_stride(desc->lda, desc->K, 16)) != MOE_OK ||
-      (st = check_stride(desc->ldb, desc->K, 16)) != MOE_OK ||
-      (st = check_stride(desc->ld_as, nb, 1)) != MOE_OK ||
-      (st = check_stride(desc->ldo, desc->N, 1)) != MOE_OK)
+  if ((st = check_stride(d->lda, d->K, 16)) != MOE_OK ||
+      (st = check_stride(d->ldb, d->K, 16)) != MOE_OK ||
+      (st = check_stride(d->ld_as, nb, 1)) != MOE_OK ||
+      (st = check_stride(d->ldo, d->N, 1)) != MOE_OK)
     return st;
-  if (desc->K % 16 != 0) return MOE_ERR_UNSUPPORTED;
-  if (desc->M > kMaxGemmRows || desc->N > kMaxGemmRows ||
-      (int64_t)desc->M * desc->N > moe::kMaxGemmArea)
+  if (d->K % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  if (d->M > kMaxGemmRows || d->N > kMaxGemmRows || (int64_t)d->M * d->N > moe::kMaxGemmArea)
     return MOE_ERR_UNSUPPORTED;
   // the tile kernels' offsets from a tile's first row have 32 bits (256 rows)
-  if (std::max(or_dense(desc->lda, desc->K), or_dense(desc->ldb, desc->K)) > kMaxGemmStride ||
-      or_dense(desc->ld_as, nb) > kMaxGemmStride / 4)
+  if (std::max(or_dense(d->lda, d->K), or_dense(d->ldb, d->K)) > kMaxGemmStride ||
+      or_dense(d->ld_as, nb) > kMaxGemmStride / 4)
     return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+}  // namespace
+
+const char* moe_gemm_fp8_kernel(const moe_gemm_desc* desc) {
+  if (check_gemm_sizes(desc) != MOE_OK || check_gemm_limits(desc) != MOE_OK) return nullptr;
+  return moe::fp8_gemm_kernel_name(desc->M, desc->N, desc->K, desc->out_dtype == MOE_F32);
+}
+
+int moe_gemm_fp8(const moe_gemm_desc* desc, const void* a, const float* a_scale, const void* b,
+                 const float* b_scale, void* out, moe_stream_t stream) {
+  int st = check_gemm_sizes(desc);
+  if (st != MOE_OK) return st;
+  if (!a || !a_scale || !b || !b_scale || !out) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(b)) return MOE_ERR_INVALID_ARG;
+  if ((st = check_gemm_limits(desc)) != MOE_OK) return st;
+  const int64_t nb = ((int64_t)desc->K + 127) / 128;
   const moe::Fp8Gemm p{static_cast<const uint8_t*>(a), a_scale, static_cast<const uint8_t*>(b),
                        b_scale, out, desc->M, desc->N, desc->K, or_dense(desc->lda, desc->K),
                        or_dense(desc->ld_as, nb), or_dense(desc->ldb, desc->K),

@@ -249,6 +249,8 @@ struct Fp8Gemm {
 // M N at most (a block has 16 x 16 results or more), and blocks
 constexpr long long kMaxGemmArea = 1LL << 38, kMaxGemmBlocks = 0x7ffffff0LL;
 hipError_t launch_fp8_gemm(const Fp8Gemm& p, hipStream_t s);
+// The kernel it takes (host only).
+const char* fp8_gemm_kernel_name(int M, int N, int K, bool out_f32);
 // codes and scales of rows of cols values (of SiLU(gate) * up of rows of 2
 // cols values: gate, then up); strides in elements; cols and ld_codes
 // multiples of 16, rows of in 16-byte aligned.

@@ -325,6 +325,11 @@ typedef struct moe_gemm_desc {
 int moe_gemm_fp8(const moe_gemm_desc* desc, const void* a, const float* a_scale,
                  const void* b, const float* b_scale, void* out, moe_stream_t stream);
 
+/* The kernel that moe_gemm_fp8 takes for a descriptor (host, pure): "rows 16",
+ * "rows 32" (token rows of a block whose waves split K) or "tile 64 x 32" and
+ * larger (token rows x weight rows).  NULL for one that it refuses. */
+const char* moe_gemm_fp8_kernel(const moe_gemm_desc* desc);
+
 /* Descriptor of the token quantisations (host struct).
  *   rows       >= 1
  *   cols       values of an output row, >= 1, a multiple of 16

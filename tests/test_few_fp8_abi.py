@@ -409,3 +409,18 @@ def test_workspace_of_a_capture_on_the_layer_s_device(monkeypatch):
     assert len({t.data_ptr() for t in (eager, *graphs)}) == 3
     capturing.clear()
     assert layer.few_workspace(2) is eager and current == [0]
+
+
+def test_gemm_names_the_kernel_it_takes(lib):
+    assert moe.moe_gemm_fp8_kernel(1, 4096, 7168) == "rows 16"
+    assert moe.moe_gemm_fp8_kernel(8192, 4096, 7168) == "tile 256 x 256"
+    assert moe.moe_gemm_fp8_kernel(8192, 4096, 7168, torch.float32) == "tile 128 x 256"
+    for sizes in ((0, 8, 128), (4, 8, 120), (1 << 30, 1 << 9, 128)):
+        with pytest.raises(moe.MoeError):
+            moe.moe_gemm_fp8_kernel(*sizes)
+    with pytest.raises(ValueError):
+        moe.moe_gemm_fp8_kernel(4, 8, 128, torch.float16)
+    with pytest.raises(ValueError):
+        moe.moe_gemm_fp8_kernel(4, 8, 1 << 32)
+    assert lib.moe_gemm_fp8_kernel(None) is None
+    assert lib.moe_gemm_fp8_kernel(ctypes.byref(_g(lda=112))) is None

@@ -437,3 +437,63 @@ def test_quantisation_of_the_longest_row():
     assert torch.equal(codes[0, whole:].cpu(), end[0])
     assert torch.equal(scales[0, :-16].view(-1, 16), scale.expand(n // P, 16))
     assert torch.equal(scales[0, -16:].cpu(), end_scale[0])
+
+
+B, F = torch.bfloat16, torch.float32
+
+
+@pytest.mark.parametrize("kernel, M, N, K, dtypes", [
+    # waves of 5 or 6, 8, 4 or 5 K blocks; weights that one block reads, or several
+    ("rows 16", 3, 200, 5136, (B, F)), ("rows 16", 16, 4100, 8176, (B, F)),
+    ("rows 16", 20, 100, 4240, (B, F)), ("rows 16", 37, 1001, 5136, (B, F)),
+    ("rows 32", 24, 4096, 4368, (B, F)), ("rows 32", 17, 3000, 5008, (B, F)),
+    ("rows 32", 64, 2000, 5136, (B, F)), ("rows 32", 65, 2000, 5008, (F,)),
+    # 9, 16, 17 or 18 and 33 K blocks: two stages of scales and more, odd ends of
+    # two-block stages, several turns of the ring; columns and K that end inside
+    ("tile 64 x 32", 33, 3000, 1040, (B, F)), ("tile 64 x 32", 65, 3000, 1936, (B, F)),
+    ("tile 64 x 32", 33, 3000, 2064, (B, F)), ("tile 64 x 32", 33, 4090, 4112, (B, F)),
+    ("tile 64 x 64", 65, 6000, 1040, (B, F)), ("tile 64 x 64", 70, 6000, 1936, (B, F)),
+    ("tile 64 x 64", 130, 3000, 2192, (B, F)), ("tile 64 x 64", 130, 3000, 4112, (B, F)),
+    ("tile 64 x 128", 130, 6000, 1040, (B,)), ("tile 64 x 128", 130, 6000, 1936, (B,)),
+    ("tile 64 x 128", 130, 6000, 2064, (B,)), ("tile 64 x 128", 150, 5900, 4112, (B,)),
+    ("tile 128 x 128", 1000, 2050, 1040, (B, F)), ("tile 128 x 128", 1000, 2050, 1936, (B, F)),
+    ("tile 128 x 128", 1000, 2050, 2064, (B, F)), ("tile 128 x 128", 520, 3900, 4112, (B, F)),
+    ("tile 128 x 256", 2050, 2050, 1040, (B, F)), ("tile 128 x 256", 2050, 2050, 1936, (B, F)),
+    ("tile 128 x 256", 2050, 2050, 2064, (B, F)), ("tile 128 x 256", 1000, 4100, 4112, (B, F)),
+    ("tile 256 x 256", 2050, 4090, 1040, (B,)), ("tile 256 x 256", 2050, 4090, 1936, (B,)),
+    ("tile 256 x 256", 2050, 4090, 2064, (B,)), ("tile 256 x 256", 4000, 2100, 4112, (B,)),
+])
+def test_product_by_every_kernel_over_long_k(kernel, M, N, K, dtypes):
+    """Scales that differ by powers of two from block to block, and bounds of the
+    formula: fp32 as in _check_product; bf16 half a step, and of each eight
+    products seven times 2^-13 of the largest (at most the product of the largest
+    codes), beside the fp32 roundings."""
+    a, sa, b, sb = [t.cuda() for t in _operands(M + N + K, M, N, K)]
+    sa *= torch.exp2(torch.arange(_blocks(K), device="cuda") % 5 - 2.0)
+    sb *= torch.exp2(torch.arange(_blocks(K), device="cuda") % 3 - 1.0)
+    nb = _blocks(K)
+    a64 = a.view(F8).double() * sa.double().repeat_interleave(128, 1)[:, :K]
+    b64 = b.view(F8).double() * sb.double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+    ref, mag = a64 @ b64.T, a64.abs() @ b64.abs().T
+    eights = lambda t: t.abs().view(t.shape[0], K // 8, 8).amax(2)  # noqa: E731
+    for dtype in dtypes:
+        assert moe.moe_gemm_fp8_kernel(M, N, K, dtype) == kernel
+        tol = (K + 2 * nb + 8) * U * mag
+        if dtype == torch.bfloat16:
+            tol = tol + 7 * 2.0 ** -13 * (eights(a64) @ eights(b64).T)
+            tol = BF16 * (ref.abs() + tol) + tol
+        out = moe.moe_gemm_fp8(a, sa, b, sb, out_dtype=dtype)
+        off = (out.double() - ref).abs()
+        assert (off <= tol).all(), float((off / tol).max())
+        for _ in range(3):
+            assert torch.equal(out, moe.moe_gemm_fp8(a, sa, b, sb, out_dtype=dtype))
+
+
+def test_the_kernels_over_long_k_are_all_there_are():
+    """Every kernel that some sizes take is among those above."""
+    tested = {(case[0], d) for case in
+              test_product_by_every_kernel_over_long_k.pytestmark[0].args[1] for d in case[4]}
+    sizes = [int(2 ** (i / 3)) for i in range(43)]
+    taken = {(moe.moe_gemm_fp8_kernel(M, N, K, d), d) for d in (B, F) for M in sizes for N in sizes
+             for K in (16, 128, 1024, 2048, 8192, 65536)}
+    assert taken == tested
