@@ -415,3 +415,26 @@ def test_scales_put_in_place_after_a_call():
     first = layer.dev.forward_few(x)
     layer.dev.s13, layer.dev.s2 = layer.dev.s13.clone(), 4 * layer.dev.s2
     assert torch.equal(layer.dev.forward_few(x), 4 * first)
+
+
+@pytest.mark.parametrize("T, H, E, I, k, ns, fp8, packed", [
+    # 32 columns a block: rings of 4, row-major of 3, of one or two 32-wide steps
+    (16, 4224, 32, 256, 4, 0, False, True), (16, 4224, 32, 160, 4, 1, False, True),
+    (16, 4224, 32, 256, 4, 0, False, False), (16, 4224, 40, 192, 4, 1, False, False),
+    (16, 4224, 32, 160, 4, 0, False, False),
+    (16, 4224, 32, 256, 4, 1, True, True), (16, 4224, 32, 384, 4, 0, True, False),
+    # 16 columns a block: rings of 8, row-major and fp8 of 4
+    (16, 1024, 64, 256, 4, 0, False, True), (13, 1152, 64, 160, 5, 1, False, True),
+    (16, 1024, 64, 256, 4, 0, False, False), (16, 1024, 64, 224, 4, 0, False, False),
+    (16, 1024, 64, 256, 4, 1, True, True), (13, 1152, 48, 384, 5, 0, True, False),
+])
+def test_down_launch_of_many_experts(T, H, E, I, k, ns, fp8, packed):
+    """Every wave of the down launch goes round its ring and on into a part of a
+    round, over several experts, whose columns end inside a round or at its end."""
+    layer = Layer(T + H + I + k, H, E, I, k, ns, fp8=fp8, packed=packed)
+    x, _ = _check(layer, T)
+    chosen = (layer.router.double() @ x.double().T).topk(k, 0).indices.unique().numel() + ns
+    wide = not fp8 and not packed and I % 64 == 0
+    steps = chosen * I // (64 if fp8 or wide else 32)
+    ring = (3 if H > 4096 else 4) if wide else 4 if fp8 or H > 4096 else 8
+    assert steps // (12 if wide else 16) > ring
