@@ -438,3 +438,51 @@ def test_down_launch_of_many_experts(T, H, E, I, k, ns, fp8, packed):
     steps = chosen * I // (64 if fp8 or wide else 32)
     ring = (3 if H > 4096 else 4) if wide else 4 if fp8 or H > 4096 else 8
     assert steps // (12 if wide else 16) > ring
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T, H, I", [(1, 32640, 32768), (5, 32640, 32768), (3, 128, (1 << 23) - 128)])
+def test_experts_of_the_largest_size(T, H, I, fp8, packed):
+    """H I just below 2^30: offsets beyond 32 bits between experts and rows of h',
+    and up to them inside an expert.  Only 64 columns of h', from the first to the
+    last, are not zero; the reference has those (and zeros for 128 more, as for
+    fp8 each is a block of its own, with two roundings beside the sum's)."""
+    E, k = 3, 2
+    g = torch.Generator().manual_seed(T + H)
+    cols = torch.linspace(0, I - 1, 64).long()
+    ref = Layer.__new__(Layer)
+    ref.H, ref.E, ref.I, ref.k, ref.ns, ref.g = H, E, 192, k, 0, g
+    ref.router = (torch.randn(E, H, generator=g) / math.sqrt(H)).bfloat16()
+    ref.w13 = torch.zeros(E, 384, H, dtype=torch.float64)
+    ref.w2 = torch.zeros(E, H, 192, dtype=torch.float64)
+    dt = torch.uint8 if fp8 else torch.bfloat16
+    w13 = torch.zeros(E, 2 * I, H, dtype=dt, device="cuda")
+    w2 = torch.zeros(E, H, I, dtype=dt, device="cuda")
+    s13 = s2 = None
+    if fp8:
+        s13 = torch.rand(E, 2 * I // 128, H // 128, generator=g) / (100 * math.sqrt(H))
+        s2 = torch.rand(E, H // 128, I // 128, generator=g) / 800
+    for e in range(E):
+        for half, first in ((0, 0), (192, I)):
+            if fp8:
+                w = _codes(g, 64, H)
+                scale = s13[e, (first + cols) // 128].double().repeat_interleave(128, 1)
+                ref.w13[e, half:half + 64] = w.view(torch.float8_e4m3fn).double() * scale
+            else:
+                w = (torch.randn(64, H, generator=g) / math.sqrt(H)).bfloat16()
+                ref.w13[e, half:half + 64] = w.double()
+            w13[e, (first + cols).cuda()] = w.cuda()
+        if fp8:
+            w = _codes(g, H, 64)
+            scale = s2[e][:, cols // 128].double().repeat_interleave(128, 0)
+            ref.w2[e, :, :64] = w.view(torch.float8_e4m3fn).double() * scale
+        else:
+            w = (torch.randn(H, 64, generator=g) / 8).bfloat16()
+            ref.w2[e, :, :64] = w.double()
+        w2[e, :, cols.cuda()] = w.cuda()
+    ref.dev = moe.DeviceLayer(ref.router, w13, w2, k, 0, s13, s2, packed=packed)
+    del w13, w2
+    _check(ref, T)
+    ref.dev = None
+    torch.cuda.empty_cache()

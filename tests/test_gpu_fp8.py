@@ -497,3 +497,45 @@ def test_the_kernels_over_long_k_are_all_there_are():
     taken = {(moe.moe_gemm_fp8_kernel(M, N, K, d), d) for d in (B, F) for M in sizes for N in sizes
              for K in (16, 128, 1024, 2048, 8192, 65536)}
     assert taken == tested
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M, N, K", [(40, 40, 272), (300, 260, 272)])
+def test_product_of_the_widest_rows(M, N, K, dtype):
+    """Strides at their limits, 2^23 bytes and 2^21 scales, and results 2^23
+    values apart: every tile's last row lies 2 GB behind its first."""
+    a, sa, b, sb = _operands(11, M, N, K)
+    wide = lambda t, ld: torch.empty(t.shape[0], ld, dtype=t.dtype, device="cuda")[:, :t.shape[1]].copy_(t)  # noqa: E731
+    out = torch.full((M, 1 << 23), 5.0, dtype=dtype, device="cuda")
+    moe.moe_gemm_fp8(wide(a, 1 << 23), wide(sa, 1 << 21), wide(b, 1 << 23), sb.cuda(), out=out[:, 3:N + 3])
+    _check_product(out[:, 3:N + 3].clone(), a, sa, b, sb)
+    assert (out[:, :3] == 5).all() and (out[:, N + 3:] == 5).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_product_of_more_results_than_32_bits_address(dtype):
+    """Operands that repeat every 1024 rows: so must the result, both ways."""
+    M, N, K, P = 66 * 1024, 33 * 1024, 16, 1024
+    a, sa, b, sb = [t.cuda() for t in _operands(12, P, P, K)]
+    out = moe.moe_gemm_fp8(a.repeat(66, 1), sa.repeat(66, 1), b.repeat(33, 1), sb.repeat(33, 1),
+                           out_dtype=dtype)
+    first = out[:P, :P].clone()
+    _check_product(first, *[t.cpu() for t in (a, sa, b, sb)])
+    for m in range(66):
+        assert torch.equal(out[m * P:(m + 1) * P].view(P, 33, P), first[:, None].expand(P, 33, P)), m
+
+
+@pytest.mark.parametrize("silu", [False, True])
+def test_quantisation_of_rows_far_apart(silu):
+    """Rows of the input 2^29 values apart, of the codes 2^30 and of the scales
+    2^28: 4 GB between the first and the last."""
+    M, K = 5, 272
+    n = K * (2 if silu else 1)
+    fn = moe.moe_silu_mul_quant_fp8 if silu else moe.moe_quant_fp8
+    x = torch.empty(M, 1 << 29, dtype=torch.bfloat16, device="cuda")[:, :n]
+    x.copy_(torch.randn(M, n, generator=torch.Generator().manual_seed(13)))
+    want = fn(x.contiguous())
+    codes = torch.empty(M, 1 << 30, dtype=torch.uint8, device="cuda")[:, :K]
+    scales = torch.empty(M, 1 << 28, device="cuda")[:, :3]
+    fn(x, codes=codes, scales=scales)
+    assert torch.equal(codes, want[0]) and torch.equal(scales, want[1])
