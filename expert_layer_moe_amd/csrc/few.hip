@@ -18,11 +18,12 @@
 // rows the waits cost more than a launch (16 rows of the 256-expert layer: 248
 // us in two launches, 199 in three).
 //
-// Bound by HBM.  One row, bf16: 48 experts of I = 640 top-3 (83 MB) 27.8 us,
-// 256 of I = 256 top-8 and a shared one (103 MB) 30.4 us, of which the weights
+// Bound by HBM.  One row, bf16: 48 experts of I = 640 top-3 (83 MB) 28.0 us,
+// 256 of I = 256 top-8 and a shared one (103 MB) 30.6 us, of which the weights
 // take 16 and 20 at the rate of a large copy; the logits and their launch
-// take 5, the top-k in every block 4, the handover of h' 3.  16 rows, row-major
-// (1.14 GB): 207 us, 5.5 TB/s.
+// take 5, the top-k in every block 4, the handover of h' 3.  (The latter in fp8,
+// 51 MB: 28.1 us, the same steps.)  16 rows, row-major (1.14 GB): 200 to 212 us,
+// 5.4 to 5.7 TB/s.
 #include "moe_common.h"
 #include "moe_kernels.h"
 
@@ -592,8 +593,7 @@ __device__ __forceinline__ void gate_up_unit(const FewArgs& a, const FewTables* 
       uint32_t hi[2], lo[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) split_h(silu_mul(gs[i], us[i]) * wt, hi[i], lo[i]);
-      // readers wait for the words themselves to change, so nothing has to be
-      // ordered around the stores
+      // (read by the next launch)
       uint32_t* to = a.hw + ((size_t)slot * I + c0 + c) / 2;
       __hip_atomic_store(to, hi[0] | hi[1] << 16, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       __hip_atomic_store(to + a.plane, lo[0] | lo[1] << 16, __ATOMIC_RELAXED,
@@ -604,7 +604,7 @@ __device__ __forceinline__ void gate_up_unit(const FewArgs& a, const FewTables* 
 
 // A range of the gate/up units' 128-wide blocks of K, unit after unit, STAGED:
 // the calls' few units would not go evenly into the chip's CUs (288 into 256
-// for one row of the 256-expert layer: 34.8 us, with equal shares 30.4), so each
+// for one row of the 256-expert layer: 36.3 us, with equal shares 31.4), so each
 // block takes an equal share of all their blocks instead, at most kFewParts of them
 // sharing a unit.  Every wave takes its part of each unit's blocks in the range
 // (a segment) as one stream: the ring runs on from segment to segment, only the

@@ -18,12 +18,12 @@
 // need not.  For fp32 results the codes become bf16, exactly, and four bf16 MFMAs
 // add up the block in fp32 (F32 below).
 //
-// Measured (bf16 results): 8192 x 4096 x 7168 219 to 225 us, 2.2 PFLOP/s, where the
-// card's library product of the same size, with one scale for all, takes 169:
-// the matrix cores are busy 49 % of the cycles.  Without the FMAs it would take
-// a tenth less, without the loads a fifth, with zeros for operands 200 us.
-// 1000 x 7168 x 2048 20.5 us; 1 x 4096 x 7168, 29 MB, 7.0 us (4.2
-// TB/s).
+// Measured (bf16 results): 8192 x 4096 x 7168 207 to 227 us from card to card,
+// 2.1 to 2.3 PFLOP/s, where the library product of the same size, with one scale
+// for all, takes 169: the matrix cores are busy 49 % of the cycles.  Without the
+// FMAs it would take a tenth less, without the loads a fifth, with zeros for
+// operands 200 us.  (fp32 results: 430 us.)  1000 x 7168 x 2048 20.3 to 21.4 us;
+// 1 x 4096 x 7168, 29 MB, 6.4 us (4.6 TB/s).
 #include "moe_common.h"
 #include "moe_kernels.h"
 
@@ -159,8 +159,8 @@ dim3 grid_of(long long blocks) {
 // meet in LDS.  Bound by reading the weights: they stream through rings in LDS,
 // whole 128-byte lines of 8 rows a load, kAhead K blocks ahead, and with them
 // the scales; the token rows, from L2, through registers as far ahead.  (Weights by way of
-// registers, in half lines: 1 x 4096 x 7168 9.0 us, 7.0 so; 16 x 18432 x 7168 49
-// and 38.  16 waves with half the blocks each: 7.9 and 53.)
+// registers, in half lines: 1 x 4096 x 7168 9.0 us, 6.4 so; 16 x 18432 x 7168 49
+// and 34.  16 waves with half the blocks each: 7.9 and 53.)
 //
 // Rows and columns past the end read the last ones, unstored.  Pieces of K past
 // the end: the tokens' lie outside the buffer and are 0, the weights' are those

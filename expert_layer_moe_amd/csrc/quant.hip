@@ -18,7 +18,7 @@ constexpr float kTiny = 1e-12f;
 
 // As the formula has it: expf to one unit in the last place, a correctly rounded
 // division; 0 from v = -88.8 on, where exp(-v) overflows.  8192 x 2048 bf16 gates
-// and ups are bound by it: 20.4 us.  (With exp2 and reciprocal instructions and a
+// and ups are bound by it: 19.8 to 20.4 us.  (With exp2 and reciprocal instructions and a
 // correction each they take 17.2, but scales are then off by up to 5.3 units of
 // 2^-24 in place of 3.6.)
 __device__ __forceinline__ float silu(float v) { return v / (1.f + expf(-v)); }

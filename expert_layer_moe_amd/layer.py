@@ -83,6 +83,8 @@ class DeviceLayer:
         return self._ws[T]
 
     def forward(self, x, valid=None, out=None, workspace=None, stream=None):
+        """The layer for x [T, H] (forward_few is faster for a few rows).
+        Returns out."""
         T = x.shape[0]
         if out is None:
             out = torch.empty_like(x)
@@ -114,7 +116,8 @@ class DeviceLayer:
 
     def forward_few(self, x, valid=None, out=None, workspace=None, stream=None):
         """forward for at most FEW_MAX_ROWS token rows (one or a few sequences
-        decoding), in two or three launches.  Returns out."""
+        decoding) of a layer with bf16 activations, in two or three launches; other
+        roundings than forward's, so not its bits.  Returns out."""
         T = x.size(0)
         if out is None:
             out = _empty((T, self.H), x.dtype, x.device, stream)

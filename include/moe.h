@@ -159,7 +159,9 @@ int moe_align(const moe_desc* desc, const int32_t* topk_ids, int32_t topk,
  *   w13  [E+n_shared, 2I, H]: gate rows 0..I-1, then up rows I..2I-1
  *   w2   [E+n_shared, H, I]
  *   (fp8: uint8 e4m3fn codes; W = code value * block scale)
- *   out  [T, H] act_dtype (must not alias any input) */
+ *   out  [T, H] act_dtype (must not alias any input)
+ * For T <= MOE_FEW_MAX_ROWS rows with bf16 activations moe_forward_few is faster
+ * (a third to nine tenths of the time). */
 int moe_forward(const moe_desc* desc, const void* x, const uint8_t* valid_rows,
                 const void* router_w, const void* w13, const void* w2,
                 int32_t topk, void* out, void* workspace,
@@ -352,7 +354,8 @@ typedef struct moe_quant_desc {
  * both divisions correctly rounded in fp32, the code rounded to nearest even.
  * A NaN value gives a NaN code and leaves the rest of its block as if it were
  * 0; a block that holds an infinity gets an infinite scale, so that all of it
- * stands for NaN.  Gaps between rows are not written.  Errors as moe_gemm_fp8
+ * stands for NaN.  Gaps between rows are not written; codes and scales must not
+ * overlap x (rows are read after others' codes have been written).  Errors as moe_gemm_fp8
  * (MOE_ERR_UNSUPPORTED for cols or strides off their multiples, or 2^31 blocks
  * of 128 or more). */
 int moe_quant_fp8(const moe_quant_desc* desc, const void* x, void* codes, float* scales,
