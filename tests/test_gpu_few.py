@@ -486,3 +486,37 @@ def test_experts_of_the_largest_size(T, H, I, fp8, packed):
     _check(ref, T)
     ref.dev = None
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("kind", ["bf16 nan", "bf16 inf", "fp8 nan", "fp8 scale inf"])
+@pytest.mark.parametrize("T, H, I", [(2, 256, 128), (5, 4224, 128), (16, 2048, 256)])
+def test_gate_and_up_weights_that_are_not_finite_stay_with_their_rows(T, H, I, kind, packed):
+    """The same of the first product: a row that chose the expert has an h' that is
+    not a number, and with it no output that is finite; the others keep theirs."""
+    E, k, fp8 = 32, 3, kind.startswith("fp8")
+    layer = Layer(400 + T, H, E, I, k, fp8=fp8)
+    x = layer.rows(T)
+    valid = torch.ones(T, dtype=torch.uint8)
+    valid[T - 1] = 0
+    picks = [(layer.router.double() @ r.double()).topk(k).indices.tolist() for r in x]
+    chosen = [e for t in range(T - 1) for e in picks[t]]
+    e = min(c for c in chosen if chosen.count(c) == 1)
+    owner = next(t for t in range(T - 1) if e in picks[t])
+    ref, tol = layer.reference(x, valid)
+    dev = layer.dev
+    if kind == "fp8 scale inf":
+        dev.s13[e, 0, 0] = float("inf")
+    else:
+        dev.w13[e, 5, 9] = {"bf16 nan": float("nan"), "bf16 inf": float("inf"), "fp8 nan": 0x7F}[kind]
+    if packed:
+        dev = moe.DeviceLayer(dev.router, dev.w13, dev.w2, k, 0, dev.s13, dev.s2, packed=True)
+    x[T - 1] = float("nan")
+    got = dev.forward_few(x.cuda(), valid.cuda()).double().cpu()
+    others = torch.arange(T) != owner
+    assert ((got - ref).abs() <= tol)[others].all() and (got[T - 1] == 0).all()
+    if kind.endswith("nan"):
+        assert got[owner].isnan().all()
+    # SiLU(-inf) is NaN, SiLU(inf) infinite: times a weight, and 0 in fp8, never finite
+    if kind == "fp8 scale inf" or (kind == "bf16 inf"):
+        assert not torch.isfinite(got[owner]).any()
