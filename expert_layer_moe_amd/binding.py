@@ -24,6 +24,8 @@ _STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED",
 EXPORTS = ["moe_workspace_size", "moe_route", "moe_align", "moe_forward",
            "moe_forward_few", "moe_few_workspace_size", "moe_gemm_fp8",
            "moe_gemm_fp8_kernel", "moe_quant_fp8", "moe_silu_mul_quant_fp8",
+           "moe_quant_mxfp4", "moe_silu_mul_quant_mxfp4", "moe_dequant_mxfp4", "moe_gemm_mxfp4",
+           "moe_add_rms_norm", "moe_add_rms_norm_quant_fp8",
            "moe_forward_noalloc", "moe_forward_signaled", "moe_block_signal_count", "moe_set_signal_wait_us", "moe_set_one_launch",
            "moe_pack_weights", "moe_set_path_thresholds", "moe_set_fp8_mfma", "moe_status_str", "moe_num_stages", "moe_stage_name",
            "moe_profile_enable", "moe_profile_read"]
@@ -53,6 +55,21 @@ class moe_quant_desc(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
                 ("in_dtype", ctypes.c_int32), ("ld_in", ctypes.c_int64),
                 ("ld_codes", ctypes.c_int64), ("ld_scales", ctypes.c_int64)]
+
+
+class moe_mx_gemm_desc(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("lda", ctypes.c_int64), ("ldb", ctypes.c_int64),
+                ("ld_as", ctypes.c_int64), ("ld_bs", ctypes.c_int64), ("ldo", ctypes.c_int64)]
+
+
+class moe_norm_desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
+                ("res_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("ld_x", ctypes.c_int64),
+                ("ld_res", ctypes.c_int64), ("ld_res_out", ctypes.c_int64),
+                ("ld_out", ctypes.c_int64), ("ld_codes", ctypes.c_int64),
+                ("ld_scales", ctypes.c_int64)]
 
 
 _lib = None
@@ -95,9 +112,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_gemm_fp8.restype = ctypes.c_int
     lib.moe_gemm_fp8_kernel.argtypes = [ctypes.POINTER(moe_gemm_desc)]
     lib.moe_gemm_fp8_kernel.restype = ctypes.c_char_p
-    for name in ("moe_quant_fp8", "moe_silu_mul_quant_fp8"):
+    for name in ("moe_quant_fp8", "moe_silu_mul_quant_fp8", "moe_quant_mxfp4",
+                 "moe_silu_mul_quant_mxfp4", "moe_dequant_mxfp4"):
         getattr(lib, name).argtypes = [ctypes.POINTER(moe_quant_desc), P, P, P, P]
         getattr(lib, name).restype = ctypes.c_int
+    lib.moe_gemm_mxfp4.argtypes = [ctypes.POINTER(moe_mx_gemm_desc), P, P, P, P, P, P]
+    lib.moe_gemm_mxfp4.restype = ctypes.c_int
+    lib.moe_add_rms_norm.argtypes = [ctypes.POINTER(moe_norm_desc), P, P, P, P, P, P]
+    lib.moe_add_rms_norm.restype = ctypes.c_int
+    lib.moe_add_rms_norm_quant_fp8.argtypes = [ctypes.POINTER(moe_norm_desc)] + [P] * 8
+    lib.moe_add_rms_norm_quant_fp8.restype = ctypes.c_int
     lib.moe_pack_weights.argtypes = [D, P, P, P, P, P]
     lib.moe_pack_weights.restype = ctypes.c_int
     lib.moe_set_fp8_mfma.argtypes = [I32]
@@ -464,6 +488,181 @@ def moe_quant_fp8(x, codes=None, scales=None, stream=None):
 def moe_silu_mul_quant_fp8(gu, codes=None, scales=None, stream=None):
     """moe_quant_fp8 of SiLU(g) * u for gu [M, 2 I] (gate columns, then up)."""
     return _quant(load_library().moe_silu_mul_quant_fp8, gu, 2, codes, scales, stream)
+
+
+# ---- 4-bit microscaled floats ---------------------------------------------------
+_BYTES = (torch.uint8,)
+_MX_SCALES = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _mx_quant(entry, x, per_col, codes, scales, stream):
+    if x.dim() != 2:
+        raise ValueError(f"a matrix expected, not {tuple(x.shape)}")
+    M, n = x.shape
+    if n % (32 * per_col) != 0:
+        raise ValueError(f"a matrix of {32 * per_col} n columns expected, not {tuple(x.shape)}")
+    cols = n // per_col
+    _sizes(M, cols)
+    ld_in = _row_stride(x, "input", _FLOATS, M, n)
+    given = codes, scales
+    ld_codes = ld_scales = 0
+    if codes is None:
+        codes = _empty((M, cols // 2), torch.uint8, x.device, stream)
+    else:
+        ld_codes = _row_stride(codes, "codes", _BYTES, M, cols // 2)
+    if scales is None:
+        scales = _empty((M, cols // 32), torch.uint8, x.device, stream)
+    else:
+        ld_scales = _row_stride(scales, "scales", _MX_SCALES, M, cols // 32)
+    _enqueue(entry, _device_of(x, *given), stream,
+             moe_quant_desc(M, cols, _DT[x.dtype], ld_in, ld_codes, ld_scales), x.data_ptr(),
+             codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def moe_quant_mxfp4(x, codes=None, scales=None, stream=None):
+    """Token or weight rows x [M, K] (bf16 or fp32; rows may be strided; K a
+    multiple of 32) -> e2m1 codes [M, K/2] (uint8, two to a byte, the first in
+    the low half) and e8m0 scale codes [M, K/32] (uint8 or, if given,
+    float8_e8m0fnu), allocated here when not given.  Returns (codes, scales)."""
+    return _mx_quant(load_library().moe_quant_mxfp4, x, 1, codes, scales, stream)
+
+
+def moe_silu_mul_quant_mxfp4(gu, codes=None, scales=None, stream=None):
+    """moe_quant_mxfp4 of SiLU(g) * u for gu [M, 2 I] (gate columns, then up)."""
+    return _mx_quant(load_library().moe_silu_mul_quant_mxfp4, gu, 2, codes, scales, stream)
+
+
+def moe_dequant_mxfp4(codes, scales, out=None, out_dtype=torch.bfloat16, stream=None):
+    """The values [M, K] (bf16 or fp32, exact) of e2m1 codes [M, K/2] under e8m0
+    scale codes [M, K/32]; out is allocated here when not given."""
+    if codes.dim() != 2 or codes.shape[1] % 16 != 0:
+        raise ValueError(f"codes [M, 16 n] expected, not {tuple(codes.shape)}")
+    M, K = codes.shape[0], 2 * codes.shape[1]
+    _sizes(M, K)
+    ld_codes = _row_stride(codes, "codes", _BYTES, M, K // 2)
+    ld_scales = _row_stride(scales, "scales", _MX_SCALES, M, K // 32)
+    given, ld_out = out, 0
+    if out is None:
+        if out_dtype not in _FLOATS:
+            raise ValueError(f"out_dtype {out_dtype}: float32 or bfloat16 expected")
+        out = _empty((M, K), out_dtype, codes.device, stream)
+    else:
+        ld_out = _row_stride(out, "out", _FLOATS, M, K)
+    _enqueue(load_library().moe_dequant_mxfp4, _device_of(codes, scales, given), stream,
+             moe_quant_desc(M, K, _DT[out.dtype], ld_out, ld_codes, ld_scales), codes.data_ptr(),
+             scales.data_ptr(), out.data_ptr())
+    return out
+
+
+def moe_gemm_mxfp4(a, a_scale, b, b_scale, out=None, out_dtype=torch.bfloat16, stream=None):
+    """out [M, N] = a b^T of e2m1 codes a [M, K/2], b [N, K/2] (uint8, two to a
+    byte) under e8m0 scale codes a_scale [M, K/32], b_scale [N, K/32] (uint8 or
+    float8_e8m0fnu).  All may have wider rows (row strides); out is allocated
+    here when not given."""
+    if a.dim() != 2 or b.dim() != 2:
+        raise ValueError("a and b are matrices")
+    M, half = a.shape
+    N = b.shape[0]
+    K = 2 * half
+    _sizes(M, N, K)
+    nb = K // 32
+    lda = _row_stride(a, "a", _BYTES, M, half)
+    ldb = _row_stride(b, "b", _BYTES, N, half)
+    ld_as = _row_stride(a_scale, "a_scale", _MX_SCALES, M, nb)
+    ld_bs = _row_stride(b_scale, "b_scale", _MX_SCALES, N, nb)
+    given, ldo = out, 0
+    if out is None:
+        if out_dtype not in _FLOATS:
+            raise ValueError(f"out_dtype {out_dtype}: float32 or bfloat16 expected")
+        out = _empty((M, N), out_dtype, a.device, stream)
+    else:
+        ldo = _row_stride(out, "out", _FLOATS, M, N)
+    _enqueue(load_library().moe_gemm_mxfp4, _device_of(a, a_scale, b, b_scale, given), stream,
+             moe_mx_gemm_desc(M, N, K, _DT[out.dtype], lda, ldb, ld_as, ld_bs, ldo), a.data_ptr(),
+             a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), out.data_ptr())
+    return out
+
+
+# ---- root-mean-square norm with the residual's addition ---------------------------
+def _norm_args(x, residual, weight, residual_out, stream):
+    """(rows, columns, strides of x, residual and residual_out, residual_out)"""
+    if x.dim() != 2:
+        raise ValueError(f"a matrix expected, not {tuple(x.shape)}")
+    M, H = x.shape
+    _sizes(M, H)
+    if weight.dtype not in _FLOATS or weight.shape != (H,) or not weight.is_contiguous():
+        raise ValueError(f"weight: {weight.dtype} {tuple(weight.shape)}, expected contiguous "
+                         f"torch.float32 or torch.bfloat16 ({H},)")
+    ld_x = _row_stride(x, "x", _FLOATS, M, H)
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out without a residual")
+        return M, H, ld_x, 0, 0, None
+    ld_res, ld_res_out = _row_stride(residual, "residual", _FLOATS, M, H), 0
+    if residual_out is None:
+        residual_out = _empty((M, H), residual.dtype, x.device, stream)
+    else:
+        ld_res_out = _row_stride(residual_out, "residual_out", (residual.dtype,), M, H)
+    return M, H, ld_x, ld_res, ld_res_out, residual_out
+
+
+def _ptr_or_none(t):
+    return None if t is None else t.data_ptr()
+
+
+def moe_add_rms_norm(x, residual, weight, eps=1e-6, out=None, residual_out=None,
+                     out_dtype=torch.bfloat16, stream=None):
+    """r = x + residual (as stored in residual_out, of residual's type), out =
+    r / sqrt(mean(r^2) + eps) * weight, for rows x, residual [M, H] (bf16 or
+    fp32, H a multiple of 16) and weight [H].  residual None: r = x.
+    residual_out may be residual, out may be x; both are allocated here when not
+    given.  Returns (out, residual_out), the latter None without a residual."""
+    M, H, ld_x, ld_res, ld_res_out, residual_out = _norm_args(x, residual, weight, residual_out,
+                                                              stream)
+    ld_out = 0
+    if out is None:
+        if out_dtype not in _FLOATS:
+            raise ValueError(f"out_dtype {out_dtype}: float32 or bfloat16 expected")
+        out = _empty((M, H), out_dtype, x.device, stream)
+    else:
+        ld_out = _row_stride(out, "out", _FLOATS, M, H)
+    _enqueue(load_library().moe_add_rms_norm,
+             _device_of(x, residual, weight, residual_out, out), stream,
+             moe_norm_desc(M, H, _DT[x.dtype], 0 if residual is None else _DT[residual.dtype],
+                           _DT[weight.dtype], _DT[out.dtype], eps, ld_x, ld_res, ld_res_out,
+                           ld_out, 0, 0),
+             x.data_ptr(), _ptr_or_none(residual), weight.data_ptr(), _ptr_or_none(residual_out),
+             out.data_ptr())
+    return out, residual_out
+
+
+def moe_add_rms_norm_quant_fp8(x, residual, weight, eps=1e-6, codes=None, scales=None,
+                               residual_out=None, out=None, stream=None):
+    """moe_add_rms_norm's result in moe_quant_fp8's codes [M, H] (uint8) and
+    scales [M, ceil(H/128)], of its fp32 values; these themselves go to `out`
+    (bf16 or fp32) only if it is given.  Returns (codes, scales, residual_out)."""
+    M, H, ld_x, ld_res, ld_res_out, residual_out = _norm_args(x, residual, weight, residual_out,
+                                                              stream)
+    ld_codes = ld_scales = ld_out = 0
+    if codes is None:
+        codes = _empty((M, H), torch.uint8, x.device, stream)
+    else:
+        ld_codes = _row_stride(codes, "codes", _CODES, M, H)
+    if scales is None:
+        scales = _empty((M, (H + 127) // 128), torch.float32, x.device, stream)
+    else:
+        ld_scales = _row_stride(scales, "scales", _F32, M, (H + 127) // 128)
+    if out is not None:
+        ld_out = _row_stride(out, "out", _FLOATS, M, H)
+    _enqueue(load_library().moe_add_rms_norm_quant_fp8,
+             _device_of(x, residual, weight, residual_out, out, codes, scales), stream,
+             moe_norm_desc(M, H, _DT[x.dtype], 0 if residual is None else _DT[residual.dtype],
+                           _DT[weight.dtype], 0 if out is None else _DT[out.dtype], eps, ld_x,
+                           ld_res, ld_res_out, ld_out, ld_codes, ld_scales),
+             x.data_ptr(), _ptr_or_none(residual), weight.data_ptr(), _ptr_or_none(residual_out),
+             _ptr_or_none(out), codes.data_ptr(), scales.data_ptr())
+    return codes, scales, residual_out
 
 
 SCRATCH_BYTES = 64 << 20   # MOE_SCRATCH_BYTES

@@ -13,8 +13,9 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libmoe_amd.so")
 
 SOURCES = ["route.hip", "align.hip", "layout.hip", "experts.hip", "gemm.hip",
-           "few.hip", "fp8_gemm.hip", "quant.hip", "moe_api.cpp"]
-HEADERS = ["moe_common.h", "moe_kernels.h"]
+           "few.hip", "fp8_gemm.hip", "quant.hip", "mxfp4.hip", "mxfp4_gemm.hip", "norm.hip",
+           "moe_api.cpp"]
+HEADERS = ["moe_common.h", "moe_gemm_tile.h", "moe_kernels.h"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",

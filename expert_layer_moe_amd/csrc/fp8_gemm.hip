@@ -25,15 +25,13 @@
 // operands 200 us.  (fp32 results: 430 us.)  1000 x 7168 x 2048 20.3 to 21.4 us;
 // 1 x 4096 x 7168, 29 MB, 6.4 us (4.6 TB/s).
 #include "moe_common.h"
+#include "moe_gemm_tile.h"
 #include "moe_kernels.h"
 
 #include <algorithm>
 
 namespace moe {
 namespace {
-
-typedef __attribute__((__vector_size__(8 * sizeof(int)))) int i32x8;
-typedef __attribute__((__vector_size__(4 * sizeof(int)))) int i32x4;
 
 constexpr int kBK = 128;   // K block
 
@@ -85,73 +83,6 @@ __device__ __forceinline__ floatx4 mfma_block(const Operand<true>& a, const Oper
 #pragma unroll
   for (int i = 0; i < 4; ++i) d = mfma16x16x32(a.v[i], b.v[i], d);
   return d;
-}
-
-// Columns n .. n + 3 of row m, as far as they exist.
-template <bool F32>
-__device__ __forceinline__ void store4(const Fp8Gemm& p, int m, int n, floatx4 v) {
-  const size_t at = (size_t)m * p.ldo + n;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (n + i >= p.N) break;
-    if constexpr (F32) static_cast<float*>(p.out)[at + i] = v[i];
-    else static_cast<uint16_t*>(p.out)[at + i] = f32_to_bf16_bits(v[i]);
-  }
-}
-
-// A buffer from p on (unbounded: the kernels keep their offsets in range).
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p, int bytes = -1) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);
-}
-// An offset behind the end of every buffer of less than 2 GB: loads give 0.
-constexpr uint32_t kNowhere = 0x80000000u;
-__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t src, uint32_t lane_offset, uint32_t offset) {
-  return __builtin_bit_cast(u32x4,
-                            __builtin_amdgcn_raw_buffer_load_b128(src, lane_offset, offset, 0));
-}
-
-// Waits until at most N of this wave's loads are outstanding and its LDS
-// accesses are done, then for the block; no memory access moves across.
-template <int N>
-__device__ __forceinline__ void wait_and_meet() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt((N & 15) | 7 << 4 | (N >> 4) << 14);
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
-// Loads straight to LDS: lane l's 4 or 16 bytes go to dst + 4 l or + 16 l.
-// (As buffer loads: the compiler takes global ones for accesses that may
-// complete out of order with LDS reads, and waits for all of either at each
-// use.)  ONCE: data that no other block reads.
-__device__ __forceinline__ void to_lds4(__amdgpu_buffer_rsrc_t src, uint32_t lane_offset,
-                                          uint32_t offset, void* dst) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)dst, 4,
-                                           lane_offset, offset, 0, 0);
-}
-template <bool ONCE = false>
-__device__ __forceinline__ void to_lds16(__amdgpu_buffer_rsrc_t src, uint32_t lane_offset,
-                                         uint32_t offset, void* dst) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)dst, 16,
-                                           lane_offset, offset, 0, ONCE ? 2 : 0);
-}
-// Waits until at most N of the wave's loads are outstanding and its LDS reads
-// are done; no memory access moves across.
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt((N & 15) | 7 << 4 | (N >> 4) << 14);
-  asm volatile("" ::: "memory");
-}
-
-// The blocks of a call, at most kGridX of them along x (a multiple of the 8 XCDs;
-// a dimension holds less than 2^32 threads): block block_index(), and behind the
-// last one some without work.
-constexpr unsigned kGridX = 1u << 22;
-__device__ __forceinline__ unsigned block_index() { return blockIdx.y * gridDim.x + blockIdx.x; }
-dim3 grid_of(long long blocks) {
-  const long long y = (blocks + kGridX - 1) / kGridX;
-  return dim3((unsigned)std::min<long long>(blocks, kGridX), (unsigned)y);
 }
 
 // ---- few rows --------------------------------------------------------------------
@@ -294,7 +225,7 @@ void fp8_gemm_rows_kernel(Fp8Gemm p) {
       for (int i = 0; i < 4; ++i) s[i] += v[i];
     }
     const int m = m0 + 16 * t + r;
-    if (m < p.M) store4<F32>(p, m, n0 + 4 * g, s);
+    if (m < p.M) store4<F32>(p.out, p.ldo, p.N, m, n0 + 4 * g, s);
   }
 }
 
@@ -493,18 +424,8 @@ void fp8_gemm_tile_kernel(Fp8Gemm p, int tiles_m, int tiles_n) {
   static_assert(BN <= 8 * kBK && SC == 8, "a wave holds a stage's weight scales");
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const int wm = wave / WN, wn = wave % WN;
-  const int r = lane % 16, g = lane / 16;
-  // The hardware hands block b to XCD b % 8: give each XCD a contiguous range
-  // of tiles, and walk them in groups of 8 rows of tiles, column by column,
-  // so that its tiles share operands in its L2.
-  const int total = tiles_m * tiles_n;
-  const int xcd = block_index() % 8, at = block_index() / 8;
-  const int tile = total / 8 * xcd + min(xcd, total % 8) + at;
-  if (at >= total / 8 + (xcd < total % 8 ? 1 : 0)) return;
-  constexpr int GM = 8;
-  const int group = tile / (GM * tiles_n), in_group = tile - group * (GM * tiles_n);
-  const int gm = min(GM, tiles_m - group * GM);
-  const int tm = group * GM + in_group % gm, tn = in_group / gm;
+  int tm, tn;
+  if (!tile_of_block(tiles_m, tiles_n, tm, tn)) return;
   const int m0 = tm * BM, n0 = tn * BN;
   const int nb = (p.K + kBK - 1) / kBK;
 
@@ -553,47 +474,10 @@ void fp8_gemm_tile_kernel(Fp8Gemm p, int tiles_m, int tiles_n) {
     if (kb + (S - 1) * KB < nb) wait_and_meet<(S - 2) * T::kLoads>();
     else wait_and_meet<0>();
   }
-  // Out through LDS, 16 rows at a time: as the MFMA leaves it, a lane has
-  // four columns of one row, and a store would cover 16 rows x 32 bytes.  The
-  // stages are free; each wave uses a part of its own.
-  constexpr int kSize = F32 ? 4 : 2, kCols = 16 * TN;
-  constexpr int kPitch = kCols * kSize + 16;
-  static_assert(W * 16 * kPitch <= S * T::kBytes, "the stages hold the waves' tiles");
-  uint8_t* mine = lds + wave * (16 * kPitch);
-  const int nw = n0 + wn * kCols;
-  constexpr int kVec = 16 / kSize, kLanes = kCols / kVec;   // values of a piece, pieces of a row
-  const bool wide = ((size_t)p.ldo * kSize | (size_t)p.N * kSize | (size_t)p.out) % 16 == 0;
-#pragma unroll
-  for (int t = 0; t < TM; ++t) {
-#pragma unroll
-    for (int q = 0; q < TN; ++q) {
-      uint8_t* to = mine + r * kPitch + (16 * q + 4 * g) * kSize;
-      if constexpr (F32) *reinterpret_cast<floatx4*>(to) = acc[t][q];
-      else
-        *reinterpret_cast<u32x2*>(to) =
-            u32x2{pack_bf16x2(acc[t][q][0], acc[t][q][1]), pack_bf16x2(acc[t][q][2], acc[t][q][3])};
-    }
-    const int mt = m0 + wm * 16 * TM + 16 * t;
-    if (wide) {
-#pragma unroll
-      for (int i = lane; i < 16 * kLanes; i += kWave) {
-        const int row = i / kLanes, c = i % kLanes * kVec;
-        const u32x4 v = ld16(mine + row * kPitch + c * kSize);
-        if (mt + row < p.M && nw + c < p.N)
-          *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(p.out) +
-                                    ((size_t)(mt + row) * p.ldo + nw + c) * kSize) = v;
-      }
-    } else {
-      for (int i = lane; i < 16 * kCols; i += kWave) {
-        const int row = i / kCols, c = i % kCols;
-        if (mt + row >= p.M || nw + c >= p.N) continue;
-        const size_t o = (size_t)(mt + row) * p.ldo + nw + c;
-        const uint8_t* from = mine + row * kPitch + c * kSize;
-        if constexpr (F32) static_cast<float*>(p.out)[o] = *reinterpret_cast<const float*>(from);
-        else static_cast<uint16_t*>(p.out)[o] = *reinterpret_cast<const uint16_t*>(from);
-      }
-    }
-  }
+  // the stages are free; each wave uses a part of its own
+  static_assert(W * tile_store_bytes<TN, F32>() <= S * T::kBytes, "the stages hold the waves' tiles");
+  store_tile<TM, TN, F32>(acc, lds + wave * tile_store_bytes<TN, F32>(), p.out, p.ldo, p.M, p.N,
+                          m0 + wm * 16 * TM, n0 + wn * 16 * TN, lane);
 }
 
 // TO_F32: also for fp32 results (the bf16 operands of a 256 x 256 tile do not fit

@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <atomic>
 #include <climits>
+#include <cmath>
 #include <mutex>
 #include <vector>
 
@@ -764,6 +765,139 @@ int moe_quant_fp8(const moe_quant_desc* desc, const void* x, void* codes, float*
 int moe_silu_mul_quant_fp8(const moe_quant_desc* desc, const void* gu, void* codes, float* scales,
                            moe_stream_t stream) {
   return quant_rows(desc, gu, codes, scales, true, stream);
+}
+
+namespace {
+bool is_float(int32_t dtype) { return dtype == MOE_F32 || dtype == MOE_BF16; }
+
+int mx_rows(const moe_quant_desc* d, const void* values, const void* codes, const void* scales,
+            int per_col, moe::MxRows* p) {
+  if (d == nullptr || d->rows < 1 || d->cols < 1) return MOE_ERR_INVALID_ARG;
+  if (!is_float(d->in_dtype)) return MOE_ERR_INVALID_ARG;
+  if (!values || !codes || !scales || !aligned16(values) || !aligned16(codes)) return MOE_ERR_INVALID_ARG;
+  if (d->cols % 32 != 0) return MOE_ERR_UNSUPPORTED;
+  const bool bf16 = d->in_dtype == MOE_BF16;
+  const int64_t len = per_col * (int64_t)d->cols, nb = d->cols / 32;
+  int st;
+  if ((st = check_stride(d->ld_in, len, bf16 ? 8 : 4)) != MOE_OK ||
+      (st = check_stride(d->ld_codes, d->cols / 2, 16)) != MOE_OK ||
+      (st = check_stride(d->ld_scales, nb, 1)) != MOE_OK)
+    return st;
+  if ((int64_t)d->rows * nb > moe::kMaxMxBlocks) return MOE_ERR_UNSUPPORTED;
+  *p = moe::MxRows{const_cast<void*>(values), static_cast<uint8_t*>(const_cast<void*>(codes)),
+                   static_cast<uint8_t*>(const_cast<void*>(scales)), d->rows, d->cols,
+                   or_dense(d->ld_in, len), or_dense(d->ld_codes, d->cols / 2),
+                   or_dense(d->ld_scales, nb), bf16};
+  return MOE_OK;
+}
+
+int mx_quant(const moe_quant_desc* d, const void* in, void* codes, void* scales, bool silu_mul,
+             moe_stream_t stream) {
+  moe::MxRows p;
+  if (const int st = mx_rows(d, in, codes, scales, silu_mul ? 2 : 1, &p); st != MOE_OK) return st;
+  return moe::launch_mx_quant(p, silu_mul, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK
+                                                                                          : MOE_ERR_HIP;
+}
+}  // namespace
+
+int moe_quant_mxfp4(const moe_quant_desc* desc, const void* x, void* codes, void* scales,
+                    moe_stream_t stream) {
+  return mx_quant(desc, x, codes, scales, false, stream);
+}
+
+int moe_silu_mul_quant_mxfp4(const moe_quant_desc* desc, const void* gu, void* codes,
+                             void* scales, moe_stream_t stream) {
+  return mx_quant(desc, gu, codes, scales, true, stream);
+}
+
+int moe_dequant_mxfp4(const moe_quant_desc* desc, const void* codes, const void* scales,
+                      void* values, moe_stream_t stream) {
+  moe::MxRows p;
+  if (const int st = mx_rows(desc, values, codes, scales, 1, &p); st != MOE_OK) return st;
+  return moe::launch_mx_dequant(p, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+namespace {
+int check_mx_gemm(const moe_mx_gemm_desc* d) {
+  if (d == nullptr || d->M < 1 || d->N < 1 || d->K < 1 || !is_float(d->out_dtype))
+    return MOE_ERR_INVALID_ARG;
+  if (d->K % 32 != 0) return MOE_ERR_UNSUPPORTED;
+  int st;
+  if ((st = check_stride(d->lda, d->K / 2, 16)) != MOE_OK ||
+      (st = check_stride(d->ldb, d->K / 2, 16)) != MOE_OK ||
+      (st = check_stride(d->ld_as, d->K / 32, 1)) != MOE_OK ||
+      (st = check_stride(d->ld_bs, d->K / 32, 1)) != MOE_OK ||
+      (st = check_stride(d->ldo, d->N, 1)) != MOE_OK)
+    return st;
+  if (d->M > kMaxGemmRows || d->N > kMaxGemmRows || (int64_t)d->M * d->N > moe::kMaxGemmArea)
+    return MOE_ERR_UNSUPPORTED;
+  // the tile kernels' offsets from a tile's first row have 32 bits (256 rows)
+  if (std::max(or_dense(d->lda, d->K / 2), or_dense(d->ldb, d->K / 2)) > kMaxGemmStride)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+}  // namespace
+
+int moe_gemm_mxfp4(const moe_mx_gemm_desc* desc, const void* a, const void* a_scale,
+                   const void* b, const void* b_scale, void* out, moe_stream_t stream) {
+  if (desc == nullptr || !a || !a_scale || !b || !b_scale || !out || !aligned16(a) || !aligned16(b))
+    return MOE_ERR_INVALID_ARG;
+  if (const int st = check_mx_gemm(desc); st != MOE_OK) return st;
+  const moe::MxGemm p{static_cast<const uint8_t*>(a), static_cast<const uint8_t*>(a_scale),
+                      static_cast<const uint8_t*>(b), static_cast<const uint8_t*>(b_scale), out,
+                      desc->M, desc->N, desc->K, or_dense(desc->lda, desc->K / 2),
+                      or_dense(desc->ld_as, desc->K / 32), or_dense(desc->ldb, desc->K / 2),
+                      or_dense(desc->ld_bs, desc->K / 32), or_dense(desc->ldo, desc->N),
+                      desc->out_dtype == MOE_F32};
+  return moe::launch_mx_gemm(p, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+namespace {
+// codes null: the form without them
+int norm_rows(const moe_norm_desc* d, const void* x, const void* residual, const void* weight,
+              void* residual_out, void* out, void* codes, float* scales, moe_stream_t stream) {
+  if (d == nullptr || d->rows < 1 || d->cols < 1) return MOE_ERR_INVALID_ARG;
+  if (!is_float(d->x_dtype) || !is_float(d->w_dtype) || (residual && !is_float(d->res_dtype)) ||
+      (out && !is_float(d->out_dtype)))
+    return MOE_ERR_INVALID_ARG;
+  if (!(d->eps >= 0.f) || !std::isfinite(d->eps)) return MOE_ERR_INVALID_ARG;
+  if (!x || !weight || (residual && !residual_out)) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {x, residual, weight, static_cast<const void*>(residual ? residual_out : nullptr),
+                        static_cast<const void*>(out), static_cast<const void*>(codes)})
+    if (!aligned16(p)) return MOE_ERR_INVALID_ARG;   // (null is aligned)
+  if (d->cols % 16 != 0 || d->cols > moe::kMaxNormCols) return MOE_ERR_UNSUPPORTED;
+  const auto multiple = [](int32_t dtype) { return dtype == MOE_BF16 ? 8 : 4; };
+  const int64_t n = d->cols, nb = (n + 127) / 128;
+  int st;
+  if ((st = check_stride(d->ld_x, n, multiple(d->x_dtype))) != MOE_OK) return st;
+  if (residual && ((st = check_stride(d->ld_res, n, multiple(d->res_dtype))) != MOE_OK ||
+                   (st = check_stride(d->ld_res_out, n, multiple(d->res_dtype))) != MOE_OK))
+    return st;
+  if (out && (st = check_stride(d->ld_out, n, multiple(d->out_dtype))) != MOE_OK) return st;
+  if (codes && ((st = check_stride(d->ld_codes, n, 16)) != MOE_OK ||
+                (st = check_stride(d->ld_scales, nb, 1)) != MOE_OK))
+    return st;
+  const moe::NormRows p{x, residual, weight, residual ? residual_out : nullptr, out,
+                        static_cast<uint8_t*>(codes), scales, d->rows, d->cols, d->eps,
+                        or_dense(d->ld_x, n), or_dense(d->ld_res, n), or_dense(d->ld_res_out, n),
+                        or_dense(d->ld_out, n), or_dense(d->ld_codes, n), or_dense(d->ld_scales, nb),
+                        d->x_dtype == MOE_BF16, d->res_dtype == MOE_BF16, d->w_dtype == MOE_BF16,
+                        d->out_dtype == MOE_BF16};
+  return moe::launch_norm(p, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+}  // namespace
+
+int moe_add_rms_norm(const moe_norm_desc* desc, const void* x, const void* residual,
+                     const void* weight, void* residual_out, void* out, moe_stream_t stream) {
+  if (!out) return MOE_ERR_INVALID_ARG;
+  return norm_rows(desc, x, residual, weight, residual_out, out, nullptr, nullptr, stream);
+}
+
+int moe_add_rms_norm_quant_fp8(const moe_norm_desc* desc, const void* x, const void* residual,
+                               const void* weight, void* residual_out, void* out, void* codes,
+                               float* scales, moe_stream_t stream) {
+  if (!codes || !scales) return MOE_ERR_INVALID_ARG;
+  return norm_rows(desc, x, residual, weight, residual_out, out, codes, scales, stream);
 }
 
 size_t moe_block_signal_count(const moe_desc* desc) {

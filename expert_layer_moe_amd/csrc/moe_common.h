@@ -127,6 +127,37 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
   return __fdividef(g, 1.0f + __expf(-g)) * u;
 }
 
+// SiLU as the formula has it: expf to one unit in the last place, a correctly
+// rounded division; 0 from v = -88.8 on, where exp(-v) overflows.  The
+// quantisation of 8192 x 2048 bf16 gates and ups is bound by it: 19.8 to 20.4 us.
+// (With exp2 and reciprocal instructions and a correction each it takes 17.2, but
+// scales are then off by up to 5.3 units of 2^-24 in place of 3.6.)
+__device__ __forceinline__ float silu(float v) { return v / (1.f + expf(-v)); }
+
+// A block of 128 values in e4m3fn, top = max(largest |v|, kFp8Tiny).  One division
+// per lane, r = 1 / scale; every v / scale is then q + (v - q scale) r with
+// q = v r, which is the correctly rounded quotient for a correctly rounded r
+// (Markstein; nothing here comes near overflow, and quotients too small for the
+// remainder to be exact have code 0).
+constexpr float kFp8Max = 448.f, kFp8Tiny = 1e-12f;
+struct Fp8Block {
+  float scale, r, back;
+  __device__ __forceinline__ explicit Fp8Block(float top)
+      // (an infinite scale: no remainder, all finite values are 0)
+      : scale(top / kFp8Max), r(1.f / scale), back(scale < INFINITY ? scale : 0.f) {}
+  // four values to four codes
+  __device__ __forceinline__ uint32_t codes(const float* v) const {
+    float f[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float x = v[k], y = x * r;
+      f[k] = copysignf(fmaf(fmaf(-y, back, x), r, y), x);   // (-0 stays -0)
+    }
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], w, true);
+  }
+};
+
 __device__ __forceinline__ u32x4 ld16(const void* p) {
   return *reinterpret_cast<const u32x4*>(p);
 }

@@ -266,4 +266,55 @@ struct QuantRows {
 constexpr long long kMaxQuantBlocks = (1LL << 31) - 1;
 hipError_t launch_quant(const QuantRows& p, bool silu_mul, hipStream_t s);
 
+// ---- 4-bit microscaled floats ----------------------------------------------------
+// out[M, N] = a[M, K] b[N, K]^T, e2m1 codes two to a byte (lda, ldb in bytes,
+// multiples of 16), e8m0 scale codes sa [M][K / 32], sb [N][K / 32]; K a multiple
+// of 32.
+struct MxGemm {
+  const uint8_t* a;
+  const uint8_t* sa;
+  const uint8_t* b;
+  const uint8_t* sb;
+  void* out;
+  int M, N, K;
+  long long lda, ldsa, ldb, ldsb, ldo;
+  bool out_f32;
+};
+hipError_t launch_mx_gemm(const MxGemm& p, hipStream_t s);
+// Rows of cols values (silu_mul: 2 cols, gate, then up) and their codes and scale
+// codes, cols a multiple of 32; ld_codes in bytes, a multiple of 16; rows of
+// values 16-byte aligned.  The quantisation reads the values, the other writes them.
+struct MxRows {
+  void* values;
+  uint8_t* codes;
+  uint8_t* scales;
+  int rows, cols;
+  long long ld_values, ld_codes, ld_scales;
+  bool bf16;
+};
+// rows x blocks of 32 per row, at most
+constexpr long long kMaxMxBlocks = (1LL << 31) - 1;
+hipError_t launch_mx_quant(const MxRows& p, bool silu_mul, hipStream_t s);
+hipError_t launch_mx_dequant(const MxRows& p, hipStream_t s);
+
+// ---- norm ------------------------------------------------------------------------
+// res_out = r = x + res (r = x without res), out = r / sqrt(mean(r^2) + eps) w, codes
+// and scales of that as launch_quant's; out may be null beside codes.  Strides in
+// elements; cols a multiple of 16, all rows 16-byte aligned.
+struct NormRows {
+  const void* x;
+  const void* res;
+  const void* w;
+  void* res_out;
+  void* out;
+  uint8_t* codes;   // null: out alone
+  float* scales;
+  int rows, cols;
+  float eps;
+  long long ld_x, ld_res, ld_res_out, ld_out, ld_codes, ld_scales;
+  bool x_bf16, res_bf16, w_bf16, out_bf16;
+};
+constexpr int kMaxNormCols = 1 << 15;
+hipError_t launch_norm(const NormRows& p, hipStream_t s);
+
 }  // namespace moe

@@ -13,16 +13,6 @@
 namespace moe {
 namespace {
 
-constexpr float kE4m3Max = 448.f;
-constexpr float kTiny = 1e-12f;
-
-// As the formula has it: expf to one unit in the last place, a correctly rounded
-// division; 0 from v = -88.8 on, where exp(-v) overflows.  8192 x 2048 bf16 gates
-// and ups are bound by it: 19.8 to 20.4 us.  (With exp2 and reciprocal instructions and a
-// correction each they take 17.2, but scales are then off by up to 5.3 units of
-// 2^-24 in place of 3.6.)
-__device__ __forceinline__ float silu(float v) { return v / (1.f + expf(-v)); }
-
 constexpr int kPer = 16;                    // values of a lane: 16 bytes of codes
 constexpr int kLanes = 128 / kPer;          // lanes of a block of 128
 constexpr int kGroups = 256 / kLanes;       // blocks a workgroup does at once
@@ -53,11 +43,8 @@ __device__ __forceinline__ void load(const void* base, size_t off, float (&v)[kP
 
 // One pass: 8 lanes per block of 128 values, 16 values per lane, so that codes
 // leave 16 bytes a lane.  Bound by memory (3 bytes a bf16 value), if the
-// arithmetic stays small: one division per lane, r = 1 / scale; every v / scale
-// is then q + (v - q scale) r with q = v r, which is the correctly rounded
-// quotient for a correctly rounded r (Markstein; nothing here comes near
-// overflow, and quotients too small for the remainder to be exact have code 0).
-// 8192 x 7168 bf16: 32 us, 5.6 TB/s; with a division per value 43.
+// arithmetic stays small (Fp8Block).  8192 x 7168 bf16: 32 us, 5.6 TB/s; with a
+// division per value 43.
 template <bool BF16, bool SILU>
 __global__ __launch_bounds__(256) void quant_kernel(QuantRows p) {
   const uint32_t nb = (p.cols + 127u) / 128, total = (uint32_t)p.rows * nb;   // < 2^31
@@ -80,30 +67,18 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantRows p) {
         for (int i = 0; i < kPer; ++i) v[i] = silu(v[i]) * u[i];
       }
     }
-    float top = kTiny;
+    float top = kFp8Tiny;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) top = fmaxf(top, fabsf(v[i]));
 #pragma unroll
     for (int d = 1; d < kLanes; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-    const float scale = top / kE4m3Max, r = 1.f / scale;
-    // an infinite scale: no remainder, all finite values are 0
-    const float back = scale < INFINITY ? scale : 0.f;
+    const Fp8Block b(top);
     if (!in) continue;
     u32x4 q;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float f[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float x = v[4 * i + k], y = x * r;
-        f[k] = copysignf(fmaf(fmaf(-y, back, x), r, y), x);   // (-0 stays -0)
-      }
-      int w = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
-      w = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], w, true);
-      q[i] = (uint32_t)w;
-    }
+    for (int i = 0; i < 4; ++i) q[i] = b.codes(v + 4 * i);
     *reinterpret_cast<u32x4*>(p.codes + (size_t)row * p.ld_codes + c) = q;
-    if (part == 0) p.scales[(size_t)row * p.ld_scales + kb] = scale;
+    if (part == 0) p.scales[(size_t)row * p.ld_scales + kb] = b.scale;
   }
 }
 

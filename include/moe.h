@@ -368,6 +368,109 @@ int moe_quant_fp8(const moe_quant_desc* desc, const void* x, void* codes, float*
 int moe_silu_mul_quant_fp8(const moe_quant_desc* desc, const void* gu, void* codes,
                            float* scales, moe_stream_t stream);
 
+/* ---- 4-bit microscaled floats (MXFP4) -------------------------------------------
+ * Codes e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives: three bits and a
+ * sign), two to a byte, the first in the low half; one scale code per 32 values
+ * of a row, e8m0: c stands for 2^(c - 127), 255 for NaN.
+ *
+ * Token rows x [rows, cols] -> codes [rows, cols / 2] bytes, scales [rows, cols /
+ * 32] bytes.  Of a block's largest magnitude m: e = floor(log2 m) - 2, at least
+ * -127 (-127 for a block of zeros); scale code e + 127; code = e2m1(x / 2^e), to
+ * the nearest, ties to the even code, magnitudes above 6 (x / 2^e lies below 8)
+ * to 6; the sign is that of x.  A block that holds a NaN or an infinity gets
+ * scale code 255 and codes 0, so that all of it stands for NaN.
+ * The descriptor is moe_quant_fp8's, with cols a multiple of 32, ld_codes in
+ * bytes (0 = cols / 2, else at least that and a multiple of 16) and ld_scales in
+ * bytes (0 = cols / 32, else at least that).  Pointers of values and codes are
+ * 16-byte aligned, scales need no alignment.  Gaps between rows are not written;
+ * codes and scales must not overlap x.  Errors as moe_quant_fp8
+ * (MOE_ERR_UNSUPPORTED for 2^31 blocks of 32 or more). */
+int moe_quant_mxfp4(const moe_quant_desc* desc, const void* x, void* codes, void* scales,
+                    moe_stream_t stream);
+
+/* The same of v = SiLU(g) * u for gu [rows, 2 cols], in moe_silu_mul_quant_fp8's
+ * fp32 arithmetic. */
+int moe_silu_mul_quant_mxfp4(const moe_quant_desc* desc, const void* gu, void* codes,
+                             void* scales, moe_stream_t stream);
+
+/* The values that codes stand for: values [rows, cols] of type in_dtype with row
+ * stride ld_in.  Exact; a value beyond fp32 or bf16 (from 2^128 on) becomes an
+ * infinity, scale code 255 a block of NaN.  Errors as moe_quant_mxfp4. */
+int moe_dequant_mxfp4(const moe_quant_desc* desc, const void* codes, const void* scales,
+                      void* values, moe_stream_t stream);
+
+/* Descriptor of moe_gemm_mxfp4 (host struct).
+ *   M, N, K    >= 1; M and N at most 2^30, M N at most 2^38; K a multiple of 32
+ *   out_dtype  MOE_F32 or MOE_BF16
+ *   lda, ldb   row strides of a and b in bytes: 0 = K / 2, else at least that, a
+ *              multiple of 16, at most 2^23
+ *   ld_as, ld_bs  row strides of a_scale and b_scale in bytes: 0 = K / 32, else
+ *              at least that
+ *   ldo        row stride of out in elements: 0 = N, else at least N */
+typedef struct moe_mx_gemm_desc {
+  int32_t M, N, K;
+  int32_t out_dtype;
+  int64_t lda, ldb, ld_as, ld_bs, ldo;
+} moe_mx_gemm_desc;
+
+/* out[m, n] = sum over blocks b of 32 of 2^(a_scale[m, b] + b_scale[n, b] - 254)
+ *             sum_{k in block b} a[m, k] b[n, k]
+ *   a        [M, K / 2] bytes of e2m1 codes (token rows, moe_quant_mxfp4)
+ *   a_scale  [M, K / 32] e8m0
+ *   b        [N, K / 2] (weights), b_scale [N, K / 32] e8m0
+ *   out      [M, N] out_dtype (must not alias an input)
+ * Products and their sums over four blocks at a time are exact, the sums of those
+ * fp32; rounded once to out_dtype.  Products below 2^-149 may be lost.  A scale
+ * code 255 gives NaN in its row or column.  The bits of a row do not depend on
+ * the other rows' values.  Nothing of out outside its M x N values is written.
+ * a and b are 16-byte aligned, the scales need no alignment.  Errors as
+ * moe_gemm_fp8 (MOE_ERR_UNSUPPORTED for K not a multiple of 32). */
+int moe_gemm_mxfp4(const moe_mx_gemm_desc* desc, const void* a, const void* a_scale,
+                   const void* b, const void* b_scale, void* out, moe_stream_t stream);
+
+/* ---- root-mean-square norm with the residual's addition ------------------------
+ * What stands ahead of the layers in a decoder block.  Descriptor (host struct):
+ *   rows       >= 1
+ *   cols       1..32768, a multiple of 16
+ *   x_dtype    type of x; MOE_F32 or MOE_BF16, like the others
+ *   res_dtype  type of residual and residual_out (not used without a residual)
+ *   w_dtype    type of weight
+ *   out_dtype  type of out (not used if out is null)
+ *   eps        >= 0, finite
+ *   ld_*       row strides in elements: 0 = dense, else at least the row length,
+ *              rows 16-byte aligned (a multiple of 4 for fp32, of 8 for bf16;
+ *              codes: of 16); ld_scales as moe_quant_fp8's */
+typedef struct moe_norm_desc {
+  int32_t rows, cols;
+  int32_t x_dtype, res_dtype, w_dtype, out_dtype;
+  float eps;
+  int64_t ld_x, ld_res, ld_res_out, ld_out, ld_codes, ld_scales;
+} moe_norm_desc;
+
+/* r = x + residual, in fp32, rounded to res_dtype: residual_out
+ * out = r / sqrt(mean(r^2) + eps) * weight, in fp32 from r as it is stored,
+ *       rounded once to out_dtype
+ *   residual      [rows, cols] or NULL (r = x; residual_out is then not used)
+ *   weight        [cols]
+ *   residual_out  [rows, cols]; may be residual itself (same row stride)
+ *   out           [rows, cols]; may be x itself (same type and row stride)
+ * Other outputs must not overlap inputs or each other.  The squares are summed in
+ * fp32: a row whose sum passes its range (values around 2^60) gives zeros, as one
+ * with an infinity does in its finite places (NaN in that one); a row with a NaN
+ * gives NaN.  Bits of a row do not depend on other rows.  MOE_ERR_INVALID_ARG: null
+ * or misaligned pointers (16 bytes), sizes below 1, strides below the row length,
+ * eps below 0 or not finite, other types; MOE_ERR_UNSUPPORTED: cols above 32768
+ * or off its multiple, strides off theirs. */
+int moe_add_rms_norm(const moe_norm_desc* desc, const void* x, const void* residual,
+                     const void* weight, void* residual_out, void* out, moe_stream_t stream);
+
+/* The same with the codes [rows, cols] and scales [rows, ceil(cols / 128)] that
+ * moe_quant_fp8 makes of r / sqrt(mean(r^2) + eps) * weight in fp32 (not of its
+ * rounding to out_dtype); out may be NULL. */
+int moe_add_rms_norm_quant_fp8(const moe_norm_desc* desc, const void* x, const void* residual,
+                               const void* weight, void* residual_out, void* out, void* codes,
+                               float* scales, moe_stream_t stream);
+
 /* One-time re-layout of the expert weights (at load time) into the order in
  * which the layer's MFMA kernels fetch them, so that each wave-wide weight
  * load is one contiguous 1 KB (bf16) / 512 B (fp8) block instead of 16 rows x

@@ -1,0 +1,296 @@
+"""GPU tests of the 4-bit microscaled operators (quantisation, SiLU*mul
+quantisation, values of codes, product) against their formulas in 64 bits.
+
+Bounds (u = 2^-24 for fp32, half a step of bf16 2^-8):
+  codes    a function of the input, equal bit by bit.
+  values   exact.
+  SiLU     v to 16 u (the exponential, a sum, a quotient, a product), so that a
+           code lies between those of v (1 - 16 u) and v (1 + 16 u).
+  product  S = sum of |a b| under their scales.  128 products at a time are exact
+           but for one rounding of accumulator and sum together; up to 8 partial
+           sums meet: ceil(K / 128) + 9 roundings of u of at most S.  bf16
+           results: half a step of the result more."""
+import pytest
+import torch
+
+import expert_layer_moe_amd as moe
+
+pytestmark = pytest.mark.gpu
+U, BF16 = 2.0 ** -24, 2.0 ** -8
+VALUES = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64)
+MIDDLES = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5], dtype=torch.float64)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    moe.load_library()
+
+
+def _pack(codes):
+    return codes[..., ::2] | codes[..., 1::2] << 4
+
+
+def _unpack(codes):
+    return torch.stack([codes & 15, codes >> 4], -1).flatten(-2)
+
+
+def _quant64(x):
+    """(codes [M, K], one to a byte, scale codes) of rows of 64-bit values."""
+    M, K = x.shape
+    wide = x.view(M, K // 32, 32)
+    bad = ~torch.isfinite(wide).all(2)
+    top = torch.where(bad, 1.0, wide.abs().nan_to_num(0, 0, 0).amax(2))
+    # frexp: top = m 2^e with m in [1/2, 1)
+    e = torch.where(top > 0, torch.frexp(top).exponent.long() - 3, -127).clamp(min=-127)
+    q = torch.where(bad[..., None], 0.0, wide) / torch.exp2(e.double())[..., None]
+    below = torch.searchsorted(MIDDLES, q.abs().contiguous())
+    upto = torch.searchsorted(MIDDLES, q.abs().contiguous(), right=True)
+    code = torch.where(upto % 2 == 0, upto, below)   # of a tie the even one
+    code += 8 * torch.signbit(q).long()
+    code[bad] = 0
+    return code.view(M, K).to(torch.uint8), torch.where(bad, 255, e + 127).to(torch.uint8)
+
+
+def _values64(codes, scales):
+    """64-bit values of packed codes under scale codes."""
+    c = _unpack(codes).long()
+    v = VALUES[c & 7] * (1.0 - 2.0 * (c >> 3).double())
+    s = torch.where(scales == 255, float("nan"), torch.exp2(scales.double() - 127))
+    return v * s.repeat_interleave(32, 1)
+
+
+def _rows(seed, M, K, dtype):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(M, K, generator=g) * torch.exp2(torch.randint(-12, 12, (M, K // 32), generator=g)
+                                                   .float()).repeat_interleave(32, 1)
+    return x.to(dtype)
+
+
+def _check_quant(got, x):
+    codes, scales = got
+    want, want_s = _quant64(x.double())
+    assert torch.equal(scales.cpu(), want_s)
+    assert torch.equal(codes.cpu(), _pack(want))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M, K", [(1, 32), (1, 64), (3, 96), (2, 1024), (7, 4128), (129, 544), (1000, 32),
+                                  (64, 7168), (1, 65536)])
+def test_quant(M, K, dtype):
+    x = _rows(M + K, M, K, dtype)
+    _check_quant(moe.moe_quant_mxfp4(x.cuda()), x)
+
+
+def test_every_bf16_value():
+    """Each of the 65536, beside 31 zeros and beside a value of each exponent."""
+    every = torch.arange(65536, dtype=torch.int32).to(torch.uint16).view(torch.bfloat16)
+    x = torch.zeros(65536, 32, dtype=torch.bfloat16)
+    x[:, 5] = every
+    y = x.clone()
+    # the block's largest: of the same exponent or up to 5 more
+    size = every.float().abs()
+    up = torch.exp2(torch.frexp(size).exponent.float() + torch.arange(65536) % 6)
+    y[:, 17] = torch.where(torch.isfinite(up), up, 1.0).bfloat16()
+    for v in (x, y, -y):
+        _check_quant(moe.moe_quant_mxfp4(v.cuda()), v)
+
+
+def test_ties_and_borders_in_fp32():
+    """Midpoints of codes and their fp32 neighbours at scales over the whole
+    range, the smallest ones below the normal numbers."""
+    mid = torch.cat([MIDDLES, torch.tensor([0.0, 6, 7, 7.5], dtype=torch.float64)]).float()
+    near = torch.cat([mid, torch.nextafter(mid, torch.tensor(9.0)),
+                      torch.nextafter(mid, torch.tensor(-9.0))])
+    near = torch.cat([near, near.new_tensor([4.0])])[:32]
+    near = torch.nn.functional.pad(near, (0, 32 - near.numel()))
+    near[31] = 7.9999995   # exponent 2, so that the scale is 1
+    rows = torch.stack([near.double() * 2.0 ** e for e in range(-148, 126)]).float()
+    rows = torch.cat([rows, -rows])
+    _check_quant(moe.moe_quant_mxfp4(rows.cuda()), rows)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_blocks_that_are_not_finite(dtype):
+    """NaN and infinities take their own block and no other."""
+    x = _rows(3, 9, 256, dtype)
+    for i, bad in enumerate((float("nan"), float("inf"), -float("inf"), -float("nan"))):
+        x[2 * i, 32 * i + 7 * i] = bad
+    codes, scales = moe.moe_quant_mxfp4(x.cuda())
+    _check_quant((codes, scales), x)
+    back = moe.moe_dequant_mxfp4(codes, scales).cpu()
+    assert torch.equal(torch.isnan(back).view(9, 8, 32).all(2), scales.cpu() == 255)
+    assert int(torch.isnan(back).sum()) == 4 * 32
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quant_of_strided_rows(dtype):
+    """Strides of input and outputs; gaps stay as they were, scales lie at an odd
+    address."""
+    x = _rows(4, 21, 352, dtype)
+    wide = torch.full((21, 400), float("nan"), dtype=dtype, device="cuda")
+    wide[:, 16:368] = x.cuda()
+    codes = torch.full((23, 208), 0x5A, dtype=torch.uint8, device="cuda")
+    scales = torch.full((23, 17), 0x5B, dtype=torch.uint8, device="cuda")
+    moe.moe_quant_mxfp4(wide[:, 16:368], codes[1:22, 16:192], scales[1:22, 3:14])
+    _check_quant((codes[1:22, 16:192], scales[1:22, 3:14]), x)
+    codes[1:22, 16:192] = 0x5A
+    scales[1:22, 3:14] = 0x5B
+    assert (codes == 0x5A).all() and (scales == 0x5B).all()
+
+
+def _between(got, lo, hi):
+    return (got >= torch.minimum(lo, hi)) & (got <= torch.maximum(lo, hi))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M, I", [(1, 32), (5, 96), (33, 1056), (200, 2048), (17, 4128)])
+def test_silu_mul_quant(M, I, dtype):
+    g = torch.Generator().manual_seed(M + I)
+    gu = (2.5 * torch.randn(M, 2 * I, generator=g)).to(dtype)
+    codes, scales = moe.moe_silu_mul_quant_mxfp4(gu.cuda())
+    gate, up = gu[:, :I].double(), gu[:, I:].double()
+    v = gate * torch.sigmoid(gate) * up
+    lo, hi = v * (1 - 16 * U), v * (1 + 16 * U)
+    (clo, slo), (chi, shi) = _quant64(lo), _quant64(hi)
+    scales = scales.cpu()
+    assert (_between(scales.int(), slo.int(), shi.int())).all()
+    same = (slo == shi).repeat_interleave(32, 1)
+    assert same.double().mean() > 0.99
+    back = _values64(codes.cpu(), scales)
+    inside = _between(back, _values64(_pack(clo), slo), _values64(_pack(chi), shi))
+    assert inside[same].all()
+
+
+def test_silu_of_far_gates():
+    """Gates whose exponential is 0 or infinite: SiLU is the gate, or 0."""
+    gu = torch.zeros(4, 128)
+    gu[0, :64], gu[0, 64:] = 200.0, 3.0
+    gu[1, :64], gu[1, 64:] = -200.0, 3.0
+    gu[2, :64], gu[2, 64:] = float("-inf"), 1.0     # 0 / infinity aside: -inf / inf
+    gu[3, 5] = float("nan")
+    codes, scales = [t.cpu() for t in moe.moe_silu_mul_quant_mxfp4(gu.cuda())]
+    back = _values64(codes, scales)
+    assert (back[0] == 512.0).all()    # 600 = 4.6875 x 2^7, to 4 x 2^7
+    assert (back[1] == 0).all()
+    assert (scales[2] == 255).all() and (scales[3] == torch.tensor([255, 0])).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_dequant_of_every_code_under_every_scale(dtype):
+    codes = torch.randint(0, 256, (256, 16 * 24), dtype=torch.uint8,
+                          generator=torch.Generator().manual_seed(1))
+    codes[:, :16] = _pack(torch.arange(16).repeat(2).to(torch.uint8))
+    scales = torch.arange(256, dtype=torch.uint8)[:, None].repeat(1, 24)
+    got = moe.moe_dequant_mxfp4(codes.cuda(), scales.cuda(), out_dtype=dtype).cpu()
+    want = _values64(codes, scales).to(dtype)
+    nan = torch.isnan(want)
+    assert torch.equal(torch.isnan(got), nan) and int(nan.sum()) == 24 * 32
+    assert torch.equal(got[~nan], want[~nan])
+    assert torch.equal(torch.signbit(got[~nan]), torch.signbit(want[~nan]))
+
+
+@pytest.mark.parametrize("M, K", [(1, 32), (3, 96), (129, 544), (64, 7168)])
+def test_dequant_of_strided_rows(M, K):
+    g = torch.Generator().manual_seed(K)
+    codes = torch.randint(0, 256, (M, K // 2 + 16), generator=g, dtype=torch.uint8).cuda()[:, 16:]
+    scales = torch.randint(90, 160, (M, K // 32 + 5), generator=g, dtype=torch.uint8).cuda()[:, 5:]
+    big = torch.full((M + 2, K + 24), 7.0, device="cuda")
+    out = big[1:M + 1, 8:K + 8]
+    assert moe.moe_dequant_mxfp4(codes, scales.view(torch.float8_e8m0fnu), out=out) is out
+    assert torch.equal(out.double().cpu(), _values64(codes.cpu(), scales.cpu()))
+    big[1:M + 1, 8:K + 8] = 7.0
+    assert (big == 7.0).all()
+
+
+# ---- product ---------------------------------------------------------------------
+def _operands(seed, M, N, K, spread=6):
+    g = torch.Generator().manual_seed(seed)
+    u8 = lambda lo, hi, *shape: torch.randint(lo, hi, shape, generator=g, dtype=torch.uint8)  # noqa: E731
+    return (u8(0, 256, M, K // 2), u8(127 - spread, 128 + spread, M, K // 32),
+            u8(0, 256, N, K // 2), u8(127 - spread, 128 + spread, N, K // 32))
+
+
+def _check_product(out, a, sa, b, sb):
+    K = 2 * a.shape[1]
+    a64, b64 = _values64(a, sa), _values64(b, sb)
+    ref, mag = a64 @ b64.T, a64.abs() @ b64.abs().T
+    tol = (-(-K // 128) + 9) * U * mag
+    if out.dtype == torch.bfloat16:
+        tol = tol * (1 + BF16) + BF16 * ref.abs()
+    off = (out.double().cpu() - ref).abs()
+    assert (off <= tol).all(), float((off / tol.clamp(min=1e-300)).max())
+
+
+SIZES = [(1, 1, 32), (1, 16, 128), (1, 130, 288), (2, 127, 1024), (15, 129, 800), (16, 128, 2048),
+         (17, 1, 544), (31, 65, 256), (33, 1001, 1312), (64, 64, 224), (65, 257, 1152),
+         (100, 384, 1056), (129, 640, 512), (257, 255, 1824), (300, 2048, 256), (1000, 520, 736),
+         (2049, 130, 160), (520, 4100, 288), (16, 4096, 96), (1, 600, 7200), (40, 1000, 2080),
+         (4096, 4090, 544), (3000, 4096, 1056), (16, 1040, 16384), (5, 33, 32)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M, N, K", SIZES)
+def test_product(M, N, K, dtype):
+    a, sa, b, sb = _operands(M * 7 + N * 3 + K, M, N, K)
+    args = a.cuda(), sa.cuda(), b.cuda(), sb.cuda()
+    out = moe.moe_gemm_mxfp4(*args, out_dtype=dtype)
+    _check_product(out, a, sa, b, sb)
+    assert torch.equal(out, moe.moe_gemm_mxfp4(*args, out_dtype=dtype))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M, N, K", [(3, 50, 544), (70, 131, 800), (260, 300, 256), (300, 1000, 1120)])
+def test_product_of_strided_rows(M, N, K, dtype):
+    """Row strides of every operand (those of the scales odd); the gaps of the
+    output and the rows around it stay as they were, also at an odd first column."""
+    a, sa, b, sb = _operands(1, M, N, K)
+    wide = lambda t, pad, value: torch.cat([t, t.new_full((t.shape[0], pad), value)], 1).cuda()[:, :t.shape[1]]  # noqa: E731
+    big = torch.full((M + 2, N + 9), 5.0, dtype=dtype, device="cuda")
+    out = big[1:M + 1, 3:N + 3]
+    moe.moe_gemm_mxfp4(wide(a, 48, 0x77), wide(sa, 3 - sa.shape[1] % 2, 255), wide(b, 16, 0x77),
+                       wide(sb, 5, 255).view(torch.float8_e8m0fnu), out=out)
+    _check_product(out, a, sa, b, sb)
+    big[1:M + 1, 3:N + 3] = 5.0
+    assert (big == 5.0).all()
+
+
+@pytest.mark.parametrize("M, N, K", [(1, 70, 160), (16, 130, 1056), (60, 300, 544), (200, 256, 512),
+                                     (700, 4096, 288)])
+def test_nan_scales_stay_in_their_rows(M, N, K):
+    a, sa, b, sb = [t.cuda() for t in _operands(2, M, N, K)]
+    want = moe.moe_gemm_mxfp4(a, sa, b, sb)
+    sa2, sb2 = sa.clone(), sb.clone()
+    sa2[M // 2, K // 32 - 1] = 255
+    sb2[7, 0] = 255
+    got = moe.moe_gemm_mxfp4(a, sa2, b, sb2)
+    nan = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    nan[M // 2], nan[:, 7] = True, True
+    assert torch.equal(torch.isnan(got), nan)
+    assert torch.equal(got[~nan], want[~nan])
+
+
+@pytest.mark.parametrize("M", [4, 100, 600])
+def test_product_of_largest_codes_and_far_scales(M):
+    """6 x 6 in every place; scales 2^-100 to 2^100 whose products meet, and some
+    that cancel all but small terms."""
+    N, K = 300, 1024
+    a, b = torch.full((M, K // 2), 0x77, dtype=torch.uint8), torch.full((N, K // 2), 0x77, dtype=torch.uint8)
+    sa = torch.tensor([27, 227, 127, 140] * 8, dtype=torch.uint8).repeat(M, 1)
+    sb = torch.tensor([227, 27, 130, 101] * 8, dtype=torch.uint8).repeat(N, 1)
+    b[:, 300:] |= 0x88   # negative from there on
+    for dtype in (torch.float32, torch.bfloat16):
+        out = moe.moe_gemm_mxfp4(a.cuda(), sa.cuda(), b.cuda(), sb.cuda(), out_dtype=dtype)
+        _check_product(out, a, sa, b, sb)
+
+
+def test_rows_behind_each_other_have_the_bits_of_a_smaller_call():
+    """Rows of one call do not change with the others' values."""
+    a, sa, b, sb = [t.cuda() for t in _operands(5, 300, 512, 1024)]
+    want = moe.moe_gemm_mxfp4(a, sa, b, sb)
+    a2 = torch.flip(a, [0]).clone()
+    a2[100] = a[100]
+    sa2 = torch.flip(sa, [0]).clone()
+    sa2[100] = sa[100]
+    assert torch.equal(moe.moe_gemm_mxfp4(a2, sa2, b, sb)[100], want[100])
