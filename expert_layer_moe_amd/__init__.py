@@ -13,6 +13,7 @@ from .binding import (MOE_BF16, MOE_F32, MOE_FP8_E4M3, MOE_LAYOUT_FRAG16,
                       moe_quant_desc, moe_quant_fp8, moe_silu_mul_quant_fp8,
                       moe_mx_gemm_desc, moe_norm_desc, moe_quant_mxfp4,
                       moe_silu_mul_quant_mxfp4, moe_dequant_mxfp4, moe_gemm_mxfp4,
+                      moe_gemm_mxfp4_kernel,
                       moe_add_rms_norm, moe_add_rms_norm_quant_fp8)
 from .layer import DeviceLayer, DenseFP8
 
@@ -27,5 +28,5 @@ __all__ = [
     "moe_gemm_desc", "moe_gemm_fp8", "moe_gemm_fp8_kernel", "moe_quant_desc", "moe_quant_fp8",
     "moe_silu_mul_quant_fp8", "DenseFP8",
     "moe_mx_gemm_desc", "moe_norm_desc", "moe_quant_mxfp4", "moe_silu_mul_quant_mxfp4",
-    "moe_dequant_mxfp4", "moe_gemm_mxfp4", "moe_add_rms_norm", "moe_add_rms_norm_quant_fp8",
+    "moe_dequant_mxfp4", "moe_gemm_mxfp4", "moe_gemm_mxfp4_kernel", "moe_add_rms_norm", "moe_add_rms_norm_quant_fp8",
 ]

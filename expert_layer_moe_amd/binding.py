@@ -25,6 +25,7 @@ EXPORTS = ["moe_workspace_size", "moe_route", "moe_align", "moe_forward",
            "moe_forward_few", "moe_few_workspace_size", "moe_gemm_fp8",
            "moe_gemm_fp8_kernel", "moe_quant_fp8", "moe_silu_mul_quant_fp8",
            "moe_quant_mxfp4", "moe_silu_mul_quant_mxfp4", "moe_dequant_mxfp4", "moe_gemm_mxfp4",
+           "moe_gemm_mxfp4_kernel",
            "moe_add_rms_norm", "moe_add_rms_norm_quant_fp8",
            "moe_forward_noalloc", "moe_forward_signaled", "moe_block_signal_count", "moe_set_signal_wait_us", "moe_set_one_launch",
            "moe_pack_weights", "moe_set_path_thresholds", "moe_set_fp8_mfma", "moe_status_str", "moe_num_stages", "moe_stage_name",
@@ -118,6 +119,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         getattr(lib, name).restype = ctypes.c_int
     lib.moe_gemm_mxfp4.argtypes = [ctypes.POINTER(moe_mx_gemm_desc), P, P, P, P, P, P]
     lib.moe_gemm_mxfp4.restype = ctypes.c_int
+    lib.moe_gemm_mxfp4_kernel.argtypes = [ctypes.POINTER(moe_mx_gemm_desc)]
+    lib.moe_gemm_mxfp4_kernel.restype = ctypes.c_char_p
     lib.moe_add_rms_norm.argtypes = [ctypes.POINTER(moe_norm_desc), P, P, P, P, P, P]
     lib.moe_add_rms_norm.restype = ctypes.c_int
     lib.moe_add_rms_norm_quant_fp8.argtypes = [ctypes.POINTER(moe_norm_desc)] + [P] * 8
@@ -582,6 +585,17 @@ def moe_gemm_mxfp4(a, a_scale, b, b_scale, out=None, out_dtype=torch.bfloat16, s
              moe_mx_gemm_desc(M, N, K, _DT[out.dtype], lda, ldb, ld_as, ld_bs, ldo), a.data_ptr(),
              a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), out.data_ptr())
     return out
+
+
+def moe_gemm_mxfp4_kernel(M: int, N: int, K: int) -> str:
+    """The kernel that moe_gemm_mxfp4 takes for these sizes ("rows 16", "tile 64 x
+    128", ...)."""
+    _sizes(M, N, K)
+    name = load_library().moe_gemm_mxfp4_kernel(
+        ctypes.byref(moe_mx_gemm_desc(M, N, K, _DT[torch.bfloat16], 0, 0, 0, 0, 0)))
+    if name is None:
+        raise MoeError(-2, "sizes that moe_gemm_mxfp4 does not take")
+    return name.decode()
 
 
 # ---- root-mean-square norm with the residual's addition ---------------------------

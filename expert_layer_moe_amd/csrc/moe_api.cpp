@@ -838,6 +838,11 @@ int check_mx_gemm(const moe_mx_gemm_desc* d) {
 }
 }  // namespace
 
+const char* moe_gemm_mxfp4_kernel(const moe_mx_gemm_desc* desc) {
+  if (check_mx_gemm(desc) != MOE_OK) return nullptr;
+  return moe::mx_gemm_kernel_name(desc->M, desc->N, desc->K);
+}
+
 int moe_gemm_mxfp4(const moe_mx_gemm_desc* desc, const void* a, const void* a_scale,
                    const void* b, const void* b_scale, void* out, moe_stream_t stream) {
   if (desc == nullptr || !a || !a_scale || !b || !b_scale || !out || !aligned16(a) || !aligned16(b))

@@ -281,6 +281,8 @@ struct MxGemm {
   bool out_f32;
 };
 hipError_t launch_mx_gemm(const MxGemm& p, hipStream_t s);
+// The kernel it takes (host only).
+const char* mx_gemm_kernel_name(int M, int N, int K);
 // Rows of cols values (silu_mul: 2 cols, gate, then up) and their codes and scale
 // codes, cols a multiple of 32; ld_codes in bytes, a multiple of 16; rows of
 // values 16-byte aligned.  The quantisation reads the values, the other writes them.

@@ -20,26 +20,26 @@
 namespace moe {
 namespace {
 
-constexpr int kBlock = 32;     // values of a block, 16 bytes: a piece
-constexpr int kRow = 128;      // bytes of a step of a row: 8 pieces, 256 values
-constexpr uint32_t kOne = 127; // scale code of 1, for pieces past the end
+constexpr int kBlock = 32;      // values of a block, 16 bytes: a piece
+constexpr int kLine = 128;      // bytes of a row that are loaded at a time: 8 pieces, 256 values
+constexpr uint32_t kOne = 127;  // scale code of 1, for pieces past the end
 
 __device__ __forceinline__ i32x8 operand(u32x4 p) {
-  return __builtin_shufflevector(__builtin_bit_cast(i32x4, p), __builtin_bit_cast(i32x4, p), 0, 1, 2,
-                                 3, -1, -1, -1, -1);
+  const i32x4 v = __builtin_bit_cast(i32x4, p);
+  return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
 }
-// D(16x16, fp32) += A(16x128) * B(128x16) under byte W of wscale and byte A of
-// ascale: lane l has row l % 16 of A, column l % 16 of B, and D[4 (l / 16) + i][l % 16].
-template <int W, int A>
+// D(16x16, fp32) += A(16x128) * B(128x16) under byte I of either scale word: lane l has
+// row l % 16 of A, column l % 16 of B, and D[4 (l / 16) + i][l % 16].
+template <int I>
 __device__ __forceinline__ floatx4 mfma(u32x4 w, uint32_t wscale, u32x4 a, uint32_t ascale, floatx4 c) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w), operand(a), c, 4, 4, W,
-                                                          (int)wscale, A, (int)ascale);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w), operand(a), c, 4, 4, I,
+                                                          (int)wscale, I, (int)ascale);
 }
 
-// Two or four scale codes from any byte address on.
-__device__ __forceinline__ uint32_t load_u16(const uint8_t* p) {
-  uint16_t v;
-  __builtin_memcpy(&v, p, 2);
+// 8 or 16 scale codes from any byte address on.
+__device__ __forceinline__ uint64_t load_u64(const uint8_t* p) {
+  uint64_t v;
+  __builtin_memcpy(&v, p, 8);
   return v;
 }
 __device__ __forceinline__ u32x4 load_u128(const uint8_t* p) {
@@ -49,61 +49,57 @@ __device__ __forceinline__ u32x4 load_u128(const uint8_t* p) {
 }
 
 // ---- few rows --------------------------------------------------------------------
-// One block per 16 columns and 16 MT rows; its 8 waves split the steps of K and
-// meet in LDS.  Bound by reading the weights: they stream through rings in LDS,
-// whole 128-byte lines of 8 rows a load; the token rows and all scales, from L2,
-// through registers.  In a step lane group g takes pieces 2 g and 2 g + 1, whose
-// scale codes lie side by side.
+// One block per 16 columns and 16 rows; its 8 waves split the steps of K (256 values)
+// and meet in LDS.  Bound by reading the weights: they go through LDS, whole 128-byte
+// lines of 8 rows a load; the token rows and all scales, from L2, through registers.
+// MFMA q = 0, 1 of a step takes piece 4 q + g in lane group g, so that a load of token
+// rows covers 64 bytes of each.  kSets steps are on the way at a time (all that a wave
+// has, up to K = 8192); one after the other in the same registers, the compiler waits
+// for all of them at each use: 1 x 4096 x 7168 5.3 us either way.
 //
 // Rows and columns past the end read the last ones, unstored.  The last step, if
-// it ends inside, is a wave's of its own: pieces past the end are zeros under 1.
-template <int MT, bool ONCE>
+// it ends inside, is the last wave's besides: pieces past the end are zeros under 1.
+template <bool ONCE>
 struct Rows {
-  static constexpr int W = 8, kSets = 4, kAhead = kSets - 1;
-  static constexpr int kEntry = 16 * kRow;
-  static constexpr int kLoads = 2 + 1 + 3 * MT;   // of a step, in flight
+  static constexpr int W = 8, kSets = 4;
+  static constexpr int kEntry = 16 * kLine;   // bytes of a step's weights
   __amdgpu_buffer_rsrc_t wbuf, abuf;
-  const uint8_t *wsc, *asc[MT];   // this lane's scale codes of step 0
-  uint32_t wrow[2], arow[MT];
-  u32x4 a[kSets][MT][2];
-  uint32_t sa[kSets][MT], sw[kSets];
-  floatx4 acc[MT];
+  const uint8_t *wsc, *asc;   // this lane's rows of scale codes
+  uint32_t wrow[2], arow;     // and of codes
+  u32x4 a[kSets][2];
+  uint64_t sa[kSets], sw[kSets];
+  floatx4 acc;
 
   __device__ __forceinline__ void issue(uint8_t* __restrict__ to, int step, int set) {
-    const uint32_t k0 = step * kRow;
+    const uint32_t k0 = step * kLine;
 #pragma unroll
     for (int p = 0; p < 2; ++p) to_lds16<ONCE>(wbuf, wrow[p], k0, to + 1024 * p);
-    sw[set] = load_u16(wsc + step * 8);
+    sw[set] = load_u64(wsc + step * 8);
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      a[set][t][0] = load16(abuf, arow[t], k0);
-      a[set][t][1] = load16(abuf, arow[t] + 16, k0);
-      sa[set][t] = load_u16(asc[t] + step * 8);
-    }
+    for (int q = 0; q < 2; ++q) a[set][q] = load16(abuf, arow + 64 * q, k0);
+    sa[set] = load_u64(asc + step * 8);
   }
   // The step in set i and `cur`.
   __device__ __forceinline__ void multiply(const uint8_t* __restrict__ cur, int lane, int i) {
     const int r = lane % 16, g = lane / 16;
-    const u32x4 w0 = ld16(cur + r * kRow + 16 * (2 * g ^ r / 2)),
-                w1 = ld16(cur + r * kRow + 16 * ((2 * g + 1) ^ r / 2));
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      acc[t] = mfma<0, 0>(w0, sw[i], a[i][t][0], sa[i][t], acc[t]);
-      acc[t] = mfma<1, 1>(w1, sw[i], a[i][t][1], sa[i][t], acc[t]);
+    for (int q = 0; q < 2; ++q) {
+      const u32x4 w = ld16(cur + r * kLine + 16 * ((4 * q + g) ^ r / 2));
+      acc = mfma<0>(w, (uint32_t)(sw[i] >> 32 * q) >> 8 * g, a[i][q], (uint32_t)(sa[i] >> 32 * q) >> 8 * g, acc);
     }
   }
 };
 
-template <int MT, bool F32, bool ONCE>
+template <bool F32, bool ONCE>
 __global__ __launch_bounds__(8 * kWave) __attribute__((amdgpu_waves_per_eu(4)))
 void mx_gemm_rows_kernel(MxGemm p) {
-  using RW = Rows<MT, ONCE>;
+  using RW = Rows<ONCE>;
   constexpr int W = RW::W;
   __shared__ __attribute__((aligned(16))) uint8_t ring[W][RW::kSets * RW::kEntry];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const int r = lane % 16, g = lane / 16;
   const int blocks_n = (p.N + 15) / 16;
-  const int n0 = (int)(block_index() % blocks_n) * 16, m0 = (int)(block_index() / blocks_n) * (16 * MT);
+  const int n0 = (int)(block_index() % blocks_n) * 16, m0 = (int)(block_index() / blocks_n) * 16;
   if (m0 >= p.M) return;
   const int nb = p.K / kBlock, steps = nb / 8;   // (whole steps)
   RW rw;
@@ -114,15 +110,11 @@ void mx_gemm_rows_kernel(MxGemm p) {
     const int row = 8 * q + lane / 8;
     rw.wrow[q] = (uint32_t)min(row, p.N - 1 - n0) * (uint32_t)p.ldb + 16 * (lane % 8 ^ row / 2);
   }
-  const int wr = min(r, p.N - 1 - n0);
-  rw.wsc = p.sb + (size_t)(n0 + wr) * p.ldsb + 2 * g;
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const uint32_t m = min(16 * t + r, p.M - 1 - m0);
-    rw.arow[t] = m * (uint32_t)p.lda + 32 * g;
-    rw.asc[t] = p.sa + (size_t)(m0 + m) * p.ldsa + 2 * g;
-    rw.acc[t] = floatx4{0.f, 0.f, 0.f, 0.f};
-  }
+  const int wr = min(r, p.N - 1 - n0), ar = min(r, p.M - 1 - m0);
+  rw.wsc = p.sb + (size_t)(n0 + wr) * p.ldsb;
+  rw.asc = p.sa + (size_t)(m0 + ar) * p.ldsa;
+  rw.arow = (uint32_t)ar * (uint32_t)p.lda + 16 * g;
+  rw.acc = floatx4{0.f, 0.f, 0.f, 0.f};
   const int b0 = (int)((long long)steps * wave / W), n = (int)((long long)steps * (wave + 1) / W) - b0;
   uint8_t* mine = ring[wave];
   for (int j = 0; j < n; j += RW::kSets) {
@@ -133,93 +125,99 @@ void mx_gemm_rows_kernel(MxGemm p) {
 #pragma unroll
     for (int i = 0; i < RW::kSets; ++i)
       if (j + i < n) rw.multiply(mine + i * RW::kEntry, lane, i);
-    wait_loads<0>();
+    wait_loads<0>();   // (the reads of what is loaded over)
   }
   if (const int left = nb - 8 * steps; left != 0 && wave == W - 1) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int piece = 2 * g + h;
+    for (int q = 0; q < 2; ++q) {
+      const int piece = 4 * q + g;
       const bool in = piece < left;
-      const uint32_t k0 = steps * kRow;
+      const uint32_t k0 = steps * kLine;
       const u32x4 zero = {0u, 0u, 0u, 0u};
-      const u32x4 w = in ? load16(rw.wbuf, wr * (uint32_t)p.ldb + 16 * piece, k0) : zero;
-      const uint32_t sw = in ? rw.wsc[steps * 8 + h] : kOne;
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const u32x4 a = in ? load16(rw.abuf, rw.arow[t] + 16 * h, k0) : zero;
-        const uint32_t sa = in ? rw.asc[t][steps * 8 + h] : kOne;
-        rw.acc[t] = mfma<0, 0>(w, sw, a, sa, rw.acc[t]);
-      }
+      const u32x4 w = in ? load16(rw.wbuf, (uint32_t)wr * (uint32_t)p.ldb + 16 * piece, k0) : zero;
+      const u32x4 a = in ? load16(rw.abuf, rw.arow + 64 * q, k0) : zero;
+      rw.acc = mfma<0>(w, in ? rw.wsc[steps * 8 + piece] : kOne, a, in ? rw.asc[steps * 8 + piece] : kOne, rw.acc);
     }
   }
-  floatx4* red = reinterpret_cast<floatx4*>(mine);
-#pragma unroll
-  for (int t = 0; t < MT; ++t) red[t * kWave + lane] = rw.acc[t];
+  reinterpret_cast<floatx4*>(mine)[lane] = rw.acc;
   __syncthreads();
-  for (int t = wave; t < MT; t += W) {
+  if (wave == 0) {
     floatx4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      const floatx4 v = reinterpret_cast<const floatx4*>(ring[w])[t * kWave + lane];
+      const floatx4 v = reinterpret_cast<const floatx4*>(ring[w])[lane];
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[i] += v[i];
     }
-    const int m = m0 + 16 * t + r;
+    const int m = m0 + r;
     if (m < p.M) store4<F32>(p.out, p.ldo, p.N, m, n0 + 4 * g, s);
   }
 }
 
 // ---- tiles ---------------------------------------------------------------------------
 // BM token rows x BN weight rows per block; wave (wm, wn) of WM x WN computes
-// 16 TM rows x 16 TN columns.  Steps of K of both operands go from memory straight
-// to LDS (16 bytes a lane, no registers) into S stages, S - 1 of them ahead of the
-// one that is multiplied: rows of 128 bytes whose piece c lies at place c ^ (row / 2
-// % 8), so that the 16 rows of an operand read fall on all banks once.  Rows past
-// the end read the last one, unstored; pieces past the end are zeros under 1.
+// 16 TM rows x 16 TN columns.  256 values of K of both operands at a time go from
+// memory straight to LDS (16 bytes a lane, no registers) into S stages: rows of 128
+// bytes whose piece c lies at place c ^ (row / 2 % 8), so that an operand read falls on
+// all banks once.  Whole lines, because half a line costs L2 as much as a whole one:
+// 55 bytes a clock and CU, 29 with rows of 64 bytes.  Rows past the end are zeros, unstored; pieces past the end are zeros under 1.
 //
-// MFMA q = 0, 1 of a step takes piece 4 q + g in lane group g.  Scale codes go
-// through registers to LDS, two steps' at a time, so that the four that a lane needs
-// lie in one word: of the 16 codes of a row, g, 4 + g, 8 + g and 12 + g; a lane's
-// rows of its wave's tiles lie side by side.
+// A stage is two halves of one MFMA a tile: half q takes piece 4 q + g in lane group g.
+// While a half is multiplied the operands of the next one are read into registers of
+// their own.  So a stage is read out when its second half begins; then the block meets,
+// with the next stage arrived, and the stage S ahead is loaded over it, a load beside
+// a row of MFMAs (all at once they hold up the reads behind them).
+//
+// Scale codes go through registers to LDS, two stages' at a time, so that the four
+// that a lane needs lie in one word: of the 16 codes of a row, g, 4 + g, 8 + g and
+// 12 + g; a lane's rows of its wave's tiles lie side by side.
+//
+// Bound by the matrix unit for large products: 8192 x 4096 x 7168 takes 112 us, 4.3
+// PFLOP/s, with the unit in use for 72 % of the time, at a clock that its own power
+// sets (1.67 GHz; 1.9 with codes that are all zero).  Smaller ones are bound by the
+// chain of a stage, a wait, a meeting and the reads behind it (0.2 to 0.5 us): 512 rows
+// 15.5 us, 256 rows 11.7.  Measured and not better: 32 x 32 x 64 MFMAs (the unit is 5 %
+// slower with them), waves of 8 x 8 tiles, stages of 128 or 512 values, operands read
+// two halves ahead, waves of a block that split K.
 template <int TM, int TN, int WM, int WN, int S>
 struct Tile {
   static constexpr int W = WM * WN, BM = 16 * TM * WM, BN = 16 * TN * WN;
   static constexpr int LA = BM / 8 / W, LB = BN / 8 / W;   // loads of 8 rows per wave and stage
-  static constexpr int kBytes = (BM + BN) * kRow;          // of a stage
+  static constexpr int kBytes = (BM + BN) * kLine;         // of a stage
   static constexpr int kLoads = LA + LB;                   // a wave's loads of a stage
   static constexpr int kThreads = W * kWave;
   static constexpr int LS = (BM + BN + kThreads - 1) / kThreads;   // rows of scale codes of a thread
-  static constexpr int kScales = (BM + BN) * 16;           // bytes of two steps' scale codes
+  static constexpr int kScales = (BM + BN) * 16;           // bytes of two stages' scale codes
   static_assert(LA * 8 * W == BM && LB * 8 * W == BN, "whole loads");
 
+  struct Operands {
+    u32x4 a[TM], w[TN];
+  };
+  struct Scales {
+    uint32_t a[TM], w[TN];
+  };
+
   int nb;
-  __amdgpu_buffer_rsrc_t abuf, bbuf;         // from the tile's first row on
-  uint32_t aoff[LA], boff[LB];               // this lane's rows and pieces
-  int piece;                                 // of a row's 8, the same in all its rows
+  // from the tile's first row to the last one that is there: rows behind it are zeros
+  __amdgpu_buffer_rsrc_t abuf, bbuf;
+  uint32_t aoff, boff, astep, bstep;         // this lane's first row and piece, to its next row
+  int piece;                                 // of a row's 4, the same in all its rows
+  uint32_t at, bt;                           // its place in the wave's first tiles of a stage
+  uint32_t sat, sbt;                         // its scale words
   const uint8_t* src[LS];                    // this thread's rows of scale codes
-  uint32_t dst[LS], apart[LS];               // and their places: of group 0, between groups
+  uint32_t dst[LS];                          // and their places, of group 0
   u32x4 sc[LS];
 
-  // Loads step `step` into a stage.
-  __device__ __forceinline__ void load(uint8_t* __restrict__ stage, int step, int wave, int lane) {
-    uint8_t* to = stage + wave * 8 * kRow;
-    const uint32_t k0 = step * kRow;
-    const bool in = 8 * step + piece < nb;
-    if (8 * step + 8 > nb && !in) {
-#pragma unroll
-      for (int j = 0; j < LA + LB; ++j)
-        *reinterpret_cast<u32x4*>(to + j * W * 8 * kRow + 16 * lane) = u32x4{0u, 0u, 0u, 0u};
-    }
-    if (in) {
-#pragma unroll
-      for (int j = 0; j < LA; ++j) to_lds16(abuf, aoff[j], k0, to + j * W * 8 * kRow);
-#pragma unroll
-      for (int j = 0; j < LB; ++j) to_lds16(bbuf, boff[j], k0, to + (LA + j) * W * 8 * kRow);
-    }
+  // Load i of stage `stage`'s kLoads; places of pieces past the end get zeros.
+  __device__ __forceinline__ void load_one(uint8_t* __restrict__ to, int stage, int i) {
+    const bool in = 8 * stage + piece < nb;
+    if (i < LA) to_lds16(abuf, (in ? aoff : kNowhere) + i * astep, stage * kLine, to + i * W * 8 * kLine);
+    else to_lds16(bbuf, (in ? boff : kNowhere) + (i - LA) * bstep, stage * kLine, to + i * W * 8 * kLine);
   }
 
-  // The scale codes of steps 2 pair and 2 pair + 1.
+  // The scale codes of stages 2 pair and 2 pair + 1 (past the end: anything).
   __device__ __forceinline__ void load_scales(int pair) {
+    if (16 * pair >= nb) return;
 #pragma unroll
     for (int i = 0; i < LS; ++i) {
       if (16 * pair + 16 <= nb) {
@@ -230,8 +228,9 @@ struct Tile {
           uint32_t v = 0;
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
-            const int at = 16 * pair + 4 * w + b;
-            v |= (at < nb ? (uint32_t)src[i][at] : kOne) << 8 * b;
+            const int k = 16 * pair + 4 * w + b;
+            const uint32_t c = src[i][min(k, nb - 1)];
+            v |= (k < nb ? c : kOne) << 8 * b;
           }
           sc[i][w] = v;
         }
@@ -242,46 +241,83 @@ struct Tile {
   __device__ __forceinline__ void store_scales(uint8_t* __restrict__ to) const {
 #pragma unroll
     for (int i = 0; i < LS; ++i) {
-      if (dst[i] == ~0u) continue;
+      if ((BM + BN) % kThreads != 0 && dst[i] == ~0u) continue;
       const u32x4 v = sc[i];
+      const uint32_t apart = 64 * (TM == TN || dst[i] < 16 * BM ? TM : TN);   // between groups
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const uint32_t sel = 0x0c0c0000u | (uint32_t)(4 + g) << 8 | (uint32_t)g;   // {v1, v0} byte g
         const uint32_t lo = __builtin_amdgcn_perm(v[1], v[0], sel), hi = __builtin_amdgcn_perm(v[3], v[2], sel);
-        *reinterpret_cast<uint32_t*>(to + dst[i] + g * apart[i]) = lo | hi << 16;
+        *reinterpret_cast<uint32_t*>(to + dst[i] + g * apart) = lo | hi << 16;
       }
     }
   }
-  template <int H>
-  __device__ __forceinline__ void step(const uint8_t* __restrict__ cur, int wave, int lane,
-                                       const uint32_t (&sa)[TM], const uint32_t (&sw)[TN],
+  template <int N>
+  static __device__ __forceinline__ void read_words(const uint8_t* from, uint32_t (&to)[N]) {
+    __builtin_memcpy(to, __builtin_assume_aligned(from, N % 4 == 0 ? 16 : 4 * N), 4 * N);
+  }
+  __device__ __forceinline__ void read_scales(const uint8_t* __restrict__ from, Scales& s) const {
+    read_words(from + sat, s.a);
+    read_words(from + sbt, s.w);
+  }
+
+  // Operands of half Q of a stage.
+  template <int Q>
+  __device__ __forceinline__ void read_a(const uint8_t* __restrict__ stage, Operands& o, int t) const {
+    o.a[t] = ld16(stage + (Q ? at ^ 64 : at) + t * 16 * kLine);
+  }
+  template <int Q>
+  __device__ __forceinline__ void read_w(const uint8_t* __restrict__ stage, Operands& o, int q) const {
+    o.w[q] = ld16(stage + (Q ? bt ^ 64 : bt) + q * 16 * kLine);
+  }
+
+  // Byte B of the scales: half B % 2 of a stage, operands in `now`; half Q of `from` is
+  // read into `then`.  LOAD: stage `stage` is loaded into `to`.
+  template <int B, int Q, bool LOAD>
+  __device__ __forceinline__ void half(const uint8_t* __restrict__ from, uint8_t* __restrict__ to, int stage,
+                                       const Operands& now, Operands& then, const Scales& s,
                                        floatx4 (&acc)[TM][TN]) {
-    const int r = lane % 16, g = lane / 16;
-    const int sw0 = 16 * (g ^ (r / 2)), sw1 = sw0 ^ 64;   // places of pieces g, g + 4 of row r
-    const uint8_t* at = cur + (wave / WN * 16 * TM + r) * kRow;
-    const uint8_t* bt = cur + (BM + wave % WN * 16 * TN + r) * kRow;
-    u32x4 w0[TN], w1[TN];
-#pragma unroll
-    for (int q = 0; q < TN; ++q) {
-      w0[q] = ld16(bt + q * 16 * kRow + sw0);
-      w1[q] = ld16(bt + q * 16 * kRow + sw1);
-    }
 #pragma unroll
     for (int t = 0; t < TM; ++t) {
-      const u32x4 a0 = ld16(at + t * 16 * kRow + sw0), a1 = ld16(at + t * 16 * kRow + sw1);
+      // (a row's operand may take the registers of the one that was multiplied last)
 #pragma unroll
-      for (int q = 0; q < TN; ++q) acc[t][q] = mfma<2 * H, 2 * H>(w0[q], sw[q], a0, sa[t], acc[t][q]);
+      for (int q = t * TN / TM; q < (t + 1) * TN / TM; ++q) read_w<Q>(from, then, q);
+      if (t > 0) read_a<Q>(from, then, t - 1);
+      if (t == TM - 1) read_a<Q>(from, then, t);
+      if constexpr (LOAD)
 #pragma unroll
-      for (int q = 0; q < TN; ++q)
-        acc[t][q] = mfma<2 * H + 1, 2 * H + 1>(w1[q], sw[q], a1, sa[t], acc[t][q]);
+        for (int i = t * kLoads / TM; i < (t + 1) * kLoads / TM; ++i) load_one(to, stage, i);
+#pragma unroll
+      for (int q = 0; q < TN; ++q) {
+        acc[t][q] = mfma<B>(now.w[q], s.w[q], now.a[t], s.a[t], acc[t][q]);
+        // here: left to itself the compiler moves MFMAs past reads and barriers
+        asm volatile("" : "+v"(acc[t][q]));
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
+  // Stage st, of parity P, in `cur`, the next one in `next`; stage st + S goes to `to`,
+  // which is `cur`, read out by then.  (The loads wait for no read and the reads for no
+  // load but where this says so: that is what __restrict__ tells the compiler.)
+  template <int P>
+  __device__ __forceinline__ void stage(int st, const uint8_t* __restrict__ cur, const uint8_t* __restrict__ next,
+                                        uint8_t* __restrict__ to, uint8_t* __restrict__ scales, int wave,
+                                        Operands& even, Operands& odd, Scales& s, Scales& s_next,
+                                        floatx4 (&acc)[TM][TN]) {
+    if constexpr (P == 0) {
+      s = s_next;
+      load_scales(st / 2 + 1);
+    }
+    half<2 * P, 1, false>(cur, nullptr, 0, even, odd, s, acc);
+    // (of the two stages to come: loaded a stage ago)
+    if constexpr (P == 1) store_scales(scales);
+    // the next stage has arrived (the S - 2 behind it may still be on their way),
+    // this one is read
+    wait_and_meet<(S - 2) * kLoads>();
+    if constexpr (P == 1) read_scales(scales, s_next);
+    half<2 * P + 1, 0, true>(next, to + wave * 8 * kLine, st + S, odd, even, s, acc);
+  }
 };
-
-template <int N>
-__device__ __forceinline__ void read_words(const uint8_t* from, uint32_t (&to)[N]) {
-  __builtin_memcpy(to, __builtin_assume_aligned(from, N % 4 == 0 ? 16 : 4 * N), 4 * N);
-}
 
 template <int TM, int TN, int WM, int WN, int S, bool F32>
 __global__ __launch_bounds__(WM * WN * kWave) __attribute__((amdgpu_waves_per_eu(TM * TN >= 64 ? 1 : 2)))
@@ -295,19 +331,24 @@ void mx_gemm_tile_kernel(MxGemm p, int tiles_m, int tiles_n) {
   int tm, tn;
   if (!tile_of_block(tiles_m, tiles_n, tm, tn)) return;
   const int m0 = tm * BM, n0 = tn * BN;
-  const int nb = p.K / kBlock, steps = (nb + 7) / 8;
+  const int nb = p.K / kBlock, stages = (nb + 7) / 8;
 
   T tl;
   tl.nb = nb;
-  tl.abuf = buffer_at(p.a + (size_t)m0 * p.lda);
-  tl.bbuf = buffer_at(p.b + (size_t)n0 * p.ldb);
+  const uint32_t lda = (uint32_t)p.lda, ldb = (uint32_t)p.ldb;
+  tl.abuf = buffer_at(p.a + (size_t)m0 * p.lda, (int)((uint32_t)min(BM, p.M - m0) * lda));
+  tl.bbuf = buffer_at(p.b + (size_t)n0 * p.ldb, (int)((uint32_t)min(BN, p.N - n0) * ldb));
   tl.piece = (lane % 8) ^ ((wave * 4 + lane / 16) % 8);
-#pragma unroll
-  for (int j = 0; j < T::LA; ++j)
-    tl.aoff[j] = (uint32_t)min((j * W + wave) * 8 + lane / 8, p.M - 1 - m0) * (uint32_t)p.lda + 16 * tl.piece;
-#pragma unroll
-  for (int j = 0; j < T::LB; ++j)
-    tl.boff[j] = (uint32_t)min((j * W + wave) * 8 + lane / 8, p.N - 1 - n0) * (uint32_t)p.ldb + 16 * tl.piece;
+  tl.aoff = (uint32_t)(wave * 8 + lane / 8) * lda + 16 * tl.piece;
+  tl.boff = (uint32_t)(wave * 8 + lane / 8) * ldb + 16 * tl.piece;
+  tl.astep = W * 8 * lda;
+  tl.bstep = W * 8 * ldb;
+  const int r = lane % 16, g = lane / 16;
+  const int sw = 16 * (g ^ r / 2);
+  tl.at = (wm * 16 * TM + r) * kLine + sw;
+  tl.bt = (BM + wn * 16 * TN + r) * kLine + sw;
+  tl.sat = 4 * (wm * 64 + lane) * TM;
+  tl.sbt = 16 * BM + 4 * (wn * 64 + lane) * TN;
 #pragma unroll
   for (int i = 0; i < T::LS; ++i) {
     const int f = i * T::kThreads + (int)threadIdx.x;   // row of the tile: tokens, then weights
@@ -315,12 +356,10 @@ void mx_gemm_tile_kernel(MxGemm p, int tiles_m, int tiles_n) {
     if (row < BM) {
       tl.src[i] = p.sa + (size_t)(m0 + min(row, p.M - 1 - m0)) * p.ldsa;
       tl.dst[i] = 4 * ((row / (16 * TM) * 64 + row % 16) * TM + row / 16 % TM);
-      tl.apart[i] = 64 * TM;
     } else {
       const int n = row - BM;
       tl.src[i] = p.sb + (size_t)(n0 + min(n, p.N - 1 - n0)) * p.ldsb;
       tl.dst[i] = 16 * BM + 4 * ((n / (16 * TN) * 64 + n % 16) * TN + n / 16 % TN);
-      tl.apart[i] = 64 * TN;
     }
     if (f != row) tl.dst[i] = ~0u;
   }
@@ -333,38 +372,31 @@ void mx_gemm_tile_kernel(MxGemm p, int tiles_m, int tiles_n) {
 
   tl.load_scales(0);
 #pragma unroll
-  for (int i = 0; i < S - 1; ++i)
-    if (i < steps) tl.load(lds + i * T::kBytes, i, wave, lane);
+  for (int i = 0; i < S; ++i)
+#pragma unroll
+    for (int j = 0; j < T::kLoads; ++j) tl.load_one(lds + i * T::kBytes + wave * 8 * kLine, i, j);
   tl.store_scales(scales);
-  wait_and_meet<0>();
-  const uint8_t* my_a = scales + 4 * (wm * 64 + lane) * TM;
-  const uint8_t* my_w = scales + 16 * BM + 4 * (wn * 64 + lane) * TN;
-  int cur = 0, next = S - 1;
-  const auto advance = [&] {
+  wait_and_meet<(S - 1) * T::kLoads>();
+  typename T::Operands even, odd;
+  typename T::Scales s, s_next;
+#pragma unroll
+  for (int q = 0; q < TN; ++q) tl.template read_w<0>(lds, even, q);
+#pragma unroll
+  for (int t = 0; t < TM; ++t) tl.template read_a<0>(lds, even, t);
+  tl.read_scales(scales, s_next);
+  int cur = 0;
+  // (a stage that lies past the end: zeros)
+#pragma unroll 1
+  for (int st = 0; st < stages; st += 2) {
+    uint8_t* sc = scales + ((st / 2 + 1) & 1) * T::kScales;
+    uint8_t* stage = lds + cur * T::kBytes;
     cur = cur + 1 == S ? 0 : cur + 1;
-    next = next + 1 == S ? 0 : next + 1;
-  };
-  for (int st = 0; st < steps; st += 2) {
-    const int turn = st / 2 & 1;
-    uint32_t sa[TM], sw[TN];
-    read_words(my_a + turn * T::kScales, sa);
-    read_words(my_w + turn * T::kScales, sw);
-    if (st + 2 < steps) tl.load_scales(st / 2 + 1);
-    if (st + S - 1 < steps) tl.load(lds + next * T::kBytes, st + S - 1, wave, lane);
-    tl.template step<0>(lds + cur * T::kBytes, wave, lane, sa, sw, acc);
-    advance();
-    // the next stage has arrived (the S - 2 behind it may still be on their
-    // way), this one is free
-    if (st + S - 1 < steps) wait_and_meet<(S - 2) * T::kLoads>();
-    else wait_and_meet<0>();
-    if (st + 1 >= steps) break;
-    if (st + S < steps) tl.load(lds + next * T::kBytes, st + S, wave, lane);
-    tl.template step<1>(lds + cur * T::kBytes, wave, lane, sa, sw, acc);
-    if (st + 2 < steps) tl.store_scales(scales + (turn ^ 1) * T::kScales);
-    advance();
-    if (st + S < steps) wait_and_meet<(S - 2) * T::kLoads>();
-    else wait_and_meet<0>();
+    uint8_t* next = lds + cur * T::kBytes;
+    tl.template stage<0>(st, stage, next, stage, sc, wave, even, odd, s, s_next, acc);
+    cur = cur + 1 == S ? 0 : cur + 1;
+    tl.template stage<1>(st + 1, next, lds + cur * T::kBytes, next, sc, wave, even, odd, s, s_next, acc);
   }
+  wait_and_meet<0>();
   // the stages are free; each wave uses a part of its own
   static_assert(W * tile_store_bytes<TN, F32>() <= S * T::kBytes, "the stages hold the waves' tiles");
   store_tile<TM, TN, F32>(acc, lds + wave * tile_store_bytes<TN, F32>(), p.out, p.ldo, p.M, p.N,
@@ -376,42 +408,92 @@ hipError_t launch_tile(const MxGemm& p, hipStream_t s) {
   constexpr int BM = 16 * TM * WM, BN = 16 * TN * WN;
   const long long tm = ((long long)p.M + BM - 1) / BM, tn = ((long long)p.N + BN - 1) / BN;
   if (tm * tn > kMaxGemmBlocks) return hipErrorInvalidValue;
-  const dim3 grid = grid_of((tm * tn + 7) / 8 * 8);
+  const dim3 grid = grid_of((tm * tn + 7) / 8 * 8), block(WM * WN * kWave);
   if (p.out_f32)
-    hipLaunchKernelGGL((mx_gemm_tile_kernel<TM, TN, WM, WN, S, true>), grid, dim3(WM * WN * kWave), 0, s,
-                       p, (int)tm, (int)tn);
+    hipLaunchKernelGGL((mx_gemm_tile_kernel<TM, TN, WM, WN, S, true>), grid, block, 0, s, p, (int)tm, (int)tn);
   else
-    hipLaunchKernelGGL((mx_gemm_tile_kernel<TM, TN, WM, WN, S, false>), grid, dim3(WM * WN * kWave), 0, s,
-                       p, (int)tm, (int)tn);
+    hipLaunchKernelGGL((mx_gemm_tile_kernel<TM, TN, WM, WN, S, false>), grid, block, 0, s, p, (int)tm, (int)tn);
   return hipGetLastError();
 }
 
-template <int MT>
 hipError_t launch_rows(const MxGemm& p, hipStream_t s) {
-  const long long blocks = ((long long)p.M + 16 * MT - 1) / (16 * MT) * (((long long)p.N + 15) / 16);
+  const long long blocks = ((long long)p.M + 15) / 16 * (((long long)p.N + 15) / 16);
   if (blocks > kMaxGemmBlocks) return hipErrorInvalidValue;
-  const dim3 grid = grid_of(blocks);
-#define MOE_ROWS(F, O) \
-  hipLaunchKernelGGL((mx_gemm_rows_kernel<MT, F, O>), grid, dim3(8 * kWave), 0, s, p)
-  const bool once = p.M <= 16 * MT;   // each weight is read by one block: past the caches
+  const dim3 grid = grid_of(blocks), block(8 * kWave);
+  const bool once = p.M <= 16;   // each weight is read by one block: past the caches
   if (p.out_f32) {
-    if (once) MOE_ROWS(true, true);
-    else MOE_ROWS(true, false);
+    if (once) hipLaunchKernelGGL((mx_gemm_rows_kernel<true, true>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((mx_gemm_rows_kernel<true, false>), grid, block, 0, s, p);
   } else {
-    if (once) MOE_ROWS(false, true);
-    else MOE_ROWS(false, false);
+    if (once) hipLaunchKernelGGL((mx_gemm_rows_kernel<false, true>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((mx_gemm_rows_kernel<false, false>), grid, block, 0, s, p);
   }
-#undef MOE_ROWS
   return hipGetLastError();
+}
+
+// The kernels of different tiles and what they take, launch and all: a start, and us
+// per stage (256 values of K) while each CU has at most one block, and with 256 blocks
+// of as many as a CU holds.  Fitted to 104 shapes, from 12 x 64 x 256 to 8192 x 4096 x
+// 7168: the choice by them is 0.9 % slower than the best kernel of each shape, 15 % at
+// most (1.4 % without 32 x 64).  The two of 128 x 128 differ by their waves, 4 and 8.
+struct Shape {
+  int bm, bn, per_cu;
+  float start, one, full;
+};
+constexpr Shape kTiles[] = {
+    {256, 256, 1, 10.4f, 1.25f, 1.9f}, {128, 256, 1, 7.9f, .78f, 1.1f}, {128, 128, 2, 7.3f, .51f, .70f},
+    {128, 128, 1, 5.8f, .50f, .81f},   {64, 128, 2, 6.7f, .345f, .49f}, {64, 64, 2, 4.8f, .24f, .30f},
+    {32, 64, 3, 5.0f, .19f, .21f},
+};
+
+// The kernel with the least expected time: an index of kTiles, or kRows.  The rows
+// kernel's waves split K: 0.72 us for each step of a wave, in proportion to the blocks
+// beyond one a CU.
+constexpr int kRows = -1;
+int choose(int M, int N, int K) {
+  const auto ceil_div = [](long long a, long long b) { return (a + b - 1) / b; };
+  const long long stages = ceil_div(ceil_div(K, 256), 2) * 2;   // (in twos)
+  int best = kRows;
+  float least = 3.4f + .72f * (float)ceil_div(ceil_div(K, 256), 8) *
+                           std::max(1.f, (float)(ceil_div(M, 16) * ceil_div(N, 16)) / 256.f);
+  if (M <= 16) return best;
+  for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
+    const Shape& k = kTiles[i];
+    const long long blocks = ceil_div(M, k.bm) * ceil_div(N, k.bn);
+    // rounds of the blocks that the chip holds, as far as they are few
+    float each = k.one;
+    if (blocks > 256) {
+      const float rounds = k.per_cu > 1 && blocks <= 512 * k.per_cu
+                               ? (float)blocks / 256.f
+                               : (float)(ceil_div(blocks, 256 * k.per_cu) * k.per_cu);
+      each = k.per_cu == 1 ? k.full * rounds : std::max(k.one, k.full * rounds);
+    }
+    if (const float t = k.start + (float)stages * each; t < least) least = t, best = i;
+  }
+  return best;
 }
 
 }  // namespace
 
+const char* mx_gemm_kernel_name(int M, int N, int K) {
+  static const char* const kNames[] = {"rows 16",        "tile 256 x 256", "tile 128 x 256",
+                                       "tile 128 x 128", "tile 128 x 128 of 8 waves", "tile 64 x 128",
+                                       "tile 64 x 64",   "tile 32 x 64"};
+  static_assert(sizeof(kNames) / sizeof(kNames[0]) == sizeof(kTiles) / sizeof(kTiles[0]) + 1, "names");
+  return kNames[choose(M, N, K) - kRows];
+}
+
 hipError_t launch_mx_gemm(const MxGemm& p, hipStream_t s) {
-  if (p.M <= 16) return launch_rows<1>(p, s);
-  if ((long long)p.M * p.N <= 256LL * 64 * 64) return launch_tile<2, 2, 2, 2, 3>(p, s);
-  if ((long long)p.M * p.N <= 256LL * 128 * 128) return launch_tile<4, 2, 2, 4, 3>(p, s);
-  return launch_tile<8, 4, 2, 4, 2>(p, s);
+  switch (choose(p.M, p.N, p.K)) {
+    case kRows: return launch_rows(p, s);
+    case 0: return launch_tile<8, 4, 2, 4, 2>(p, s);
+    case 1: return launch_tile<4, 4, 2, 4, 3>(p, s);
+    case 2: return launch_tile<4, 4, 2, 2, 2>(p, s);
+    case 3: return launch_tile<4, 2, 2, 4, 4>(p, s);
+    case 4: return launch_tile<2, 4, 2, 2, 3>(p, s);
+    case 5: return launch_tile<2, 2, 2, 2, 3>(p, s);
+    default: return launch_tile<2, 2, 1, 2, 3>(p, s);
+  }
 }
 
 }  // namespace moe

@@ -428,6 +428,11 @@ typedef struct moe_mx_gemm_desc {
 int moe_gemm_mxfp4(const moe_mx_gemm_desc* desc, const void* a, const void* a_scale,
                    const void* b, const void* b_scale, void* out, moe_stream_t stream);
 
+/* The kernel that moe_gemm_mxfp4 takes for a descriptor (host, pure): "rows 16"
+ * (token rows of a block whose waves split K) or "tile 32 x 64" and larger (token
+ * rows x weight rows).  NULL for one that it refuses. */
+const char* moe_gemm_mxfp4_kernel(const moe_mx_gemm_desc* desc);
+
 /* ---- root-mean-square norm with the residual's addition ------------------------
  * What stands ahead of the layers in a decoder block.  Descriptor (host struct):
  *   rows       >= 1

@@ -294,3 +294,54 @@ def test_rows_behind_each_other_have_the_bits_of_a_smaller_call():
     sa2 = torch.flip(sa, [0]).clone()
     sa2[100] = sa[100]
     assert torch.equal(moe.moe_gemm_mxfp4(a2, sa2, b, sb)[100], want[100])
+
+
+@pytest.mark.parametrize("kernel, M, N, K", [
+    # K ends inside a line of 256 values (of 1, 1, 3 and 7 blocks left), with odd and even
+    # numbers of lines, up to several turns of the ring; rows and columns end inside a tile
+    ("rows 16", 3, 200, 5152), ("rows 16", 37, 1001, 8160), ("rows 16", 17, 130, 16416),
+    ("tile 32 x 64", 17, 8200, 1312), ("tile 32 x 64", 20, 6000, 2080), ("tile 32 x 64", 37, 3000, 16416),
+    ("tile 64 x 64", 70, 3000, 864), ("tile 64 x 64", 65, 6000, 2080), ("tile 64 x 64", 130, 4090, 8224),
+    ("tile 64 x 128", 260, 6000, 2080), ("tile 64 x 128", 130, 8200, 4320), ("tile 64 x 128", 260, 4090, 16416),
+    ("tile 128 x 128", 2050, 4090, 288), ("tile 128 x 128", 700, 6000, 1504),
+    ("tile 128 x 128", 1300, 3000, 4128), ("tile 128 x 128 of 8 waves", 1000, 4090, 96),
+    ("tile 128 x 128 of 8 waves", 1300, 2050, 800), ("tile 128 x 128 of 8 waves", 200, 8200, 2272),
+    ("tile 128 x 256", 1300, 4090, 800), ("tile 128 x 256", 520, 8200, 1504), ("tile 128 x 256", 2050, 2050, 16416),
+    ("tile 256 x 256", 2050, 4090, 4128), ("tile 256 x 256", 1300, 6000, 8416),
+])
+def test_product_by_every_kernel_over_long_k(kernel, M, N, K):
+    assert moe.moe_gemm_mxfp4_kernel(M, N, K) == kernel
+    a, sa, b, sb = [t.cuda() for t in _operands(M + N + K, M, N, K)]
+    values = lambda codes, scales: moe.moe_dequant_mxfp4(codes, scales, out_dtype=torch.float32).double()  # noqa: E731
+    a64, b64 = values(a, sa), values(b, sb)
+    ref, mag = a64 @ b64.T, a64.abs() @ b64.abs().T
+    for dtype in (torch.float32, torch.bfloat16):
+        tol = (-(-K // 128) + 9) * U * mag
+        if dtype == torch.bfloat16:
+            tol = tol * (1 + BF16) + BF16 * ref.abs()
+        out = moe.moe_gemm_mxfp4(a, sa, b, sb, out_dtype=dtype)
+        off = (out.double() - ref).abs()
+        assert (off <= tol).all(), float((off / tol).max())
+        for _ in range(3):
+            assert torch.equal(out, moe.moe_gemm_mxfp4(a, sa, b, sb, out_dtype=dtype))
+
+
+def test_the_kernels_over_long_k_are_all_there_are():
+    """Every kernel that some sizes take is among those above."""
+    tested = {case[0] for case in test_product_by_every_kernel_over_long_k.pytestmark[0].args[1]}
+    sizes = [int(2 ** (i / 3)) for i in range(43)]
+    taken = {moe.moe_gemm_mxfp4_kernel(M, N, K) for M in sizes for N in sizes
+             for K in (32, 256, 1024, 2080, 8192, 65536)}
+    assert taken == tested
+
+
+@pytest.mark.parametrize("M, N, K", [(40, 40, 544), (300, 260, 544)])
+def test_product_of_the_widest_rows(M, N, K):
+    """Code rows 2^23 bytes apart, scale rows and results as far: every tile's last row
+    lies up to 2 GB behind its first."""
+    a, sa, b, sb = _operands(11, M, N, K)
+    wide = lambda t: torch.empty(t.shape[0], 1 << 23, dtype=t.dtype, device="cuda")[:, :t.shape[1]].copy_(t)  # noqa: E731
+    out = torch.full((M, 1 << 23), 5.0, dtype=torch.bfloat16, device="cuda")
+    moe.moe_gemm_mxfp4(wide(a), wide(sa), wide(b), wide(sb), out=out[:, 3:N + 3])
+    _check_product(out[:, 3:N + 3], a, sa, b, sb)
+    assert (out[:, :3] == 5.0).all() and (out[:, N + 3:N + 40] == 5.0).all()
