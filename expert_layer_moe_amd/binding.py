@@ -2,12 +2,16 @@
 
 Every step of the layer runs in the library's HIP kernels; this module only
 checks tensor shapes / dtypes / devices and passes raw device pointers and the
-current HIP stream.  PyTorch provides device memory and streams.  There is no
-fallback: if the library is missing, loading raises.
+current HIP stream.  PyTorch provides device memory and streams.  The calls of
+the 4-bit operators and the norm do the same in compiled code (csrc/calls.cpp).
+There is no fallback: if the library or the compiled calls are missing, loading
+raises.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 from typing import Optional
 
@@ -15,6 +19,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "lib", "libmoe_amd.so")
+CALLS_PATH = os.path.join(_HERE, "lib", "_moe_calls.so")
 
 MOE_F32, MOE_BF16, MOE_FP8_E4M3 = 0, 1, 2
 MOE_LAYOUT_ROW_MAJOR, MOE_LAYOUT_FRAG16 = 0, 1
@@ -144,6 +149,27 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_profile_read.restype = ctypes.c_int
     _lib = lib
     return lib
+
+
+_calls = None
+
+
+def _load_calls():
+    """The compiled calls, with this library's entry points."""
+    global _calls
+    lib = load_library()
+    if not os.path.exists(CALLS_PATH):
+        raise RuntimeError(f"{CALLS_PATH} is missing: build it with __graft_entry__.build()")
+    loader = importlib.machinery.ExtensionFileLoader("_moe_calls", CALLS_PATH)
+    calls = importlib.util.module_from_spec(
+        importlib.util.spec_from_file_location("_moe_calls", CALLS_PATH, loader=loader))
+    loader.exec_module(calls)
+    entries = (lib.moe_quant_mxfp4, lib.moe_silu_mul_quant_mxfp4, lib.moe_dequant_mxfp4,
+               lib.moe_gemm_mxfp4, lib.moe_add_rms_norm, lib.moe_add_rms_norm_quant_fp8)
+    calls.bind(*(ctypes.cast(e, ctypes.c_void_p).value for e in entries),
+               torch._C._cuda_getCurrentRawStream, _empty, _check)
+    _calls = calls
+    return calls
 
 
 def _check(status: int):
@@ -494,68 +520,23 @@ def moe_silu_mul_quant_fp8(gu, codes=None, scales=None, stream=None):
 
 
 # ---- 4-bit microscaled floats ---------------------------------------------------
-_BYTES = (torch.uint8,)
-_MX_SCALES = (torch.uint8, torch.float8_e8m0fnu)
-
-
-def _mx_quant(entry, x, per_col, codes, scales, stream):
-    if x.dim() != 2:
-        raise ValueError(f"a matrix expected, not {tuple(x.shape)}")
-    M, n = x.shape
-    if n % (32 * per_col) != 0:
-        raise ValueError(f"a matrix of {32 * per_col} n columns expected, not {tuple(x.shape)}")
-    cols = n // per_col
-    _sizes(M, cols)
-    ld_in = _row_stride(x, "input", _FLOATS, M, n)
-    given = codes, scales
-    ld_codes = ld_scales = 0
-    if codes is None:
-        codes = _empty((M, cols // 2), torch.uint8, x.device, stream)
-    else:
-        ld_codes = _row_stride(codes, "codes", _BYTES, M, cols // 2)
-    if scales is None:
-        scales = _empty((M, cols // 32), torch.uint8, x.device, stream)
-    else:
-        ld_scales = _row_stride(scales, "scales", _MX_SCALES, M, cols // 32)
-    _enqueue(entry, _device_of(x, *given), stream,
-             moe_quant_desc(M, cols, _DT[x.dtype], ld_in, ld_codes, ld_scales), x.data_ptr(),
-             codes.data_ptr(), scales.data_ptr())
-    return codes, scales
-
-
 def moe_quant_mxfp4(x, codes=None, scales=None, stream=None):
     """Token or weight rows x [M, K] (bf16 or fp32; rows may be strided; K a
     multiple of 32) -> e2m1 codes [M, K/2] (uint8, two to a byte, the first in
     the low half) and e8m0 scale codes [M, K/32] (uint8 or, if given,
     float8_e8m0fnu), allocated here when not given.  Returns (codes, scales)."""
-    return _mx_quant(load_library().moe_quant_mxfp4, x, 1, codes, scales, stream)
+    return (_calls or _load_calls()).quant_mxfp4(x, codes, scales, stream)
 
 
 def moe_silu_mul_quant_mxfp4(gu, codes=None, scales=None, stream=None):
     """moe_quant_mxfp4 of SiLU(g) * u for gu [M, 2 I] (gate columns, then up)."""
-    return _mx_quant(load_library().moe_silu_mul_quant_mxfp4, gu, 2, codes, scales, stream)
+    return (_calls or _load_calls()).silu_mul_quant_mxfp4(gu, codes, scales, stream)
 
 
 def moe_dequant_mxfp4(codes, scales, out=None, out_dtype=torch.bfloat16, stream=None):
     """The values [M, K] (bf16 or fp32, exact) of e2m1 codes [M, K/2] under e8m0
     scale codes [M, K/32]; out is allocated here when not given."""
-    if codes.dim() != 2 or codes.shape[1] % 16 != 0:
-        raise ValueError(f"codes [M, 16 n] expected, not {tuple(codes.shape)}")
-    M, K = codes.shape[0], 2 * codes.shape[1]
-    _sizes(M, K)
-    ld_codes = _row_stride(codes, "codes", _BYTES, M, K // 2)
-    ld_scales = _row_stride(scales, "scales", _MX_SCALES, M, K // 32)
-    given, ld_out = out, 0
-    if out is None:
-        if out_dtype not in _FLOATS:
-            raise ValueError(f"out_dtype {out_dtype}: float32 or bfloat16 expected")
-        out = _empty((M, K), out_dtype, codes.device, stream)
-    else:
-        ld_out = _row_stride(out, "out", _FLOATS, M, K)
-    _enqueue(load_library().moe_dequant_mxfp4, _device_of(codes, scales, given), stream,
-             moe_quant_desc(M, K, _DT[out.dtype], ld_out, ld_codes, ld_scales), codes.data_ptr(),
-             scales.data_ptr(), out.data_ptr())
-    return out
+    return (_calls or _load_calls()).dequant_mxfp4(codes, scales, out, out_dtype, stream)
 
 
 def moe_gemm_mxfp4(a, a_scale, b, b_scale, out=None, out_dtype=torch.bfloat16, stream=None):
@@ -563,28 +544,7 @@ def moe_gemm_mxfp4(a, a_scale, b, b_scale, out=None, out_dtype=torch.bfloat16, s
     byte) under e8m0 scale codes a_scale [M, K/32], b_scale [N, K/32] (uint8 or
     float8_e8m0fnu).  All may have wider rows (row strides); out is allocated
     here when not given."""
-    if a.dim() != 2 or b.dim() != 2:
-        raise ValueError("a and b are matrices")
-    M, half = a.shape
-    N = b.shape[0]
-    K = 2 * half
-    _sizes(M, N, K)
-    nb = K // 32
-    lda = _row_stride(a, "a", _BYTES, M, half)
-    ldb = _row_stride(b, "b", _BYTES, N, half)
-    ld_as = _row_stride(a_scale, "a_scale", _MX_SCALES, M, nb)
-    ld_bs = _row_stride(b_scale, "b_scale", _MX_SCALES, N, nb)
-    given, ldo = out, 0
-    if out is None:
-        if out_dtype not in _FLOATS:
-            raise ValueError(f"out_dtype {out_dtype}: float32 or bfloat16 expected")
-        out = _empty((M, N), out_dtype, a.device, stream)
-    else:
-        ldo = _row_stride(out, "out", _FLOATS, M, N)
-    _enqueue(load_library().moe_gemm_mxfp4, _device_of(a, a_scale, b, b_scale, given), stream,
-             moe_mx_gemm_desc(M, N, K, _DT[out.dtype], lda, ldb, ld_as, ld_bs, ldo), a.data_ptr(),
-             a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), out.data_ptr())
-    return out
+    return (_calls or _load_calls()).gemm_mxfp4(a, a_scale, b, b_scale, out, out_dtype, stream)
 
 
 def moe_gemm_mxfp4_kernel(M: int, N: int, K: int) -> str:
@@ -599,32 +559,6 @@ def moe_gemm_mxfp4_kernel(M: int, N: int, K: int) -> str:
 
 
 # ---- root-mean-square norm with the residual's addition ---------------------------
-def _norm_args(x, residual, weight, residual_out, stream):
-    """(rows, columns, strides of x, residual and residual_out, residual_out)"""
-    if x.dim() != 2:
-        raise ValueError(f"a matrix expected, not {tuple(x.shape)}")
-    M, H = x.shape
-    _sizes(M, H)
-    if weight.dtype not in _FLOATS or weight.shape != (H,) or not weight.is_contiguous():
-        raise ValueError(f"weight: {weight.dtype} {tuple(weight.shape)}, expected contiguous "
-                         f"torch.float32 or torch.bfloat16 ({H},)")
-    ld_x = _row_stride(x, "x", _FLOATS, M, H)
-    if residual is None:
-        if residual_out is not None:
-            raise ValueError("residual_out without a residual")
-        return M, H, ld_x, 0, 0, None
-    ld_res, ld_res_out = _row_stride(residual, "residual", _FLOATS, M, H), 0
-    if residual_out is None:
-        residual_out = _empty((M, H), residual.dtype, x.device, stream)
-    else:
-        ld_res_out = _row_stride(residual_out, "residual_out", (residual.dtype,), M, H)
-    return M, H, ld_x, ld_res, ld_res_out, residual_out
-
-
-def _ptr_or_none(t):
-    return None if t is None else t.data_ptr()
-
-
 def moe_add_rms_norm(x, residual, weight, eps=1e-6, out=None, residual_out=None,
                      out_dtype=torch.bfloat16, stream=None):
     """r = x + residual (as stored in residual_out, of residual's type), out =
@@ -632,23 +566,8 @@ def moe_add_rms_norm(x, residual, weight, eps=1e-6, out=None, residual_out=None,
     fp32, H a multiple of 16) and weight [H].  residual None: r = x.
     residual_out may be residual, out may be x; both are allocated here when not
     given.  Returns (out, residual_out), the latter None without a residual."""
-    M, H, ld_x, ld_res, ld_res_out, residual_out = _norm_args(x, residual, weight, residual_out,
-                                                              stream)
-    ld_out = 0
-    if out is None:
-        if out_dtype not in _FLOATS:
-            raise ValueError(f"out_dtype {out_dtype}: float32 or bfloat16 expected")
-        out = _empty((M, H), out_dtype, x.device, stream)
-    else:
-        ld_out = _row_stride(out, "out", _FLOATS, M, H)
-    _enqueue(load_library().moe_add_rms_norm,
-             _device_of(x, residual, weight, residual_out, out), stream,
-             moe_norm_desc(M, H, _DT[x.dtype], 0 if residual is None else _DT[residual.dtype],
-                           _DT[weight.dtype], _DT[out.dtype], eps, ld_x, ld_res, ld_res_out,
-                           ld_out, 0, 0),
-             x.data_ptr(), _ptr_or_none(residual), weight.data_ptr(), _ptr_or_none(residual_out),
-             out.data_ptr())
-    return out, residual_out
+    return (_calls or _load_calls()).add_rms_norm(x, residual, weight, eps, out, residual_out,
+                                                  out_dtype, stream)
 
 
 def moe_add_rms_norm_quant_fp8(x, residual, weight, eps=1e-6, codes=None, scales=None,
@@ -656,27 +575,8 @@ def moe_add_rms_norm_quant_fp8(x, residual, weight, eps=1e-6, codes=None, scales
     """moe_add_rms_norm's result in moe_quant_fp8's codes [M, H] (uint8) and
     scales [M, ceil(H/128)], of its fp32 values; these themselves go to `out`
     (bf16 or fp32) only if it is given.  Returns (codes, scales, residual_out)."""
-    M, H, ld_x, ld_res, ld_res_out, residual_out = _norm_args(x, residual, weight, residual_out,
-                                                              stream)
-    ld_codes = ld_scales = ld_out = 0
-    if codes is None:
-        codes = _empty((M, H), torch.uint8, x.device, stream)
-    else:
-        ld_codes = _row_stride(codes, "codes", _CODES, M, H)
-    if scales is None:
-        scales = _empty((M, (H + 127) // 128), torch.float32, x.device, stream)
-    else:
-        ld_scales = _row_stride(scales, "scales", _F32, M, (H + 127) // 128)
-    if out is not None:
-        ld_out = _row_stride(out, "out", _FLOATS, M, H)
-    _enqueue(load_library().moe_add_rms_norm_quant_fp8,
-             _device_of(x, residual, weight, residual_out, out, codes, scales), stream,
-             moe_norm_desc(M, H, _DT[x.dtype], 0 if residual is None else _DT[residual.dtype],
-                           _DT[weight.dtype], 0 if out is None else _DT[out.dtype], eps, ld_x,
-                           ld_res, ld_res_out, ld_out, ld_codes, ld_scales),
-             x.data_ptr(), _ptr_or_none(residual), weight.data_ptr(), _ptr_or_none(residual_out),
-             _ptr_or_none(out), codes.data_ptr(), scales.data_ptr())
-    return codes, scales, residual_out
+    return (_calls or _load_calls()).add_rms_norm_quant_fp8(
+        x, residual, weight, eps, codes, scales, residual_out, out, stream)
 
 
 SCRATCH_BYTES = 64 << 20   # MOE_SCRATCH_BYTES

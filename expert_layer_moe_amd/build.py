@@ -1,16 +1,19 @@
-"""Compile libmoe_amd.so for gfx950 with hipcc (in-tree, no JIT cache)."""
+"""Compile libmoe_amd.so for gfx950 with hipcc, and the compiled Python calls for this
+interpreter and torch with the host compiler (in-tree, no JIT cache)."""
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libmoe_amd.so")
+CALLS = os.path.join(LIBDIR, "_moe_calls.so")
 
 SOURCES = ["route.hip", "align.hip", "layout.hip", "experts.hip", "gemm.hip",
            "few.hip", "fp8_gemm.hip", "quant.hip", "mxfp4.hip", "mxfp4_gemm.hip", "norm.hip",
@@ -32,6 +35,35 @@ def hipcc() -> str:
     return p
 
 
+def _run(cmd, verbose: bool, noise: str = ""):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    err = "\n".join(l for l in (r.stdout + r.stderr).splitlines() if not noise or noise not in l)
+    if r.returncode != 0:
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed ({r.returncode}):\n{err}")
+    if verbose and err.strip():
+        print(err)
+
+
+def build_calls(verbose: bool = False) -> str:
+    import torch
+    base = os.path.dirname(torch.__file__)
+    inc, lib = os.path.join(base, "include"), os.path.join(base, "lib")
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("no host C++ compiler: the Python calls cannot be built")
+    tmp = CALLS + ".tmp"
+    _run([cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+          "-isystem", sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"),
+          os.path.join(CSRC, "calls.cpp"), "-o", tmp, "-L", lib, f"-Wl,-rpath,{lib}",
+          "-ltorch_python", "-ltorch_cpu", "-lc10"], verbose)
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(LIBDIR, exist_ok=True)
     srcs = []
@@ -41,16 +73,9 @@ def build(verbose: bool = False) -> str:
         srcs += ["-x", "hip", path]
     tmp = LIB + ".tmp"
     cmd = [hipcc()] + HIPCC_FLAGS + ["-I", os.path.join(ROOT, "include"), "-I", CSRC] + srcs + ["-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    noise = "is not a recognized feature for this target"
-    err = "\n".join(l for l in (r.stdout + r.stderr).splitlines() if noise not in l)
-    if r.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({r.returncode}):\n{err}")
-    if verbose and err.strip():
-        print(err)
+    _run(cmd, verbose, noise="is not a recognized feature for this target")
     os.replace(tmp, LIB)
+    build_calls(verbose)
     return LIB
 
 
