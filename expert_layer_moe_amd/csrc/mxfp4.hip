@@ -101,7 +101,7 @@ __device__ __forceinline__ void silu8(float (&v)[kPer]) {
   for (int i = 0; i < kPer; ++i) {
     const float d = 1.f + expf(-v[i]), r0 = __builtin_amdgcn_rcpf(d), r = fmaf(fmaf(-d, r0, 1.f), r0, r0);
     const float q = v[i] * r;
-    v[i] = fmaf(fmaf(-d, q, v[i]), r, q);
+    v[i] = fmaf(-fmaf(d, q, -v[i]), r, q);   // (so that -0 stays -0)
   }
 }
 

@@ -345,3 +345,17 @@ def test_product_of_the_widest_rows(M, N, K):
     moe.moe_gemm_mxfp4(wide(a), wide(sa), wide(b), wide(sb), out=out[:, 3:N + 3])
     _check_product(out[:, 3:N + 3], a, sa, b, sb)
     assert (out[:, :3] == 5.0).all() and (out[:, N + 3:N + 40] == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_silu_of_zeros_keeps_their_signs(dtype):
+    """SiLU(-0) = -0: the codes of zeros of either sign, by ups of either sign, beside a
+    value and among themselves."""
+    gu = torch.zeros(4, 128, dtype=dtype)
+    gu[:, 0:64:3] = -0.0
+    gu[:, 64:] = torch.where(torch.arange(64) % 2 == 0, 2.0, -2.0).to(dtype)
+    gu[2:, 5] = 1.0
+    want, want_s = _quant64((gu[:, :64] * gu[:, 64:]).double())
+    want[2:, 5], want_s[2:, 0] = 7 + 8, 127 - 2   # -2 SiLU(1) = -1.46: -5.8 under 1/4, code -6
+    codes, scales = moe.moe_silu_mul_quant_mxfp4(gu.cuda())
+    assert torch.equal(scales.cpu(), want_s) and torch.equal(codes.cpu(), _pack(want))
