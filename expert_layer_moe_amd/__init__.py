@@ -15,7 +15,7 @@ from .binding import (MOE_BF16, MOE_F32, MOE_FP8_E4M3, MOE_LAYOUT_FRAG16,
                       moe_silu_mul_quant_mxfp4, moe_dequant_mxfp4, moe_gemm_mxfp4,
                       moe_gemm_mxfp4_kernel,
                       moe_add_rms_norm, moe_add_rms_norm_quant_fp8)
-from .layer import DeviceLayer, DenseFP8
+from .layer import DeviceLayer, DenseFP8, DenseFP4
 
 __all__ = [
     "MOE_BF16", "MOE_F32", "MOE_FP8_E4M3", "MOE_LAYOUT_FRAG16", "MOE_LAYOUT_ROW_MAJOR",
@@ -26,7 +26,7 @@ __all__ = [
     "moe_workspace_size", "stage_names", "DeviceLayer",
     "FEW_MAX_ROWS", "alloc_few_workspace", "moe_few_workspace_size", "moe_forward_few",
     "moe_gemm_desc", "moe_gemm_fp8", "moe_gemm_fp8_kernel", "moe_quant_desc", "moe_quant_fp8",
-    "moe_silu_mul_quant_fp8", "DenseFP8",
+    "moe_silu_mul_quant_fp8", "DenseFP8", "DenseFP4",
     "moe_mx_gemm_desc", "moe_norm_desc", "moe_quant_mxfp4", "moe_silu_mul_quant_mxfp4",
     "moe_dequant_mxfp4", "moe_gemm_mxfp4", "moe_gemm_mxfp4_kernel", "moe_add_rms_norm", "moe_add_rms_norm_quant_fp8",
 ]

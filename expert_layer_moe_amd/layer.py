@@ -9,9 +9,10 @@ import torch
 
 from .binding import (MOE_BF16, MOE_F32, MOE_FP8_E4M3, MOE_LAYOUT_FRAG16,
                       MOE_LAYOUT_ROW_MAJOR, _empty, alloc_few_workspace, alloc_workspace,
-                      make_desc, moe_forward, moe_forward_few, moe_forward_signaled,
-                      moe_gemm_fp8, moe_pack_weights, moe_quant_fp8, moe_route,
-                      moe_silu_mul_quant_fp8)
+                      make_desc, moe_add_rms_norm, moe_add_rms_norm_quant_fp8, moe_forward,
+                      moe_forward_few, moe_forward_signaled, moe_gemm_fp8, moe_gemm_mxfp4,
+                      moe_pack_weights, moe_quant_fp8, moe_quant_mxfp4, moe_route,
+                      moe_silu_mul_quant_fp8, moe_silu_mul_quant_mxfp4)
 
 _ACT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 _W = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.uint8: MOE_FP8_E4M3}
@@ -189,6 +190,69 @@ class DenseFP8:
     def forward(self, x, out=None, stream=None):
         """x [T, H] bf16 or fp32 -> out [T, H], bf16 unless `out` is fp32."""
         xq, xs = moe_quant_fp8(x, stream=stream)
+        return self._of_codes(xq, xs, out, stream)
+
+    def forward_normed(self, x, residual, weight, eps=1e-6, out=None, residual_out=None,
+                       stream=None):
+        """forward of moe_add_rms_norm's rows, whose codes leave the norm at once.
+        Returns (out, residual_out); without a residual (None) the latter is None."""
+        xq, xs, kept = moe_add_rms_norm_quant_fp8(x, residual, weight, eps,
+                                                  residual_out=residual_out, stream=stream)
+        return self._of_codes(xq, xs, out, stream), kept
+
+    def _of_codes(self, xq, xs, out, stream):
         gu = moe_gemm_fp8(xq, xs, self.w13, self.s13, out_dtype=self.gate_up, stream=stream)
         hq, hs = moe_silu_mul_quant_fp8(gu, stream=stream)
         return moe_gemm_fp8(hq, hs, self.w2, self.s2, out=out, stream=stream)
+
+
+class DenseFP4:
+    """DenseFP8's block in 4 bits: e2m1 codes, two to a byte, in blocks of 32 under
+    a power of two (e8m0), weights and tokens.
+
+    w13 [2I, H/2] (gate rows, then up rows) and w2 [H, I/2]: uint8, the first of
+    two codes in the low half; scale codes s13 [2I, H/32], s2 [H, I/32], uint8 or
+    float8_e8m0fnu.  H and I multiples of 32.  gate_up: as DenseFP8's.
+    """
+
+    def __init__(self, w13, w2, s13, s2, device="cuda", gate_up=torch.bfloat16):
+        if gate_up not in _ACT:
+            raise ValueError(f"gate_up {gate_up}: torch.float32 or torch.bfloat16 expected")
+        self.gate_up = gate_up
+        self.w13 = w13.to(device).contiguous()
+        self.w2 = w2.to(device).contiguous()
+        self.s13 = s13.to(device).contiguous()
+        self.s2 = s2.to(device).contiguous()
+        self.I, self.H = self.w13.shape[0] // 2, 2 * self.w13.shape[1]
+        if self.H % 32 or self.I % 32 or tuple(self.w13.shape) != (2 * self.I, self.H // 2) or \
+                tuple(self.w2.shape) != (self.H, self.I // 2):
+            raise ValueError("dense weights are w13 [2I, H/2] and w2 [H, I/2], H and I multiples of 32")
+        if tuple(self.s13.shape) != (2 * self.I, self.H // 32) or \
+                tuple(self.s2.shape) != (self.H, self.I // 32):
+            raise ValueError("s13 is [2I, H/32], s2 [H, I/32]")
+        for name in ("w13", "w2", "s13", "s2"):
+            dtype = getattr(self, name).dtype
+            if dtype != torch.uint8 and (name[0] == "w" or dtype != torch.float8_e8m0fnu):
+                raise ValueError(f"{name}: {dtype}, expected torch.uint8")
+
+    @classmethod
+    def quantised(cls, w13, w2, device="cuda", gate_up=torch.bfloat16):
+        """Of weights w13 [2I, H], w2 [H, I] in bf16 or fp32 (moe_quant_mxfp4)."""
+        c13, s13 = moe_quant_mxfp4(w13.to(device))
+        c2, s2 = moe_quant_mxfp4(w2.to(device))
+        return cls(c13, c2, s13, s2, device, gate_up)
+
+    def forward(self, x, out=None, stream=None):
+        """x [T, H] bf16 or fp32 -> out [T, H], bf16 unless `out` is fp32."""
+        xq, xs = moe_quant_mxfp4(x, stream=stream)
+        gu = moe_gemm_mxfp4(xq, xs, self.w13, self.s13, out_dtype=self.gate_up, stream=stream)
+        hq, hs = moe_silu_mul_quant_mxfp4(gu, stream=stream)
+        return moe_gemm_mxfp4(hq, hs, self.w2, self.s2, out=out, stream=stream)
+
+    def forward_normed(self, x, residual, weight, eps=1e-6, out=None, residual_out=None,
+                       stream=None):
+        """forward of moe_add_rms_norm's rows (in bf16).  Returns (out,
+        residual_out); without a residual (None) the latter is None."""
+        normed, kept = moe_add_rms_norm(x, residual, weight, eps, residual_out=residual_out,
+                                        stream=stream)
+        return self.forward(normed, out, stream), kept
