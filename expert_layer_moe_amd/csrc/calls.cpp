@@ -128,7 +128,10 @@ struct Call {
     return t;
   }
   void on_device(const at::Tensor& t) {
-    if (!t.is_cuda()) refuse("tensors must be on the GPU");
+    if (!t.is_cuda()) {
+      off_gpu_ = true;   // (said behind what is wrong with the tensors themselves)
+      return;
+    }
     const int d = t.get_device();
     if (device_ >= 0 && d != device_) refuse("tensors on cuda:%d and cuda:%d: one GPU expected", device_, d);
     device_ = d;
@@ -137,6 +140,7 @@ struct Call {
   // A result that is written on the call's stream (its memory is reused in that
   // stream's order).
   at::Tensor empty(int64_t rows, int64_t cols, at::ScalarType dtype) const {
+    all_on_gpu();
     const int64_t size[2] = {rows, cols}, stride[2] = {cols, 1};
     if (stream_ == Py_None)
       return at::empty_strided(at::IntArrayRef(size, 2), at::IntArrayRef(stride, 2),
@@ -155,6 +159,7 @@ struct Call {
   // The entry point with that GPU current, on the given stream or its current one.
   template <typename F>
   void enqueue(F&& launch) const {
+    all_on_gpu();
     void* stream;
     if (stream_ == Py_None) {
       const Ref index(PyLong_FromLong(device_));
@@ -179,7 +184,11 @@ struct Call {
   }
 
  private:
+  void all_on_gpu() const {
+    if (off_gpu_) refuse("tensors must be on the GPU");
+  }
   PyObject* stream_;
+  bool off_gpu_ = false;
   int device_ = -1;
 };
 

@@ -221,8 +221,12 @@ class DenseFP4:
         self.gate_up = gate_up
         self.w13 = w13.to(device).contiguous()
         self.w2 = w2.to(device).contiguous()
-        self.s13 = s13.to(device).contiguous()
-        self.s2 = s2.to(device).contiguous()
+        for name, t in (("w13", w13), ("w2", w2), ("s13", s13), ("s2", s2)):
+            if t.dtype != torch.uint8 and (name[0] == "w" or t.dtype != torch.float8_e8m0fnu):
+                raise ValueError(f"{name}: {t.dtype}, expected torch.uint8")
+        # (as bytes: torch does not pickle all of its 8-bit types)
+        self.s13 = s13.to(device).contiguous().view(torch.uint8)
+        self.s2 = s2.to(device).contiguous().view(torch.uint8)
         self.I, self.H = self.w13.shape[0] // 2, 2 * self.w13.shape[1]
         if self.H % 32 or self.I % 32 or tuple(self.w13.shape) != (2 * self.I, self.H // 2) or \
                 tuple(self.w2.shape) != (self.H, self.I // 2):
@@ -230,10 +234,6 @@ class DenseFP4:
         if tuple(self.s13.shape) != (2 * self.I, self.H // 32) or \
                 tuple(self.s2.shape) != (self.H, self.I // 32):
             raise ValueError("s13 is [2I, H/32], s2 [H, I/32]")
-        for name in ("w13", "w2", "s13", "s2"):
-            dtype = getattr(self, name).dtype
-            if dtype != torch.uint8 and (name[0] == "w" or dtype != torch.float8_e8m0fnu):
-                raise ValueError(f"{name}: {dtype}, expected torch.uint8")
 
     @classmethod
     def quantised(cls, w13, w2, device="cuda", gate_up=torch.bfloat16):

@@ -359,3 +359,46 @@ def test_silu_of_zeros_keeps_their_signs(dtype):
     want[2:, 5], want_s[2:, 0] = 7 + 8, 127 - 2   # -2 SiLU(1) = -1.46: -5.8 under 1/4, code -6
     codes, scales = moe.moe_silu_mul_quant_mxfp4(gu.cuda())
     assert torch.equal(scales.cpu(), want_s) and torch.equal(codes.cpu(), _pack(want))
+
+
+def test_quant_and_values_of_rows_far_apart():
+    """Rows 2^28 values, and codes and scales 2^28 bytes apart: the last one lies 2^31
+    values and 2^32 bytes behind."""
+    M, K = 17, 96
+    x = _rows(3, M, K, torch.bfloat16)
+    gu = torch.cat([x, x.flip(1)], 1)
+    want, want_s = moe.moe_quant_mxfp4(x.cuda())
+    silu, silu_s = moe.moe_silu_mul_quant_mxfp4(gu.cuda())
+    big = torch.empty(M, 1 << 28, dtype=torch.bfloat16, device="cuda")
+    bytes_ = torch.empty(M, 1 << 28, dtype=torch.uint8, device="cuda")
+    vx, vg, vo = big[:, 8:8 + K], big[:, 1024:1024 + 2 * K], big[:, 2048:2048 + K]
+    vx.copy_(x)
+    vg.copy_(gu)
+    vc, vs = bytes_[:, 16:16 + K // 2], bytes_[:, 1001:1001 + K // 32]
+    moe.moe_quant_mxfp4(vx, codes=vc, scales=vs)
+    assert torch.equal(vc, want) and torch.equal(vs, want_s)
+    moe.moe_dequant_mxfp4(vc, vs, out=vo)
+    assert torch.equal(vo.double().cpu(), _values64(want.cpu(), want_s.cpu()))
+    moe.moe_silu_mul_quant_mxfp4(vg, codes=vc, scales=vs)
+    assert torch.equal(vc, silu) and torch.equal(vs, silu_s)
+
+
+def test_more_blocks_than_a_grid_takes_at_once():
+    """2^31 + 2^20 values to codes and 2^32 + 2^20 back: the workgroups take a second turn."""
+    K = 1 << 20
+    x = _rows(4, 1, K, torch.bfloat16).cuda()
+    want, want_s = moe.moe_quant_mxfp4(x)
+    codes, scales = moe.moe_quant_mxfp4(x.expand(2049, K).contiguous())
+    assert torch.equal(scales, want_s.expand(2049, -1)) and (codes == want).all()
+    del codes, scales
+    out = moe.moe_dequant_mxfp4(want.expand(4097, -1).contiguous(), want_s.expand(4097, -1).contiguous())
+    one = moe.moe_dequant_mxfp4(want, want_s)
+    assert all(torch.equal(part, one.expand_as(part)) for part in out.split(512))
+
+
+@pytest.mark.parametrize("M, N, K", [(5, 40, 800), (70, 131, 800), (300, 300, 1120)])
+def test_product_with_scales_at_odd_addresses(M, N, K):
+    a, sa, b, sb = _operands(6, M, N, K)
+    odd = lambda t: torch.cat([t.new_full((t.shape[0], 1), 255), t], 1).cuda()[:, 1:]  # noqa: E731
+    out = moe.moe_gemm_mxfp4(a.cuda(), odd(sa), b.cuda(), odd(sb), out_dtype=torch.float32)
+    _check_product(out, a, sa, b, sb)

@@ -173,3 +173,42 @@ def test_rows_do_not_depend_on_how_many():
     for i in (0, 7, 599):
         one, _ = moe.moe_add_rms_norm(x[i:i + 1], res[i:i + 1], w)
         assert torch.equal(one[0], all_rows[i])
+
+
+@pytest.mark.parametrize("dtype", [B, F])
+@pytest.mark.parametrize("H", [16, 528, 1296, 5136, 8208, 16400, 32752])
+def test_in_place_where_rows_end_inside_a_wave(dtype, H):
+    """Lanes behind a row's end read its last values, which others may have replaced."""
+    x, res, w = [t.cuda() for t in _inputs(H, 300, H, dtype, dtype, dtype)]
+    want, kept = moe.moe_add_rms_norm(x, res, w, out_dtype=dtype)
+    codes, scales, _ = moe.moe_add_rms_norm_quant_fp8(x, res, w)
+    for _ in range(3):
+        x2, res2 = x.clone(), res.clone()
+        got_c, got_s, got_r = moe.moe_add_rms_norm_quant_fp8(x2, res2, w, residual_out=res2, out=x2)
+        assert got_r is res2 and torch.equal(x2, want) and torch.equal(res2, kept)
+        assert torch.equal(got_c, codes) and torch.equal(got_s, scales)
+
+
+def test_more_rows_than_blocks():
+    M = (1 << 20) + 3
+    x, res, w = [t.cuda() for t in _inputs(7, 1000, 16, B, B, B)]
+    want, kept = moe.moe_add_rms_norm(x, res, w)
+    at = torch.arange(M, device="cuda") % 1000
+    out, r = moe.moe_add_rms_norm(x[at], res[at], w)
+    assert torch.equal(out, want[at]) and torch.equal(r, kept[at])
+
+
+def test_rows_far_apart():
+    """Rows 2^28 values apart: the last one lies 2^31 values and 2^32 bytes behind."""
+    M, H = 9, 400
+    x, res, w = [t.cuda() for t in _inputs(8, M, H, B, B, F)]
+    want = moe.moe_add_rms_norm_quant_fp8(x, res, w, out=(want_out := torch.empty_like(x)))
+    big = torch.empty(M, 1 << 28, dtype=B, device="cuda")
+    vx, vr, vk, vo = [big[:, 1024 * i:1024 * i + H] for i in range(4)]
+    vx.copy_(x)
+    vr.copy_(res)
+    vc = torch.empty(M, 1 << 28, dtype=torch.uint8, device="cuda")[:, 16:16 + H]
+    vs = torch.empty(M, 1 << 28, dtype=F, device="cuda")[:, 1:5]
+    moe.moe_add_rms_norm_quant_fp8(vx, vr, w, codes=vc, scales=vs, residual_out=vk, out=vo)
+    for got, wanted in zip((vc, vs, vk, vo), (*want, want_out)):
+        assert torch.equal(got, wanted)
