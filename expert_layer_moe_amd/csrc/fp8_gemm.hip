@@ -424,6 +424,7 @@ void fp8_gemm_tile_kernel(Fp8Gemm p, int tiles_m, int tiles_n) {
   static_assert(BN <= 8 * kBK && SC == 8, "a wave holds a stage's weight scales");
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const int wm = wave / WN, wn = wave % WN;
+  const int r = lane % 16, g = lane / 16;
   int tm, tn;
   if (!tile_of_block(tiles_m, tiles_n, tm, tn)) return;
   const int m0 = tm * BM, n0 = tn * BN;
@@ -477,7 +478,7 @@ void fp8_gemm_tile_kernel(Fp8Gemm p, int tiles_m, int tiles_n) {
   // the stages are free; each wave uses a part of its own
   static_assert(W * tile_store_bytes<TN, F32>() <= S * T::kBytes, "the stages hold the waves' tiles");
   store_tile<TM, TN, F32>(acc, lds + wave * tile_store_bytes<TN, F32>(), p.out, p.ldo, p.M, p.N,
-                          m0 + wm * 16 * TM, n0 + wn * 16 * TN, lane);
+                          m0 + wm * 16 * TM, n0 + wn * 16 * TN, lane, r, g);
 }
 
 // TO_F32: also for fp32 results (the bf16 operands of a 256 x 256 tile do not fit

@@ -97,18 +97,18 @@ __device__ __forceinline__ bool tile_of_block(int tiles_m, int tiles_n, int& tm,
 
 // A wave's 16 TM rows x 16 TN columns, from row m0 and column n0 on, out through
 // `mine`, its part of LDS (tile_store_bytes), 16 rows at a time: as the MFMA leaves
-// it, a lane has four columns of one row, and a store would cover 16 rows x 32 bytes.
+// it, lane (r, g) = (lane % 16, lane / 16) has four columns of one row, and a store
+// would cover 16 rows x 32 bytes.
 template <int TN, bool F32>
 constexpr int tile_store_bytes() {
   return 16 * (16 * TN * (F32 ? 4 : 2) + 16);
 }
 template <int TM, int TN, bool F32>
 __device__ __forceinline__ void store_tile(const floatx4 (&acc)[TM][TN], uint8_t* mine, void* out,
-                                           long long ldo, int M, int N, int m0, int n0, int lane) {
+                                           long long ldo, int M, int N, int m0, int n0, int lane, int r, int g) {
   constexpr int kSize = F32 ? 4 : 2, kCols = 16 * TN;
   constexpr int kPitch = kCols * kSize + 16;
   constexpr int kVec = 16 / kSize, kLanes = kCols / kVec;   // values of a piece, pieces of a row
-  const int r = lane % 16, g = lane / 16;
   const bool wide = ((size_t)ldo * kSize | (size_t)N * kSize | (size_t)out) % 16 == 0;
 #pragma unroll
   for (int t = 0; t < TM; ++t) {

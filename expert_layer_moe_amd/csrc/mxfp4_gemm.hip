@@ -400,7 +400,7 @@ void mx_gemm_tile_kernel(MxGemm p, int tiles_m, int tiles_n) {
   // the stages are free; each wave uses a part of its own
   static_assert(W * tile_store_bytes<TN, F32>() <= S * T::kBytes, "the stages hold the waves' tiles");
   store_tile<TM, TN, F32>(acc, lds + wave * tile_store_bytes<TN, F32>(), p.out, p.ldo, p.M, p.N,
-                          m0 + wm * 16 * TM, n0 + wn * 16 * TN, lane);
+                          m0 + wm * 16 * TM, n0 + wn * 16 * TN, lane, r, g);
 }
 
 template <int TM, int TN, int WM, int WN, int S>
