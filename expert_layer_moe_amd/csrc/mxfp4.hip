@@ -198,27 +198,16 @@ dim3 grid_for(const MxRows& p, long long each) {
 hipError_t launch_mx_quant(const MxRows& p, bool silu_mul, hipStream_t s) {
   if ((long long)p.rows * (p.cols / kMx) > kMaxMxBlocks) return hipErrorInvalidValue;
   const Divider d = divider(p.cols / kMx);
-#define MOE_Q(B, S) hipLaunchKernelGGL((mx_quant_kernel<B, S>), grid_for(p, kThreads / kLanes), dim3(kThreads), 0, s, p, d)
-  if (p.bf16) {
-    if (silu_mul) MOE_Q(true, true);
-    else MOE_Q(true, false);
-  } else {
-    if (silu_mul) MOE_Q(false, true);
-    else MOE_Q(false, false);
-  }
-#undef MOE_Q
-  return hipGetLastError();
+  const auto kernel = p.bf16 ? silu_mul ? mx_quant_kernel<true, true> : mx_quant_kernel<true, false>
+                             : silu_mul ? mx_quant_kernel<false, true> : mx_quant_kernel<false, false>;
+  return enqueue(kernel, grid_for(p, kThreads / kLanes), dim3(kThreads), s, p, d);
 }
 
 hipError_t launch_mx_dequant(const MxRows& p, hipStream_t s) {
   if ((long long)p.rows * (p.cols / kMx) > kMaxMxBlocks) return hipErrorInvalidValue;
   const Divider d = divider(p.cols / kMx);
-#define MOE_D(B) \
-  hipLaunchKernelGGL((mx_dequant_kernel<B>), grid_for(p, Dequant<B>::kEach), dim3(kThreads), 0, s, p, d)
-  if (p.bf16) MOE_D(true);
-  else MOE_D(false);
-#undef MOE_D
-  return hipGetLastError();
+  if (p.bf16) return enqueue(mx_dequant_kernel<true>, grid_for(p, Dequant<true>::kEach), dim3(kThreads), s, p, d);
+  return enqueue(mx_dequant_kernel<false>, grid_for(p, Dequant<false>::kEach), dim3(kThreads), s, p, d);
 }
 
 }  // namespace moe

@@ -409,11 +409,9 @@ hipError_t launch_tile(const MxGemm& p, hipStream_t s) {
   const long long tm = ((long long)p.M + BM - 1) / BM, tn = ((long long)p.N + BN - 1) / BN;
   if (tm * tn > kMaxGemmBlocks) return hipErrorInvalidValue;
   const dim3 grid = grid_of((tm * tn + 7) / 8 * 8), block(WM * WN * kWave);
-  if (p.out_f32)
-    hipLaunchKernelGGL((mx_gemm_tile_kernel<TM, TN, WM, WN, S, true>), grid, block, 0, s, p, (int)tm, (int)tn);
-  else
-    hipLaunchKernelGGL((mx_gemm_tile_kernel<TM, TN, WM, WN, S, false>), grid, block, 0, s, p, (int)tm, (int)tn);
-  return hipGetLastError();
+  const auto kernel = p.out_f32 ? mx_gemm_tile_kernel<TM, TN, WM, WN, S, true>
+                                : mx_gemm_tile_kernel<TM, TN, WM, WN, S, false>;
+  return enqueue(kernel, grid, block, s, p, (int)tm, (int)tn);
 }
 
 hipError_t launch_rows(const MxGemm& p, hipStream_t s) {
@@ -421,14 +419,9 @@ hipError_t launch_rows(const MxGemm& p, hipStream_t s) {
   if (blocks > kMaxGemmBlocks) return hipErrorInvalidValue;
   const dim3 grid = grid_of(blocks), block(8 * kWave);
   const bool once = p.M <= 16;   // each weight is read by one block: past the caches
-  if (p.out_f32) {
-    if (once) hipLaunchKernelGGL((mx_gemm_rows_kernel<true, true>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((mx_gemm_rows_kernel<true, false>), grid, block, 0, s, p);
-  } else {
-    if (once) hipLaunchKernelGGL((mx_gemm_rows_kernel<false, true>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((mx_gemm_rows_kernel<false, false>), grid, block, 0, s, p);
-  }
-  return hipGetLastError();
+  const auto kernel = p.out_f32 ? once ? mx_gemm_rows_kernel<true, true> : mx_gemm_rows_kernel<true, false>
+                                : once ? mx_gemm_rows_kernel<false, true> : mx_gemm_rows_kernel<false, false>;
+  return enqueue(kernel, grid, block, s, p);
 }
 
 // The kernels of different tiles and what they take, launch and all: a start, and us

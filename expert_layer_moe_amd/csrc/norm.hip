@@ -168,24 +168,15 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormRows p) {
   }
 }
 
-template <int P, bool XB, int RES>
-void launch(const NormRows& p, dim3 grid, dim3 block, hipStream_t s) {
-  if (p.codes) hipLaunchKernelGGL((norm_kernel<P, XB, RES, true>), grid, block, 0, s, p);
-  else hipLaunchKernelGGL((norm_kernel<P, XB, RES, false>), grid, block, 0, s, p);
-}
-
-template <int P>
-void launch_typed(const NormRows& p, dim3 grid, dim3 block, hipStream_t s) {
+using Kernel = void (*)(NormRows);
+template <int P, bool CODES>
+Kernel kernel_of(const NormRows& p) {
   const int res = p.res == nullptr ? 0 : p.res_bf16 ? 2 : 1;
-  if (p.x_bf16) {
-    if (res == 0) launch<P, true, 0>(p, grid, block, s);
-    else if (res == 1) launch<P, true, 1>(p, grid, block, s);
-    else launch<P, true, 2>(p, grid, block, s);
-  } else {
-    if (res == 0) launch<P, false, 0>(p, grid, block, s);
-    else if (res == 1) launch<P, false, 1>(p, grid, block, s);
-    else launch<P, false, 2>(p, grid, block, s);
-  }
+  if (p.x_bf16)
+    return res == 0 ? norm_kernel<P, true, 0, CODES>
+                    : res == 1 ? norm_kernel<P, true, 1, CODES> : norm_kernel<P, true, 2, CODES>;
+  return res == 0 ? norm_kernel<P, false, 0, CODES>
+                  : res == 1 ? norm_kernel<P, false, 1, CODES> : norm_kernel<P, false, 2, CODES>;
 }
 
 }  // namespace
@@ -196,9 +187,9 @@ hipError_t launch_norm(const NormRows& p, hipStream_t s) {
   const int pieces = (p.cols + kPer * kWave - 1) / (kPer * kWave);
   const int P = pieces <= 32 ? 2 : 4;
   const dim3 block(kWave * ((pieces + P - 1) / P)), grid((unsigned)std::min(p.rows, 1 << 20));
-  if (P == 2) launch_typed<2>(p, grid, block, s);
-  else launch_typed<4>(p, grid, block, s);
-  return hipGetLastError();
+  const Kernel kernel = P == 2 ? p.codes ? kernel_of<2, true>(p) : kernel_of<2, false>(p)
+                               : p.codes ? kernel_of<4, true>(p) : kernel_of<4, false>(p);
+  return enqueue(kernel, grid, block, s, p);
 }
 
 }  // namespace moe
