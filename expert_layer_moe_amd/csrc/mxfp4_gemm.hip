@@ -172,13 +172,14 @@ void mx_gemm_rows_kernel(MxGemm p) {
 // that a lane needs lie in one word: of the 16 codes of a row, g, 4 + g, 8 + g and
 // 12 + g; a lane's rows of its wave's tiles lie side by side.
 //
-// Bound by the matrix unit for large products: 8192 x 4096 x 7168 takes 112 us, 4.3
-// PFLOP/s, with the unit in use for 72 % of the time, at a clock that its own power
-// sets (1.67 GHz; 1.9 with codes that are all zero).  Smaller ones are bound by the
-// chain of a stage, a wait, a meeting and the reads behind it (0.2 to 0.5 us): 512 rows
-// 15.5 us, 256 rows 11.7.  Measured and not better: 32 x 32 x 64 MFMAs (the unit is 5 %
-// slower with them), waves of 8 x 8 tiles, stages of 128 or 512 values, operands read
-// two halves ahead, waves of a block that split K.
+// Large products are bound by the matrix unit's power: 8192 x 4096 x 7168 takes 113 to
+// 121 us from card to card, 4.3 to 4.0 PFLOP/s, and 93 with codes that are all zero (the
+// clock falls below 2 GHz).  Smaller ones are bound by the chain of a stage, a wait, a
+// meeting and the reads behind it (0.2 to 0.5 us): 512 rows 15.5 us, 256 rows 11.7.
+// Measured and not better: 32 x 32 x 64 MFMAs (the unit is 5 % slower with them), waves
+// of 8 x 8 tiles (2 % faster at K 7168, 7 to 11 % slower at 2048 and in 4096 rows),
+// stages of 128 or 512 values, operands read two halves ahead, columns of MFMAs taken
+// back and forth (no register is left for it: 12 % slower), waves of a block that split K.
 template <int TM, int TN, int WM, int WN, int S>
 struct Tile {
   static constexpr int W = WM * WN, BM = 16 * TM * WM, BN = 16 * TN * WN;

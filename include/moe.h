@@ -395,7 +395,8 @@ int moe_silu_mul_quant_mxfp4(const moe_quant_desc* desc, const void* gu, void* c
 
 /* The values that codes stand for: values [rows, cols] of type in_dtype with row
  * stride ld_in.  Exact; a value beyond fp32 or bf16 (from 2^128 on) becomes an
- * infinity, scale code 255 a block of NaN.  Errors as moe_quant_mxfp4. */
+ * infinity, scale code 255 a block of NaN.  values must not overlap codes and
+ * scales.  Errors as moe_quant_mxfp4. */
 int moe_dequant_mxfp4(const moe_quant_desc* desc, const void* codes, const void* scales,
                       void* values, moe_stream_t stream);
 

@@ -402,3 +402,50 @@ def test_product_with_scales_at_odd_addresses(M, N, K):
     odd = lambda t: torch.cat([t.new_full((t.shape[0], 1), 255), t], 1).cuda()[:, 1:]  # noqa: E731
     out = moe.moe_gemm_mxfp4(a.cuda(), odd(sa), b.cuda(), odd(sb), out_dtype=torch.float32)
     _check_product(out, a, sa, b, sb)
+
+
+def test_empty_matrices_are_refused():
+    e = lambda *shape: torch.empty(shape, dtype=torch.uint8, device="cuda")  # noqa: E731
+    f = lambda *shape: torch.empty(shape, device="cuda")  # noqa: E731
+    for call in (lambda: moe.moe_quant_mxfp4(f(0, 64)), lambda: moe.moe_quant_mxfp4(f(3, 0)),
+                 lambda: moe.moe_silu_mul_quant_mxfp4(f(0, 64)), lambda: moe.moe_dequant_mxfp4(e(0, 16), e(0, 1)),
+                 lambda: moe.moe_gemm_mxfp4(e(0, 16), e(0, 1), e(4, 16), e(4, 1)),
+                 lambda: moe.moe_gemm_mxfp4(e(4, 16), e(4, 1), e(0, 16), e(0, 1)),
+                 lambda: moe.moe_gemm_mxfp4(e(4, 0), e(4, 0), e(4, 0), e(4, 0)),
+                 lambda: moe.moe_add_rms_norm(f(0, 64), None, f(64)),
+                 lambda: moe.moe_add_rms_norm_quant_fp8(f(2, 0), None, f(0))):
+        with pytest.raises(moe.MoeError, match="INVALID_ARG"):
+            call()
+    # (and codes that are not 16-byte aligned)
+    with pytest.raises(moe.MoeError, match="INVALID_ARG"):
+        moe.moe_gemm_mxfp4(e(4, 32)[:, 8:24], e(4, 1), e(4, 16), e(4, 1))
+
+
+@pytest.mark.parametrize("M, N", [((1 << 26) + 40, 3), (5, (1 << 26) + 40)])
+def test_product_of_more_blocks_than_a_grid_is_wide(M, N):
+    """Rows that repeat every 1000: so do their results."""
+    a, sa, b, sb = [t.cuda() for t in _operands(8, min(M, 1000), min(N, 1000), 32)]
+    want = moe.moe_gemm_mxfp4(a, sa, b, sb)
+    # (torch's indexing fills 40 rows alone of 2^26 + 40)
+    wide = lambda t, n: t.repeat(-(-n // t.shape[0]), 1)[:n] if n > 1000 else t  # noqa: E731
+    args = wide(a, M), wide(sa, M), wide(b, N), wide(sb, N)
+    at = max(M, N) // 1000 * 1000 - 1000
+    assert torch.equal(args[0][at:at + 1000], a) if M > N else torch.equal(args[2][at:at + 1000], b)
+    out = moe.moe_gemm_mxfp4(*args)
+    for i in range(0, max(M, N) - 1000, 1000 * 1000):
+        part = out[i:i + 1000] if M > N else out[:, i:i + 1000]
+        assert torch.equal(part, want)
+    last = max(M, N) // 1000 * 1000
+    assert torch.equal(out[last:] if M > N else out[:, last:],
+                       want[:M - last] if M > N else want[:, :N - last])
+
+
+@pytest.mark.parametrize("M, N", [(2, 3), (100, 300)])
+def test_product_over_a_million_values(M, N):
+    K = 1 << 20
+    a, sa, b, sb = [t.cuda() for t in _operands(9, M, N, K)]
+    values = lambda codes, scales: moe.moe_dequant_mxfp4(codes, scales, out_dtype=torch.float32).double()  # noqa: E731
+    a64, b64 = values(a, sa), values(b, sb)
+    ref, mag = a64 @ b64.T, a64.abs() @ b64.abs().T
+    out = moe.moe_gemm_mxfp4(a, sa, b, sb, out_dtype=torch.float32)
+    assert ((out.double() - ref).abs() <= (-(-K // 128) + 9) * U * mag).all()
