@@ -425,32 +425,34 @@ hipError_t launch_rows(const MxGemm& p, hipStream_t s) {
   return enqueue(kernel, grid, block, s, p);
 }
 
-// The kernels of different tiles and what they take, launch and all: a start, and us
-// per stage (256 values of K) while each CU has at most one block, and with 256 blocks
-// of as many as a CU holds.  Fitted to 104 shapes, from 12 x 64 x 256 to 8192 x 4096 x
-// 7168: the choice by them is 0.9 % slower than the best kernel of each shape, 15 % at
-// most (1.4 % without 32 x 64).  The two of 128 x 128 differ by their waves, 4 and 8.
+// The kernels of different tiles and what they take in a captured graph: a start, and us
+// per stage (256 values of K) while each CU has at most one block, and with 256 blocks of
+// as many as a CU holds.  The rows kernel: a start, and in proportion to the blocks from
+// one a CU on a block's own time and its waves' steps, by token rows.  Fitted to 420 shapes, from
+// 1 x 64 x 128 to 8192 x 4096 x 7168 and 64 x 131072 x 7168: the choice by them is 1.1 %
+// slower than the best kernel of each shape on average, 7 % or more for one in 20, 26 % at
+// most (fitted to half of them: 1.9 % on the others).  The two of 128 x 128 differ by
+// their waves, 4 and 8 (1024 x 4096 x 7168 25.2 and 22.0); 16 x 32 takes 16 x 8192 x
+// 16384 in 17.6 (32 x 64 20.3, rows 21.4).
 struct Shape {
   int bm, bn, per_cu;
   float start, one, full;
 };
 constexpr Shape kTiles[] = {
-    {256, 256, 1, 10.4f, 1.25f, 1.9f}, {128, 256, 1, 7.9f, .78f, 1.1f}, {128, 128, 2, 7.3f, .51f, .70f},
-    {128, 128, 1, 5.8f, .50f, .81f},   {64, 128, 2, 6.7f, .345f, .49f}, {64, 64, 2, 4.8f, .24f, .30f},
-    {32, 64, 3, 5.0f, .19f, .21f},
+    {256, 256, 1, 5.7f, 1.73f, 2.53f}, {128, 256, 1, 7.4f, 1.24f, 1.50f}, {128, 128, 2, 5.5f, 1.36f, .76f},
+    {128, 128, 1, 5.9f, .58f, .91f},   {64, 128, 2, 5.3f, .433f, .686f},  {64, 64, 2, 4.03f, .306f, .452f},
+    {32, 64, 3, 3.95f, .274f, .314f},  {16, 32, 4, 2.88f, .177f, .194f},
 };
+constexpr float kRowsStart = 2.16f, kRowsBlock = .637f, kRowsStep = .442f, kRowsOf16 = .356f;
 
-// The kernel with the least expected time: an index of kTiles, or kRows.  The rows
-// kernel's waves split K: 0.72 us for each step of a wave, in proportion to the blocks
-// beyond one a CU.
+// The kernel with the least expected time: an index of kTiles, or kRows.
 constexpr int kRows = -1;
 int choose(int M, int N, int K) {
   const auto ceil_div = [](long long a, long long b) { return (a + b - 1) / b; };
-  const long long stages = ceil_div(ceil_div(K, 256), 2) * 2;   // (in twos)
+  const long long stages = ceil_div(K, 512) * 2;   // (in twos)
   int best = kRows;
-  float least = 3.4f + .72f * (float)ceil_div(ceil_div(K, 256), 8) *
-                           std::max(1.f, (float)(ceil_div(M, 16) * ceil_div(N, 16)) / 256.f);
-  if (M <= 16) return best;
+  float least = kRowsStart + std::max(1.f, (float)(ceil_div(M, 16) * ceil_div(N, 16)) / 256.f) *
+                                 (kRowsBlock + (kRowsStep + kRowsOf16 / 16 * (float)std::min(M, 16)) * (float)K / 2048.f);
   for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
     const Shape& k = kTiles[i];
     const long long blocks = ceil_div(M, k.bm) * ceil_div(N, k.bn);
@@ -472,7 +474,7 @@ int choose(int M, int N, int K) {
 const char* mx_gemm_kernel_name(int M, int N, int K) {
   static const char* const kNames[] = {"rows 16",        "tile 256 x 256", "tile 128 x 256",
                                        "tile 128 x 128", "tile 128 x 128 of 8 waves", "tile 64 x 128",
-                                       "tile 64 x 64",   "tile 32 x 64"};
+                                       "tile 64 x 64",   "tile 32 x 64",   "tile 16 x 32"};
   static_assert(sizeof(kNames) / sizeof(kNames[0]) == sizeof(kTiles) / sizeof(kTiles[0]) + 1, "names");
   return kNames[choose(M, N, K) - kRows];
 }
@@ -486,7 +488,8 @@ hipError_t launch_mx_gemm(const MxGemm& p, hipStream_t s) {
     case 3: return launch_tile<4, 2, 2, 4, 4>(p, s);
     case 4: return launch_tile<2, 4, 2, 2, 3>(p, s);
     case 5: return launch_tile<2, 2, 2, 2, 3>(p, s);
-    default: return launch_tile<2, 2, 1, 2, 3>(p, s);
+    case 6: return launch_tile<2, 2, 1, 2, 3>(p, s);
+    default: return launch_tile<1, 1, 1, 2, 4>(p, s);
   }
 }
 

@@ -430,7 +430,7 @@ int moe_gemm_mxfp4(const moe_mx_gemm_desc* desc, const void* a, const void* a_sc
                    const void* b, const void* b_scale, void* out, moe_stream_t stream);
 
 /* The kernel that moe_gemm_mxfp4 takes for a descriptor (host, pure): "rows 16"
- * (token rows of a block whose waves split K) or "tile 32 x 64" and larger (token
+ * (token rows of a block whose waves split K) or "tile 16 x 32" and larger (token
  * rows x weight rows).  NULL for one that it refuses. */
 const char* moe_gemm_mxfp4_kernel(const moe_mx_gemm_desc* desc);
 

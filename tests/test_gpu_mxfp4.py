@@ -300,14 +300,18 @@ def test_rows_behind_each_other_have_the_bits_of_a_smaller_call():
     # K ends inside a line of 256 values (of 1, 1, 3 and 7 blocks left), with odd and even
     # numbers of lines, up to several turns of the ring; rows and columns end inside a tile
     ("rows 16", 3, 200, 5152), ("rows 16", 37, 1001, 8160), ("rows 16", 17, 130, 16416),
-    ("tile 32 x 64", 17, 8200, 1312), ("tile 32 x 64", 20, 6000, 2080), ("tile 32 x 64", 37, 3000, 16416),
-    ("tile 64 x 64", 70, 3000, 864), ("tile 64 x 64", 65, 6000, 2080), ("tile 64 x 64", 130, 4090, 8224),
+    ("tile 16 x 32", 17, 8200, 1312), ("tile 16 x 32", 20, 6000, 2080), ("tile 16 x 32", 37, 3000, 16416),
+    ("tile 16 x 32", 70, 3000, 864), ("tile 16 x 32", 16, 13000, 4320),
+    ("tile 32 x 64", 100, 4090, 864), ("tile 32 x 64", 200, 2100, 2080), ("tile 32 x 64", 100, 4090, 16416),
+    ("tile 64 x 64", 520, 4090, 800), ("tile 64 x 64", 65, 6000, 2080), ("tile 64 x 64", 130, 4090, 8224),
     ("tile 64 x 128", 260, 6000, 2080), ("tile 64 x 128", 130, 8200, 4320), ("tile 64 x 128", 260, 4090, 16416),
-    ("tile 128 x 128", 2050, 4090, 288), ("tile 128 x 128", 700, 6000, 1504),
-    ("tile 128 x 128", 1300, 3000, 4128), ("tile 128 x 128 of 8 waves", 1000, 4090, 96),
-    ("tile 128 x 128 of 8 waves", 1300, 2050, 800), ("tile 128 x 128 of 8 waves", 200, 8200, 2272),
-    ("tile 128 x 256", 1300, 4090, 800), ("tile 128 x 256", 520, 8200, 1504), ("tile 128 x 256", 2050, 2050, 16416),
-    ("tile 256 x 256", 2050, 4090, 4128), ("tile 256 x 256", 1300, 6000, 8416),
+    ("tile 64 x 128", 700, 6000, 800),
+    ("tile 128 x 128", 1000, 8200, 288), ("tile 128 x 128", 2050, 4090, 800), ("tile 128 x 128", 2050, 2100, 1504),
+    ("tile 128 x 128", 2050, 4090, 8224),
+    ("tile 128 x 128 of 8 waves", 1000, 4090, 96), ("tile 128 x 128 of 8 waves", 1300, 2050, 800),
+    ("tile 128 x 128 of 8 waves", 520, 6000, 2272), ("tile 128 x 128 of 8 waves", 1000, 4090, 8416),
+    ("tile 128 x 256", 520, 13000, 2080), ("tile 128 x 256", 1000, 6000, 4320), ("tile 128 x 256", 330, 20000, 16416),
+    ("tile 256 x 256", 3900, 4090, 4128), ("tile 256 x 256", 8000, 8100, 2080), ("tile 256 x 256", 2000, 8190, 8416),
 ])
 def test_product_by_every_kernel_over_long_k(kernel, M, N, K):
     assert moe.moe_gemm_mxfp4_kernel(M, N, K) == kernel

@@ -56,7 +56,7 @@ def test_gemm_refuses_pointers(lib):
 
 def test_gemm_names_the_kernel_it_takes(lib):
     assert moe.moe_gemm_mxfp4_kernel(1, 4096, 7168) == "rows 16"
-    assert moe.moe_gemm_mxfp4_kernel(16, 100000, 7168) == "rows 16"
+    assert moe.moe_gemm_mxfp4_kernel(16, 8192, 16384) == "tile 16 x 32"
     assert moe.moe_gemm_mxfp4_kernel(8192, 4096, 7168) == "tile 256 x 256"
     for sizes in ((0, 8, 128), (4, 8, 120), (1 << 30, 1 << 9, 128)):
         with pytest.raises(moe.MoeError):
