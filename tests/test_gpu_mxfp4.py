@@ -453,3 +453,24 @@ def test_product_over_a_million_values(M, N):
     ref, mag = a64 @ b64.T, a64.abs() @ b64.abs().T
     out = moe.moe_gemm_mxfp4(a, sa, b, sb, out_dtype=torch.float32)
     assert ((out.double() - ref).abs() <= (-(-K // 128) + 9) * U * mag).all()
+
+
+def test_given_results_of_every_type():
+    """uint8 or the float8 types, the results of each other's bits."""
+    x = _rows(2, 9, 192, torch.bfloat16).cuda()
+    e8m0, e4m3 = torch.float8_e8m0fnu, torch.float8_e4m3fn
+    codes, scales = moe.moe_quant_mxfp4(x)
+    given = torch.empty(9, 6, dtype=torch.uint8, device="cuda").view(e8m0)
+    got = moe.moe_quant_mxfp4(x, scales=given)
+    assert got[1] is given and torch.equal(given.view(torch.uint8), scales) and torch.equal(got[0], codes)
+    out = moe.moe_gemm_mxfp4(codes, scales.view(e8m0), codes, scales)
+    assert torch.equal(out, moe.moe_gemm_mxfp4(codes, scales, codes, given))
+    silu, silu_s = moe.moe_silu_mul_quant_mxfp4(x[:, :128])
+    given = torch.empty(9, 2, dtype=torch.uint8, device="cuda").view(e8m0)
+    assert moe.moe_silu_mul_quant_mxfp4(x[:, :128], codes=silu.clone(), scales=given)[1] is given
+    assert torch.equal(given.view(torch.uint8), silu_s)
+    w = torch.ones(192, dtype=torch.bfloat16, device="cuda")
+    c8, s8, _ = moe.moe_add_rms_norm_quant_fp8(x, None, w)
+    given = torch.empty(9, 192, dtype=torch.uint8, device="cuda").view(e4m3)
+    got = moe.moe_add_rms_norm_quant_fp8(x, None, w, codes=given, scales=torch.empty_like(s8))
+    assert got[0] is given and torch.equal(given.view(torch.uint8), c8) and torch.equal(got[1], s8)
