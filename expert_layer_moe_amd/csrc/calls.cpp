@@ -1,9 +1,9 @@
 // The Python calls of the 4-bit operators and of the norm: checks of the tensors,
 // results, device, stream, and the library's entry point.  Compiled, because a small
-// call is bound by this: a product of one row took 7.6 us a call through ctypes, of
-// which 3.5 are the launch; it takes 4.5 here.  The entry points come from binding.py
-// (bind), so that there is one library in a process, and so do the parts of a call
-// that are not the ordinary ones: results on a stream that is not the current one,
+// call is bound by this: a product of one row takes 4.4 us a call in place of 7.6 through
+// ctypes, 3.2 of them the launch and 0.65 the result.  The entry points come from
+// binding.py (bind), so that there is one library in a process, and so do the parts of a
+// call that are not the ordinary ones: results on a stream that is not the current one,
 // and the exception for a status.
 #include <Python.h>
 
