@@ -9,6 +9,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <initializer_list>
 #include <utility>
 
 #include <ATen/core/Tensor.h>
@@ -137,14 +138,32 @@ struct Call {
     device_ = d;
   }
 
+  // Results of these bytes (0: given) in one allocation, up to 1 MB in all: an allocation
+  // costs 0.65 us of a call, a tensor in one that is there 0.2.  Larger ones apart, so that
+  // a result that is kept keeps no other one's memory.
+  void together(std::initializer_list<int64_t> bytes) {
+    int count = 0;
+    int64_t all = 0;
+    for (const int64_t n : bytes) count += n > 0, all += whole(n);
+    if (count > 1 && all <= (1 << 20) && stream_ == Py_None && !off_gpu_)
+      room_ = at::empty_strided({all}, {1}, on_gpu(at::kByte));
+  }
   // A result that is written on the call's stream (its memory is reused in that
   // stream's order).
-  at::Tensor empty(int64_t rows, int64_t cols, at::ScalarType dtype) const {
+  at::Tensor empty(int64_t rows, int64_t cols, at::ScalarType dtype) {
     all_on_gpu();
     const int64_t size[2] = {rows, cols}, stride[2] = {cols, 1};
+    if (room_.defined()) {
+      const auto type = c10::scalarTypeToTypeMeta(dtype);
+      at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(room_.storage()),
+                                                              room_.key_set(), type);
+      t.unsafeGetTensorImpl()->set_storage_offset(taken_ / (int64_t)type.itemsize());
+      t.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef(size, 2), at::IntArrayRef(stride, 2));
+      taken_ += whole(rows * cols * (int64_t)type.itemsize());
+      return t;
+    }
     if (stream_ == Py_None)
-      return at::empty_strided(at::IntArrayRef(size, 2), at::IntArrayRef(stride, 2),
-                               at::TensorOptions().dtype(dtype).device(at::kCUDA, (at::DeviceIndex)device_));
+      return at::empty_strided(at::IntArrayRef(size, 2), at::IntArrayRef(stride, 2), on_gpu(dtype));
     const Ref t(PyObject_CallFunction(empty_on, "(LL)OiO", (long long)rows, (long long)cols,
                                       reinterpret_cast<PyObject*>(torch::getTHPDtype(dtype)), device_, stream_));
     return tensor(t.p, "result");
@@ -187,10 +206,20 @@ struct Call {
   void all_on_gpu() const {
     if (off_gpu_) refuse("tensors must be on the GPU");
   }
+  at::TensorOptions on_gpu(at::ScalarType dtype) const {
+    return at::TensorOptions().dtype(dtype).device(at::kCUDA, (at::DeviceIndex)device_);
+  }
+  static int64_t whole(int64_t bytes) { return (bytes + 255) / 256 * 256; }
   PyObject* stream_;
   bool off_gpu_ = false;
   int device_ = -1;
+  at::Tensor room_;     // of `together`, of which the first bytes are taken
+  int64_t taken_ = 0;
 };
+// The bytes of a result that is not given.
+int64_t wanted(PyObject* given, int64_t rows, int64_t cols, int64_t size) {
+  return given == Py_None ? rows * cols * size : 0;
+}
 
 PyObject* pair(const at::Tensor& a, const at::Tensor& b) {
   const Ref x(THPVariable_Wrap(a)), y(THPVariable_Wrap(b));
@@ -219,6 +248,7 @@ PyObject* quant_mxfp4(PyObject* const* a) {
   Call c(a[3]);
   moe_quant_desc d{(int32_t)M, (int32_t)K};
   const at::Tensor& x = c.matrix(a[0], "input", Types::kFloats, M, n, &d.ld_in);
+  c.together({wanted(a[1], M, K / 2, 1), wanted(a[2], M, K / 32, 1)});
   const at::Tensor codes = c.result(a[1], "codes", Types::kBytes, M, K / 2, at::kByte, &d.ld_codes);
   const at::Tensor scales = c.result(a[2], "scales", Types::kMxScales, M, K / 32, at::kByte, &d.ld_scales);
   d.in_dtype = dtype_code(x.scalar_type());
@@ -275,7 +305,10 @@ struct Norm {
   moe_norm_desc d{};
   const at::Tensor *x, *res = nullptr, *w;
   at::Tensor kept;   // residual_out
-  Norm(PyObject* x_obj, PyObject* residual, PyObject* weight, PyObject* eps, PyObject* residual_out, PyObject* stream)
+  // others: the other results' bytes, of the rows and columns
+  template <typename F>
+  Norm(PyObject* x_obj, PyObject* residual, PyObject* weight, PyObject* eps, PyObject* residual_out, PyObject* stream,
+       F&& others)
       : c(stream) {
     const auto [M, H] = matrix_sizes(x_obj, "x", 1);
     d.rows = (int32_t)M;
@@ -290,12 +323,15 @@ struct Norm {
              Ref(type_and_shape(weight)).p, (long long)H);
     c.on_device(*w);
     d.w_dtype = dtype_code(w->scalar_type());
+    const std::pair<int64_t, int64_t> more = others(M, H);
     if (residual == Py_None) {
       if (residual_out != Py_None) refuse("residual_out without a residual");
+      c.together({more.first, more.second});
       return;
     }
     res = &c.matrix(residual, "residual", Types::kFloats, M, H, &d.ld_res);
     const auto type = res->scalar_type();
+    c.together({wanted(residual_out, M, H, type == at::kFloat ? 4 : 2), more.first, more.second});
     kept = c.result(residual_out, "residual_out", type == at::kFloat ? Types::kF32 : Types::kBf16, M, H, type,
                     &d.ld_res_out);
     d.res_dtype = dtype_code(type);
@@ -307,9 +343,11 @@ struct Norm {
 
 // (x, residual, weight, eps, out, residual_out, out_dtype, stream)
 PyObject* add_rms_norm(PyObject* const* a) {
-  Norm n(a[0], a[1], a[2], a[3], a[5], a[7]);
-  const at::Tensor out = n.c.result(a[4], "out", Types::kFloats, n.d.rows, n.d.cols,
-                                    a[4] == Py_None ? float_type(a[6]) : at::kFloat, &n.d.ld_out);
+  const at::ScalarType type = a[4] == Py_None ? float_type(a[6]) : at::kFloat;
+  Norm n(a[0], a[1], a[2], a[3], a[5], a[7], [&](int64_t M, int64_t H) {
+    return std::pair(wanted(a[4], M, H, type == at::kFloat ? 4 : 2), (int64_t)0);
+  });
+  const at::Tensor out = n.c.result(a[4], "out", Types::kFloats, n.d.rows, n.d.cols, type, &n.d.ld_out);
   n.d.out_dtype = dtype_code(out.scalar_type());
   n.c.enqueue([&](void* stream) {
     return entry.add_rms_norm(&n.d, n.x->const_data_ptr(), n.residual(), n.w->const_data_ptr(), n.residual_out(),
@@ -321,7 +359,9 @@ PyObject* add_rms_norm(PyObject* const* a) {
 
 // (x, residual, weight, eps, codes, scales, residual_out, out, stream)
 PyObject* add_rms_norm_quant_fp8(PyObject* const* a) {
-  Norm n(a[0], a[1], a[2], a[3], a[6], a[8]);
+  Norm n(a[0], a[1], a[2], a[3], a[6], a[8], [&](int64_t M, int64_t H) {
+    return std::pair(wanted(a[4], M, H, 1), wanted(a[5], M, (H + 127) / 128, 4));
+  });
   const int64_t M = n.d.rows, H = n.d.cols;
   const at::Tensor codes = n.c.result(a[4], "codes", Types::kCodes, M, H, at::kByte, &n.d.ld_codes);
   const at::Tensor scales = n.c.result(a[5], "scales", Types::kF32, M, (H + 127) / 128, at::kFloat, &n.d.ld_scales);

@@ -225,3 +225,33 @@ def test_each_operator_captured_and_replayed():
         torch.cuda.synchronize()
         for got, w in zip(outs, want):
             assert torch.equal(got, w)
+
+
+@pytest.mark.parametrize("inference", [False, True])
+@pytest.mark.parametrize("M", [3, 3000])
+def test_results_of_one_call_do_not_touch(M, inference):
+    """Small results of a call lie in one allocation: apart, aligned, and each a tensor of
+    its own to torch (in place, copied, resized, on the host); large ones in their own."""
+    import copy
+    with torch.inference_mode(inference):
+        x = torch.randn(M, 416, device="cuda").bfloat16()
+        w = torch.ones(416, device="cuda")
+        calls = [lambda: moe.moe_quant_mxfp4(x), lambda: moe.moe_silu_mul_quant_mxfp4(x[:, :384]),
+                 lambda: moe.moe_add_rms_norm(x, x, w, out_dtype=torch.float32),
+                 lambda: moe.moe_add_rms_norm_quant_fp8(x, x.float(), w),
+                 lambda: moe.moe_add_rms_norm_quant_fp8(x, None, w)[:2]]
+        for call in calls:
+            want = [t.cpu() for t in call()]
+            assert all(t.is_contiguous() and t.data_ptr() % 256 == 0 for t in call())
+            for i in range(len(want)):
+                got = call()
+                shared = len({t.untyped_storage().data_ptr() for t in got}) < len(got)
+                assert shared == (sum(-(-t.nbytes // 256) * 256 for t in got) <= 1 << 20)
+                got[i].zero_()
+                assert torch.equal(copy.deepcopy(got[i]).cpu(), torch.zeros_like(want[i]))
+                for j in range(len(want)):
+                    assert torch.equal(got[j].cpu(), torch.zeros_like(want[j]) if i == j else want[j])
+                got[i].resize_(M + 1000, 416)
+                got[i].fill_(1)
+                del got
+                assert all(torch.equal(t.cpu(), v) for t, v in zip(call(), want))
