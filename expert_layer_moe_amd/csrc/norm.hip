@@ -1,7 +1,8 @@
 // Root-mean-square norm of token rows, with the addition of the residual ahead of
 // it and, if asked for, e4m3fn codes of the result behind it:
 //   r = x + residual, rounded to the type it is stored in
-//   v = r / sqrt(mean(r^2) + eps) * weight, in fp32
+//   v = r / sqrt(mean(r^2) + eps) * weight, in fp32: mean, root, quotient and product
+//       rounded once each
 // out = v rounded once; codes and scales are those that quant.hip makes of v.  The
 // norm is that of the stored r, so that whoever reads r has the rows that v is of.
 //
@@ -10,6 +11,8 @@
 // slower, for rows above 16384 alone, which 16 waves of 2 pieces do not hold).
 // Bound by memory.  bf16 with a residual, 8192 x 7168 in us and TB/s: to bf16 82.0, 5.7;
 // to codes 74.5, 5.5; of 512 to 16384 columns 5.4 to 5.9.  One row 3.4, the launch.
+// fp32 with a residual 184.5, 5.1, to codes 148.5, 5.2; bf16 with an fp32 residual 129.5,
+// 5.4, to codes 121.5, 5.3.
 // Measured and not better: blocks that stay and load the next row ahead (79 to 92 us,
 // 77 to 83 to codes), fewer blocks a CU.
 #include "moe_common.h"
@@ -76,6 +79,21 @@ __device__ __forceinline__ float sum_of_wave(float v) {
   return (of(0) + of(16)) + (of(32) + of(48));
 }
 
+// x / root for the values of a row: one division a row, inv = 1 / root, and q + (x - q
+// root) inv with q = x inv, the quotient rounded once (Markstein; compared with the
+// division for 600 roots and all mantissas of x).  Without the remainder a value has one
+// rounding more, and some codes next to the middle of two become the other one.
+struct Root {
+  float root, inv, back;
+  __device__ __forceinline__ explicit Root(float mean)
+      // (an infinite root: no remainder, all finite values give 0)
+      : root(sqrtf(mean)), inv(1.f / root), back(root < INFINITY ? root : 0.f) {}
+  __device__ __forceinline__ float of(float x) const {
+    const float q = x * inv;
+    return fmaf(-fmaf(back, q, -x), inv, q);   // (so that -0 stays -0)
+  }
+};
+
 // RES: 0 no residual, 1 fp32, 2 bf16.  P pieces a lane.
 template <int P, bool XB, int RES, bool CODES>
 __global__ __launch_bounds__(1024) void norm_kernel(NormRows p) {
@@ -128,7 +146,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormRows p) {
     __syncthreads();
     sum = 0.f;
     for (int w = 0; w < waves; ++w) sum += part[turn][w];
-    const float inv = 1.f / sqrtf(sum / (float)p.cols + p.eps);
+    const Root root(sum / (float)p.cols + p.eps);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       const int c = col(i);
@@ -139,13 +157,13 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormRows p) {
           Piece<true> of;
           of.q[0] = w[i];
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) v[i][k] = v[i][k] * inv * of[k];
+          for (int k = 0; k < kPer; ++k) v[i][k] = root.of(v[i][k]) * of[k];
         } else {
           Piece<false> of;
           of.q[0] = w[i];
           of.q[1] = ld16(static_cast<const float*>(p.w) + c + 4);
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) v[i][k] = v[i][k] * inv * of[k];
+          for (int k = 0; k < kPer; ++k) v[i][k] = root.of(v[i][k]) * of[k];
         }
         if (!CODES || p.out != nullptr) {
           if (p.out_bf16) Piece<true>(v[i]).store(p.out, (size_t)row * p.ld_out + c);

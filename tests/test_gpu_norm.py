@@ -212,3 +212,34 @@ def test_rows_far_apart():
     moe.moe_add_rms_norm_quant_fp8(vx, vr, w, codes=vc, scales=vs, residual_out=vk, out=vo)
     for got, wanted in zip((vc, vs, vk, vo), (*want, want_out)):
         assert torch.equal(got, wanted)
+
+
+@pytest.mark.parametrize("M, H", [(1, 16), (40, 528), (30, 2064), (9, 7168), (3, 20000)])
+@pytest.mark.parametrize("types", [(F, None, F, F), (F, F, F, F), (B, B, B, F), (B, F, B, F)],
+                         ids=lambda t: "-".join(str(v).replace("torch.", "") for v in t))
+def test_a_row_is_the_quotient_by_one_root_times_the_weights(M, H, types):
+    """out = (r / root) * weight, each of the two rounded once: bit by bit, of one fp32 root a
+    row.  The root lies 28 u (the sum's 55 in half) and 1.5 u (mean, eps and root: two halves
+    and one) off at most, and a step is u or 2 u of the value: among 30 steps to either side."""
+    xt, rt, wt, ot = types
+    x, res, w = _inputs(M + H + 1, M, H, xt, rt, wt)
+    r, _ = _norm64(x, res, w, 1e-6)
+    r, w32 = r.float(), w.float()
+    root = torch.sqrt(r.double().square().mean(1, keepdim=True) + 1e-6).float()
+    out, _ = moe.moe_add_rms_norm(*[None if t is None else t.cuda() for t in (x, res, w)], eps=1e-6, out_dtype=ot)
+    out = out.cpu()
+    found = torch.zeros(M, dtype=torch.bool)
+    for step in range(-30, 31):
+        at = (root.view(torch.int32) + step).view(torch.float32)
+        found |= (r / at * w32 == out).all(1)
+    assert found.all(), int((~found).sum())
+
+
+@pytest.mark.parametrize("dtype", [B, F])
+def test_zeros_of_a_row_keep_their_signs(dtype):
+    x, _, w = _inputs(9, 5, 144, dtype, None, dtype)
+    w = w.abs()
+    x[:, ::3], x[:, 1::3] = 0.0, -0.0
+    out, _ = moe.moe_add_rms_norm(x.cuda(), None, w.cuda(), out_dtype=dtype)
+    assert (out[:, ::3] == 0).all() and (out[:, 1::3] == 0).all()
+    assert torch.equal(torch.signbit(out).cpu(), torch.signbit(x))
