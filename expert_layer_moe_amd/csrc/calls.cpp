@@ -106,6 +106,34 @@ at::ScalarType float_type(PyObject* dtype) {
   refuse("out_dtype %S: float32 or bfloat16 expected", dtype);
 }
 
+// The storage of one result among several in one allocation, the room: it begins where the
+// room does and ends with the result, so that a result that grows gets memory of its own, as
+// any tensor does, and leaves the ones behind it.  The room lives as long as one of its
+// storages.  The pointer frees nothing and carries the allocator's deleter, by which
+// record_stream knows the allocator's own blocks.
+struct Share final : c10::StorageImpl {
+  Share(const c10::Storage& room, int64_t end)
+      : StorageImpl(use_byte_size_t(), (size_t)end,
+                    at::DataPtr(room.mutable_data(), nullptr, room.data_ptr().get_deleter(), room.device()),
+                    room.allocator(), /*resizable=*/true),
+        room_(room) {}
+  ~Share() override { let_go(); }
+  void release_resources() override {
+    let_go();
+    StorageImpl::release_resources();
+  }
+
+ private:
+  void let_go() {
+    // Handed to another process (torch has put its own count of readers in the pointer's
+    // place, which does not know of the room): the other side may read it still, so it stays.
+    if (room_ && data_ptr().get() == room_.data() && data_ptr().get_deleter() != room_.data_ptr().get_deleter())
+      (void)c10::Storage(room_).unsafeReleaseStorageImpl();
+    room_ = c10::Storage();
+  }
+  c10::Storage room_;
+};
+
 // What all tensors of a call share.
 struct Call {
   explicit Call(PyObject* stream) : stream_(stream) {}
@@ -139,7 +167,7 @@ struct Call {
   }
 
   // Results of these bytes (0: given) in one allocation, up to 1 MB in all: an allocation
-  // costs 0.65 us of a call, a tensor in one that is there 0.2.  Larger ones apart, so that
+  // costs 0.65 us of a call, a tensor in one that is there 0.25.  Larger ones apart, so that
   // a result that is kept keeps no other one's memory.
   void together(std::initializer_list<int64_t> bytes) {
     int count = 0;
@@ -155,11 +183,12 @@ struct Call {
     const int64_t size[2] = {rows, cols}, stride[2] = {cols, 1};
     if (room_.defined()) {
       const auto type = c10::scalarTypeToTypeMeta(dtype);
-      at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(room_.storage()),
-                                                              room_.key_set(), type);
+      const int64_t bytes = rows * cols * (int64_t)type.itemsize();
+      at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+          c10::Storage(c10::make_intrusive<Share>(room_.storage(), taken_ + bytes)), room_.key_set(), type);
       t.unsafeGetTensorImpl()->set_storage_offset(taken_ / (int64_t)type.itemsize());
       t.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef(size, 2), at::IntArrayRef(stride, 2));
-      taken_ += whole(rows * cols * (int64_t)type.itemsize());
+      taken_ += whole(bytes);
       return t;
     }
     if (stream_ == Py_None)

@@ -255,3 +255,86 @@ def test_results_of_one_call_do_not_touch(M, inference):
                 got[i].fill_(1)
                 del got
                 assert all(torch.equal(t.cpu(), v) for t, v in zip(call(), want))
+
+
+@pytest.mark.parametrize("inference", [False, True])
+@pytest.mark.parametrize("more", [1, 5, 1000])
+def test_a_result_that_grows_leaves_the_others(more, inference):
+    """Each result of a call resized to more rows and written, others of the call looked at
+    behind that, and the call's memory used anew."""
+    with torch.inference_mode(inference):
+        x = torch.randn(3, 416, device="cuda").bfloat16()
+        w = torch.ones(416, device="cuda")
+        calls = [lambda: moe.moe_quant_mxfp4(x), lambda: moe.moe_silu_mul_quant_mxfp4(x[:, :384]),
+                 lambda: moe.moe_add_rms_norm(x, x, w, out_dtype=torch.float32),
+                 lambda: moe.moe_add_rms_norm_quant_fp8(x, x.float(), w),
+                 lambda: moe.moe_add_rms_norm_quant_fp8(x, None, w)[:2]]
+        for call in calls:
+            want = [t.cpu() for t in call()]
+            for i in range(len(want)):
+                got = call()
+                got[i].resize_(3 + more, want[i].shape[1])
+                assert torch.equal(got[i][:3].cpu(), want[i])
+                got[i].fill_(1)
+                for j in range(len(want)):
+                    assert i == j or torch.equal(got[j].cpu(), want[j])
+                # (what the grown one lay in is not free while others lie beside it)
+                later = [call() for _ in range(4)]
+                for j in range(len(want)):
+                    assert torch.equal(got[j].cpu(), torch.ones(got[j].shape, dtype=got[j].dtype) if i == j else want[j])
+                    assert all(torch.equal(t[j].cpu(), want[j]) for t in later)
+
+
+def test_a_result_whose_memory_is_given_back_leaves_the_others():
+    x = torch.randn(3, 416, device="cuda").bfloat16()
+    want = [t.cpu() for t in moe.moe_quant_mxfp4(x)]
+    for i in range(2):
+        got = moe.moe_quant_mxfp4(x)
+        got[i].untyped_storage().resize_(0)
+        assert torch.equal(got[1 - i].cpu(), want[1 - i])
+
+
+@pytest.mark.parametrize("i", [0, 1, 2])
+def test_results_in_use_on_another_stream_keep_their_memory(i):
+    """record_stream of one result of a call: the memory of all is not given out again while
+    that stream has work, and is afterwards."""
+    x = torch.randn(3, 416, device="cuda").bfloat16()
+    w = torch.ones(416, device="cuda")
+    call = lambda: moe.moe_add_rms_norm_quant_fp8(x, x.float(), w)  # noqa: E731
+    call()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = call()
+    place = {t.untyped_storage().data_ptr() for t in got}
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    got[i].record_stream(side)
+    del got
+    during = [call() for _ in range(3)]
+    assert not side.query(), "the side stream was done too early to tell"
+    assert not place & {t.untyped_storage().data_ptr() for r in during for t in r}
+    side.synchronize()
+    del during
+    torch.cuda.empty_cache()
+
+
+def test_results_handed_to_another_process_keep_their_memory():
+    """torch counts the readers of a storage that it shares; as long as there may be some, its
+    memory is not given out again, though the tensors here are gone."""
+    x = torch.randn(3, 416, device="cuda").bfloat16()
+    for i in range(2):
+        got = moe.moe_quant_mxfp4(x)
+        place = got[0].untyped_storage().data_ptr()
+        got[i].untyped_storage()._share_cuda_()
+        del got
+        later = [moe.moe_quant_mxfp4(x) for _ in range(4)]
+        assert place not in {t.untyped_storage().data_ptr() for r in later for t in r}
+
+
+def test_the_storage_of_a_result_ends_with_it():
+    """So that what torch does to a storage as a whole (copies, files) does not reach behind."""
+    x = torch.randn(5, 416, device="cuda").bfloat16()
+    w = torch.ones(416, device="cuda")
+    for got in (moe.moe_quant_mxfp4(x), moe.moe_add_rms_norm(x, x, w), moe.moe_add_rms_norm_quant_fp8(x, x, w)):
+        for t in got:
+            assert t.untyped_storage().nbytes() == t.storage_offset() * t.element_size() + t.nbytes
