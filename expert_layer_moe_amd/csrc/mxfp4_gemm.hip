@@ -2,10 +2,11 @@
 //   out[m][n] = sum over blocks b of 2^(sa[m][b] + sb[n][b] - 254)
 //               (sum over k in b of a[m][k] b[n][k])
 // One MFMA (16 x 16 x 128) takes four blocks of either operand with their scale
-// codes, and adds their sum to the accumulator: on this matrix unit products and
-// sums of e2m1 codes under their scales are exact, but for one rounding to fp32 of
-// accumulator and sum together (measured, with scales up to 2^60 apart), so fp32
-// results need nothing else than bf16 ones.  A scale code of 255 gives NaN.
+// codes, and adds their sum to the accumulator.  Measured on this matrix unit: a block's
+// 32 products are summed exactly; two blocks at a time are brought to the largest one's
+// scale and added, rounded to fp32, which drops nothing while the scales of the four lie
+// within 2^14, and else up to 2^-21 of the largest one.  So fp32 results need nothing
+// else than bf16 ones.  A scale code of 255 gives NaN.
 //
 // The weights are the MFMA's A operand and the token rows its B operand: a lane's
 // four sums are four columns of one token.  Lane (r, g) = (l % 16, l / 16) holds 32

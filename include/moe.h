@@ -420,10 +420,13 @@ typedef struct moe_mx_gemm_desc {
  *   a_scale  [M, K / 32] e8m0
  *   b        [N, K / 2] (weights), b_scale [N, K / 32] e8m0
  *   out      [M, N] out_dtype (must not alias an input)
- * Products and their sums over four blocks at a time are exact, the sums of those
- * fp32; rounded once to out_dtype.  Products below 2^-149 may be lost.  A scale
- * code 255 gives NaN in its row or column.  The bits of a row do not depend on
- * the other rows' values.  Nothing of out outside its M x N values is written.
+ * Sums are fp32, over four blocks of a row at a time (from block 0, 4, 8, ... on) and
+ * of those; rounded once to out_dtype.  As far as the scales of four blocks' products
+ * lie within 2^14 of each other, their sum is exact and rounded once.  Where they lie
+ * further apart, bits below 2^-20 of the largest of the four scales may be lost
+ * besides.  Partial sums beyond fp32 become infinities, products below 2^-149 may be
+ * lost.  A scale code 255 gives NaN in its row or column.  The bits of a row do not
+ * depend on the other rows' values.  Nothing of out outside its M x N values is written.
  * a and b are 16-byte aligned, the scales need no alignment.  Errors as
  * moe_gemm_fp8 (MOE_ERR_UNSUPPORTED for K not a multiple of 32). */
 int moe_gemm_mxfp4(const moe_mx_gemm_desc* desc, const void* a, const void* a_scale,
