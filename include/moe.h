@@ -422,9 +422,9 @@ typedef struct moe_mx_gemm_desc {
  *   out      [M, N] out_dtype (must not alias an input)
  * Sums are fp32, over four blocks of a row at a time (from block 0, 4, 8, ... on) and
  * of those; rounded once to out_dtype.  As far as the scales of four blocks' products
- * lie within 2^14 of each other, their sum is exact and rounded once.  Where they lie
- * further apart, bits below 2^-20 of the largest of the four scales may be lost
- * besides.  Partial sums beyond fp32 become infinities, products below 2^-149 may be
+ * lie within 2^12 of each other, their sum is exact and rounded once.  Where they lie
+ * further apart, small blocks lose bits beside large ones, up to 2^-21 of the sum of
+ * the four's |a b|.  Partial sums beyond fp32 become infinities, products below 2^-149 may be
  * lost.  A scale code 255 gives NaN in its row or column.  The bits of a row do not
  * depend on the other rows' values.  Nothing of out outside its M x N values is written.
  * a and b are 16-byte aligned, the scales need no alignment.  Errors as
