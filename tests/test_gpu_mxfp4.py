@@ -528,3 +528,49 @@ def test_products_of_far_scales(kernel, M, N, K, spread):
     out = moe.moe_gemm_mxfp4(a, sa, b, sb, out_dtype=torch.float32)
     off = (out.double() - ref).abs()
     assert (off <= tol).all(), float((off / tol).max())
+
+
+def _gates():
+    """Every bf16 value from 2^-20 to 85 in size, of either sign, and as many again of fp32."""
+    g = torch.Generator().manual_seed(12)
+    every = torch.arange(65536, dtype=torch.int32).to(torch.uint16).view(torch.bfloat16).float()
+    every = every[(every.abs() >= 2.0 ** -20) & (every.abs() <= 85)]
+    size = torch.exp2(26.4 * torch.rand(1 << 17, generator=g) - 20)
+    return torch.cat([every, size * (1 - 2 * torch.randint(0, 2, size.shape, generator=g))])
+
+
+def test_silu_to_the_last_bit():
+    """SiLU as the formula has it, g / (1 + exp(-g)), each rounded: ups that take it to middles
+    between codes, so that one step of its last bit shows.  A gate's block: a value of 7, so
+    that the scale is 1, and four middles at seven neighbouring ups."""
+    g = _gates()
+    dev = g.cuda()
+    silu = (dev / (1 + torch.exp(-dev))).cpu()
+    # (the 8-bit operator divides: its scale is the block's largest over 448)
+    rows = torch.zeros(g.numel(), 256)
+    rows[:, 0], rows[:, 128] = g, 1.0
+    _, scale = moe.moe_silu_mul_quant_fp8(rows.cuda())
+    assert torch.equal(scale.cpu()[:, 0], silu.abs().clamp(min=1e-12) / torch.full_like(silu, 448.0))
+
+    gu = torch.zeros(g.numel(), 64)
+    gu[:, :32], gu[:, 32:] = g[:, None], 0.0
+    gu[:, 0], gu[:, 32] = 100.0, 0.07
+    at = 33
+    for middle in (0.25, 0.75, 1.25, 1.75):
+        up = (middle / silu.double()).float()
+        for step in range(-3, 4):
+            gu[:, at] = (up.view(torch.int32) + step).view(torch.float32)
+            at += 1
+
+    def codes_of(s):
+        v = s[:, None] * gu[:, 32:]
+        v[:, 0] = torch.tensor(100.0) * gu[0, 32]
+        return _quant64(v.double())
+    want, want_s = codes_of(silu)
+    assert (want_s == 127).all()
+    for step in (-1, 1):   # a last bit off shows in nearly every block
+        off, _ = codes_of((silu.view(torch.int32) + step).view(torch.float32))
+        assert (off != want).any(1).double().mean() > 0.9
+    codes, scales = moe.moe_silu_mul_quant_mxfp4(gu.cuda())
+    assert torch.equal(scales.cpu(), want_s)
+    assert torch.equal(codes.cpu(), _pack(want))
