@@ -15,7 +15,9 @@ typedef __attribute__((__vector_size__(4 * sizeof(int)))) int i32x4;
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* p, int bytes = -1) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);
 }
-// An offset behind the end of every buffer of less than 2 GB: loads give 0.
+// An offset behind the end of every buffer of at most 2^31 bytes (256 rows, 2^23 apart):
+// loads give 0, also with the distance to a tile's later rows added, which stays below
+// 2^31 as the rows do.
 constexpr uint32_t kNowhere = 0x80000000u;
 __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t src, uint32_t lane_offset, uint32_t offset) {
   return __builtin_bit_cast(u32x4,

@@ -574,3 +574,42 @@ def test_silu_to_the_last_bit():
     codes, scales = moe.moe_silu_mul_quant_mxfp4(gu.cuda())
     assert torch.equal(scales.cpu(), want_s)
     assert torch.equal(codes.cpu(), _pack(want))
+
+
+TILES = [("tile 16 x 32", 260, 520, 544), ("tile 32 x 64", 520, 520, 2080), ("tile 64 x 64", 520, 1000, 544),
+         ("tile 64 x 128", 1300, 1000, 2080), ("tile 128 x 128 of 8 waves", 1000, 2050, 1056),
+         ("tile 128 x 128", 2000, 2050, 544), ("tile 128 x 256", 2000, 2050, 4128),
+         ("tile 256 x 256", 3900, 3000, 544)]
+
+
+def _check_on_gpu(out, a, sa, b, sb):
+    K = 2 * a.shape[1]
+    a64, b64 = [moe.moe_dequant_mxfp4(c.contiguous(), s.contiguous(), out_dtype=torch.float32).double()
+                for c, s in ((a, sa), (b, sb))]
+    ref, mag = a64 @ b64.T, a64.abs() @ b64.abs().T
+    assert ((out.double() - ref).abs() <= (-(-K // 128) + 9) * U * mag).all()
+
+
+@pytest.mark.parametrize("kernel, M, N, K", TILES)
+def test_every_tile_of_the_widest_rows(kernel, M, N, K):
+    """Code rows 2^23 bytes apart, the most there may be, with other codes between them: a
+    tile of 256 rows spans 2^31 bytes.  The last tiles are not full."""
+    assert moe.moe_gemm_mxfp4_kernel(M, N, K) == kernel
+    a, sa, b, sb = [t.cuda() for t in _operands(M + N, M, N, K)]
+
+    def wide(t):
+        big = torch.full((t.shape[0], 1 << 23), 0x77, dtype=torch.uint8, device="cuda")
+        big[:, :t.shape[1]].copy_(t)
+        return big[:, :t.shape[1]]
+    out = moe.moe_gemm_mxfp4(wide(a), sa, wide(b), sb, out_dtype=torch.float32)
+    _check_on_gpu(out, a, sa, b, sb)
+
+
+@pytest.mark.parametrize("kernel, M, N, K", TILES)
+def test_every_tile_with_scales_at_odd_addresses(kernel, M, N, K):
+    assert moe.moe_gemm_mxfp4_kernel(M, N, K) == kernel
+    a, sa, b, sb = [t.cuda() for t in _operands(M + N + 1, M, N, K)]
+    odd = lambda t, by: torch.cat([t.new_full((t.shape[0], by), 255), t], 1)[:, by:]  # noqa: E731
+    wide = lambda t: torch.cat([t, t.new_full((t.shape[0], 48), 0x77)], 1)[:, :t.shape[1]]  # noqa: E731
+    out = moe.moe_gemm_mxfp4(wide(a), odd(sa, 1), wide(b), odd(sb, 3 - sb.shape[1] % 2), out_dtype=torch.float32)
+    _check_on_gpu(out, a, sa, b, sb)
