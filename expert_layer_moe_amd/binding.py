@@ -4,8 +4,8 @@ Every step of the layer runs in the library's HIP kernels; this module only
 checks tensor shapes / dtypes / devices and passes raw device pointers and the
 current HIP stream.  PyTorch provides device memory and streams.  The calls of
 the 4-bit operators and the norm do the same in compiled code (csrc/calls.cpp).
-There is no fallback: if the library or the compiled calls are missing, loading
-raises.
+There is no fallback: if the library is missing, loading raises; if the compiled
+calls for this interpreter and torch are, the first such call does.
 """
 from __future__ import annotations
 
@@ -17,9 +17,11 @@ from typing import Optional
 
 import torch
 
+from .build import calls_path
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "lib", "libmoe_amd.so")
-CALLS_PATH = os.path.join(_HERE, "lib", "_moe_calls.so")
+CALLS_PATH = calls_path()
 
 MOE_F32, MOE_BF16, MOE_FP8_E4M3 = 0, 1, 2
 MOE_LAYOUT_ROW_MAJOR, MOE_LAYOUT_FRAG16 = 0, 1
@@ -159,7 +161,8 @@ def _load_calls():
     global _calls
     lib = load_library()
     if not os.path.exists(CALLS_PATH):
-        raise RuntimeError(f"{CALLS_PATH} is missing: build it with __graft_entry__.build()")
+        raise RuntimeError(f"{CALLS_PATH} is missing: build it with __graft_entry__.build(), with this "
+                           "interpreter and torch")
     loader = importlib.machinery.ExtensionFileLoader("_moe_calls", CALLS_PATH)
     calls = importlib.util.module_from_spec(
         importlib.util.spec_from_file_location("_moe_calls", CALLS_PATH, loader=loader))

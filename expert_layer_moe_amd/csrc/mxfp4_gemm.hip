@@ -323,7 +323,7 @@ struct Tile {
 };
 
 template <int TM, int TN, int WM, int WN, int S, bool F32>
-__global__ __launch_bounds__(WM * WN * kWave) __attribute__((amdgpu_waves_per_eu(TM * TN >= 64 ? 1 : 2)))
+__global__ __launch_bounds__(WM * WN * kWave) __attribute__((amdgpu_waves_per_eu(2)))
 void mx_gemm_tile_kernel(MxGemm p, int tiles_m, int tiles_n) {
   using T = Tile<TM, TN, WM, WN, S>;
   constexpr int W = T::W, BM = T::BM, BN = T::BN;
