@@ -212,13 +212,16 @@ class DenseFP4:
 
     w13 [2I, H/2] (gate rows, then up rows) and w2 [H, I/2]: uint8, the first of
     two codes in the low half; scale codes s13 [2I, H/32], s2 [H, I/32], uint8 or
-    float8_e8m0fnu.  H and I multiples of 32.  gate_up: as DenseFP8's.
+    float8_e8m0fnu.  H and I multiples of 32.  gate_up: as DenseFP8's; normed: the
+    type of forward_normed's rows between the norm and their codes (fp32: one
+    rounding less, twice the bytes).
     """
 
-    def __init__(self, w13, w2, s13, s2, device="cuda", gate_up=torch.bfloat16):
-        if gate_up not in _ACT:
-            raise ValueError(f"gate_up {gate_up}: torch.float32 or torch.bfloat16 expected")
-        self.gate_up = gate_up
+    def __init__(self, w13, w2, s13, s2, device="cuda", gate_up=torch.bfloat16, normed=torch.bfloat16):
+        for name, dtype in (("gate_up", gate_up), ("normed", normed)):
+            if dtype not in _ACT:
+                raise ValueError(f"{name} {dtype}: torch.float32 or torch.bfloat16 expected")
+        self.gate_up, self.normed = gate_up, normed
         self.w13 = w13.to(device).contiguous()
         self.w2 = w2.to(device).contiguous()
         for name, t in (("w13", w13), ("w2", w2), ("s13", s13), ("s2", s2)):
@@ -236,11 +239,11 @@ class DenseFP4:
             raise ValueError("s13 is [2I, H/32], s2 [H, I/32]")
 
     @classmethod
-    def quantised(cls, w13, w2, device="cuda", gate_up=torch.bfloat16):
+    def quantised(cls, w13, w2, device="cuda", gate_up=torch.bfloat16, normed=torch.bfloat16):
         """Of weights w13 [2I, H], w2 [H, I] in bf16 or fp32 (moe_quant_mxfp4)."""
         c13, s13 = moe_quant_mxfp4(w13.to(device))
         c2, s2 = moe_quant_mxfp4(w2.to(device))
-        return cls(c13, c2, s13, s2, device, gate_up)
+        return cls(c13, c2, s13, s2, device, gate_up, normed)
 
     def forward(self, x, out=None, stream=None):
         """x [T, H] bf16 or fp32 -> out [T, H], bf16 unless `out` is fp32."""
@@ -251,8 +254,8 @@ class DenseFP4:
 
     def forward_normed(self, x, residual, weight, eps=1e-6, out=None, residual_out=None,
                        stream=None):
-        """forward of moe_add_rms_norm's rows (in bf16).  Returns (out,
+        """forward of moe_add_rms_norm's rows (in the type `normed`).  Returns (out,
         residual_out); without a residual (None) the latter is None."""
-        normed, kept = moe_add_rms_norm(x, residual, weight, eps, residual_out=residual_out,
-                                        stream=stream)
-        return self.forward(normed, out, stream), kept
+        rows, kept = moe_add_rms_norm(x, residual, weight, eps, residual_out=residual_out,
+                                      out_dtype=self.normed, stream=stream)
+        return self.forward(rows, out, stream), kept

@@ -338,3 +338,22 @@ def test_the_storage_of_a_result_ends_with_it():
     for got in (moe.moe_quant_mxfp4(x), moe.moe_add_rms_norm(x, x, w), moe.moe_add_rms_norm_quant_fp8(x, x, w)):
         for t in got:
             assert t.untyped_storage().nbytes() == t.storage_offset() * t.element_size() + t.nbytes
+
+
+@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("rows", [torch.bfloat16, torch.float32])
+def test_dense_fp4_takes_its_codes_of_the_norm_in_either_type(T, rows):
+    """normed=fp32: no rounding to bf16 between the norm and the codes, whose scales and codes
+    it changes."""
+    H, I = 1056, 96
+    w13, w2, g = _weights(T, H, I)
+    dense = moe.DenseFP4.quantised(w13.bfloat16(), w2, normed=torch.float32)
+    half = moe.DenseFP4.quantised(w13.bfloat16(), w2)
+    norm = (1 + 0.1 * torch.randn(H, generator=g)).to(rows).cuda()
+    x, res = torch.randn(T, H, generator=g).to(rows).cuda(), torch.randn(T, H, generator=g).to(rows).cuda()
+    normed, kept = moe.moe_add_rms_norm(x, res, norm, out_dtype=torch.float32)
+    into = lambda: torch.empty(T, H, device="cuda")  # noqa: E731
+    out, r = dense.forward_normed(x, res, norm, out=into())
+    assert torch.equal(out, dense.forward(normed, out=into())) and torch.equal(r, kept)
+    rounded, _ = half.forward_normed(x, res, norm, out=into())
+    assert torch.equal(rounded, dense.forward(normed.bfloat16(), out=into())) and not torch.equal(rounded, out)

@@ -256,3 +256,12 @@ def test_dense_layer_refuses_shapes_and_types():
         layer.forward(torch.zeros(2, 64))
     with pytest.raises(ValueError, match="on the GPU"):
         layer.forward_normed(torch.zeros(2, 64), None, torch.ones(64))
+
+
+def test_dense_layer_refuses_the_type_of_its_normed_rows():
+    w13, w2, s13, s2 = _codes(128, 32), _codes(64, 32), _codes(128, 2), _codes(64, 2)
+    assert moe.DenseFP4(w13, w2, s13, s2, device="cpu").normed == BF
+    layer = moe.DenseFP4(w13, w2, s13, s2, device="cpu", normed=F32)
+    assert pickle.loads(pickle.dumps(layer)).normed == F32
+    with pytest.raises(ValueError, match="normed"):
+        moe.DenseFP4(w13, w2, s13, s2, device="cpu", normed=torch.float16)
