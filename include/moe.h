@@ -466,7 +466,10 @@ typedef struct moe_norm_desc {
  * Other outputs must not overlap inputs or each other.  The squares are summed in
  * fp32: a row whose sum passes its range (values around 2^60) gives zeros, as one
  * with an infinity does in its finite places (NaN in that one); a row with a NaN
- * gives NaN.  Bits of a row do not depend on other rows.  MOE_ERR_INVALID_ARG: null
+ * gives NaN.  Squares below 2^-126 lose bits and below 2^-149 are lost, which eps
+ * covers: with eps = 0 the mean needs values of 2^-60 or more in a row (NaN or
+ * infinities in one of much smaller ones or of zeros).  Bits of a row do not depend on
+ * other rows.  MOE_ERR_INVALID_ARG: null
  * or misaligned pointers (16 bytes), sizes below 1, strides below the row length,
  * eps below 0 or not finite, other types; MOE_ERR_UNSUPPORTED: cols above 32768
  * or off its multiple, strides off theirs. */

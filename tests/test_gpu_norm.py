@@ -243,3 +243,17 @@ def test_zeros_of_a_row_keep_their_signs(dtype):
     out, _ = moe.moe_add_rms_norm(x.cuda(), None, w.cuda(), out_dtype=dtype)
     assert (out[:, ::3] == 0).all() and (out[:, 1::3] == 0).all()
     assert torch.equal(torch.signbit(out).cpu(), torch.signbit(x))
+
+
+def test_rows_of_small_values_without_eps():
+    """From 2^-60 on, beside zeros and values whose squares are lost; the same row times a power
+    of two has the same result."""
+    x, _, w = _inputs(11, 6, 528, F, None, F)
+    x = torch.randn(6, 528, generator=torch.Generator().manual_seed(12)).clamp(-4, 4)
+    x[:, ::5] *= 2.0 ** -30
+    x[:, 1::5] = 0.0
+    x[:, 2::5] = 1 + x[:, 2::5].abs()
+    _, want = _norm64(x, None, w, 0.0)
+    for scale in (1.0, 2.0 ** -60, 2.0 ** 55):
+        out, _ = moe.moe_add_rms_norm((x * scale).cuda(), None, w.cuda(), eps=0.0, out_dtype=F)
+        _check_out(out, want)
