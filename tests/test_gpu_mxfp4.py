@@ -531,12 +531,14 @@ def test_products_of_far_scales(kernel, M, N, K, spread):
 
 
 def _gates():
-    """Every bf16 value from 2^-20 to 85 in size, of either sign, and as many again of fp32."""
+    """Every bf16 value from 2^-20 to 85 in size, of either sign, fp32 ones among them, and those
+    from -85 to where the exponential ends, -88.7."""
     g = torch.Generator().manual_seed(12)
     every = torch.arange(65536, dtype=torch.int32).to(torch.uint16).view(torch.bfloat16).float()
     every = every[(every.abs() >= 2.0 ** -20) & (every.abs() <= 85)]
     size = torch.exp2(26.4 * torch.rand(1 << 17, generator=g) - 20)
-    return torch.cat([every, size * (1 - 2 * torch.randint(0, 2, size.shape, generator=g))])
+    far = -85 - 3.7 * torch.rand(1 << 13, generator=g)
+    return torch.cat([every, size * (1 - 2 * torch.randint(0, 2, size.shape, generator=g)), far])
 
 
 def test_silu_to_the_last_bit():
