@@ -57,7 +57,7 @@ __device__ __forceinline__ u32x4 load_u128(const uint8_t* p) {
 // MFMA q = 0, 1 of a step takes piece 4 q + g in lane group g, so that a load of token
 // rows covers 64 bytes of each.  kSets steps are on the way at a time (all that a wave
 // has, up to K = 8192); one after the other in the same registers, the compiler waits
-// for all of them at each use.  1 x 4096 x 7168 4.9 us, 1 x 36864 x 7168 25.4, 5.5 TB/s.
+// for all of them at each use.  1 x 4096 x 7168 5.1 us, 1 x 36864 x 7168 25.9, 5.4 TB/s.
 //
 // Rows and columns past the end read the last ones, unstored.  The last step, if
 // it ends inside, is the last wave's besides: pieces past the end are zeros under 1.
@@ -174,10 +174,16 @@ void mx_gemm_rows_kernel(MxGemm p) {
 // that a lane needs lie in one word: of the 16 codes of a row, g, 4 + g, 8 + g and
 // 12 + g; a lane's rows of its wave's tiles lie side by side.
 //
-// Large products are bound by the matrix unit's power: 8192 x 4096 x 7168 takes 113 to
-// 121 us from card to card, 4.3 to 4.0 PFLOP/s, and 93 with codes that are all zero (the
-// clock falls below 2 GHz).  Smaller ones are bound by the chain of a stage, a wait, a
-// meeting and the reads behind it (0.2 to 0.5 us): 512 rows 15.5 us, 256 rows 11.7.
+// 8192 x 4096 x 7168 takes 113 to 121 us from card to card, 4.3 to 4.0 PFLOP/s.  The matrix
+// unit is busy in 55 % of the kernel's cycles, at 1.84 GHz: its power costs a fifth (92 us
+// with codes that are all zero), the larger part goes to the start and end of a block that
+// has its CU alone, to the meeting at which both stages' loads have arrived (28 % of the
+// waves' cycles are spent waiting) and to reads from LDS (15 % of its cycles are
+// conflicts).  The bf16 form keeps four registers of the way out's addresses in scratch,
+// stored ahead of the stages and loaded behind them (with addresses made behind the stages
+// six others go there, within them).  Smaller products are bound by the chain of a stage,
+// a wait, a meeting and the reads behind it (0.2 to 0.5 us): in a captured graph 512 rows
+// 16.2 us, 256 rows 12.0.
 // Measured and not better: 32 x 32 x 64 MFMAs (the unit is 5 % slower with them), waves
 // of 8 x 8 tiles (2 % faster at K 7168, 7 to 11 % slower at 2048 and in 4096 rows),
 // stages of 128 or 512 values, operands read two halves ahead, columns of MFMAs taken
@@ -431,8 +437,8 @@ hipError_t launch_rows(const MxGemm& p, hipStream_t s) {
 // per stage (256 values of K) while each CU has at most one block, and with 256 blocks of
 // as many as a CU holds.  The rows kernel: a start, and in proportion to the blocks from
 // one a CU on a block's own time and its waves' steps, by token rows.  Fitted to 420 shapes, from
-// 1 x 64 x 128 to 8192 x 4096 x 7168 and 64 x 131072 x 7168: the choice by them is 1.1 %
-// slower than the best kernel of each shape on average, 7 % or more for one in 20, 26 % at
+// 1 x 64 x 128 to 8192 x 4096 x 7168 and 64 x 131072 x 7168: the choice by them is 1.3 %
+// slower than the best kernel of each shape on average, 7 % or more for one in 14, 25 % at
 // most (fitted to half of them: 1.9 % on the others).  The two of 128 x 128 differ by
 // their waves, 4 and 8 (1024 x 4096 x 7168 25.2 and 22.0); 16 x 32 takes 16 x 8192 x
 // 16384 in 17.6 (32 x 64 20.3, rows 21.4).
