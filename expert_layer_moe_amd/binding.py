@@ -525,9 +525,10 @@ def moe_silu_mul_quant_fp8(gu, codes=None, scales=None, stream=None):
 # ---- 4-bit microscaled floats ---------------------------------------------------
 # (Results that a call of these or of the norm allocates lie in one allocation if they
 # take up to 1 MB together, which is free when the last of them is: each is a tensor of its
-# own that may be kept, resized or used on other streams, but a file of one holds the bytes
-# ahead of it too, and one that torch hands to another process keeps the allocation for
-# good.  A call with a `stream` allocates each by itself.)
+# own that may be kept, resized or used on other streams.  But a file of one holds the bytes
+# ahead of it too, torch.save takes several of different types only as clones (their
+# storages begin at one address), and one that torch hands to another process keeps the
+# allocation for good.  A call with a `stream` allocates each by itself.)
 def moe_quant_mxfp4(x, codes=None, scales=None, stream=None):
     """Token or weight rows x [M, K] (bf16 or fp32; rows may be strided; K a
     multiple of 32) -> e2m1 codes [M, K/2] (uint8, two to a byte, the first in
